@@ -12,6 +12,11 @@ Gradients flow to q, k, v, u, g, b, a, h, conv_w and S_init (fp32), for the
 upstream gradients of o and S_final (either may be unused).  The carried
 convolution history of prism_fwd_resume is not taken: the backward entry point
 differentiates sequences that start with a zero history.
+
+The norms around the operator, differentiable in every tensor they take:
+
+    n, r = norm_residual(x, w, y=None, scale=None, eps=1e-6)
+    y = norm_gate(o, z, w, eps=1e-6, gate="silu")
 """
 from __future__ import annotations
 
@@ -72,3 +77,64 @@ class PrismFunction(torch.autograd.Function):
 def prism(q, k, v, u, g, b, a, h, conv_w, cu_seqlens, L: int, S_init=None, residual="linear"):
     """Differentiable forward pass: returns (o, S_final)."""
     return PrismFunction.apply(q, k, v, u, g, b, a, h, conv_w, cu_seqlens, L, S_init, residual)
+
+
+def _upstream(grad, like):
+    """An upstream gradient as the kernels take it, or None."""
+    return None if grad is None else grad.to(like.dtype).contiguous()
+
+
+class NormResidualFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, y, scale, eps):
+        ctx.set_materialize_grads(False)
+        n, r = binding.norm_residual(x, w, y=y, scale=scale, eps=eps)
+        ctx.save_for_backward(r, w, y if scale is not None else None, scale)
+        ctx.eps, ctx.has_y = eps, y is not None
+        if y is None:                        # r is x itself: only n is an output of this step
+            return n
+        return n, r
+
+    @staticmethod
+    def backward(ctx, dn, dr=None):
+        r, w, y, scale = ctx.saved_tensors
+        if dn is None and dr is None:
+            return None, None, None, None, None
+        dn = torch.zeros_like(r) if dn is None else _upstream(dn, r)
+        grads = binding.norm_residual_bwd(r, w, dn, dr=_upstream(dr, r), y=y, scale=scale, eps=ctx.eps,
+                                          want_dscale=ctx.needs_input_grad[3])
+        want = ctx.needs_input_grad
+        dy = (grads["x"] if scale is None else grads["y"]) if ctx.has_y and want[2] else None
+        return (grads["x"] if want[0] else None, grads["w"].to(w.dtype) if want[1] else None, dy,
+                grads["scale"].to(scale.dtype) if want[3] else None, None)
+
+
+def norm_residual(x, w, y=None, scale=None, eps: float = 1e-6):
+    """Differentiable binding.norm_residual: returns (n, r)."""
+    if y is None:
+        if scale is not None:
+            raise ValueError("scale without y")
+        return NormResidualFunction.apply(x, w, None, None, eps), x
+    return NormResidualFunction.apply(x, w, y, scale, eps)
+
+
+class NormGateFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, o, z, w, eps, gate):
+        y = binding.norm_gate(o, z, w, eps=eps, gate=gate)
+        ctx.save_for_backward(o, z, w)
+        ctx.eps, ctx.gate = eps, gate
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        o, z, w = ctx.saved_tensors
+        grads = binding.norm_gate_bwd(o, z, w, _upstream(dy, o), eps=ctx.eps, gate=ctx.gate)
+        want = ctx.needs_input_grad
+        return (grads["o"] if want[0] else None, grads["z"] if want[1] else None,
+                grads["w"].to(w.dtype) if want[2] else None, None, None)
+
+
+def norm_gate(o, z, w, eps: float = 1e-6, gate: str = "silu"):
+    """Differentiable binding.norm_gate: returns y."""
+    return NormGateFunction.apply(o, z, w, eps, gate)

@@ -158,4 +158,86 @@ bool scan_bf16_supported(int dk, int dv, int dv_slice);
 // a device counter on the current device; reset sets it back to zero).
 hipError_t read_wait_giveups(unsigned int* count, bool reset);
 
+// Residual add with a per-channel scale and RMS norm (norm_residual.hip):
+// r = x + scale * y, n = r rstd w; and its gradients.  y and scale may be null
+// (no add / a scale of one); r may be null when y is.
+struct NormResidualArgs {
+    bool bf16;
+    int64_t rows;
+    int width;                      // 1..kNormMaxWidth
+    float eps;
+    const void *x, *y, *scale, *w;
+    void *r, *n;                    // r: out of the forward, in of the backward
+    // backward: dr may be null (zero), dy may be null (not written), dscale may
+    // be null (then y is not read)
+    const void *dn, *dr;
+    void *dx, *dy;
+    float *dw, *dscale;
+    float* ws;                      // norm_residual_bwd_blocks() partial rows of dw (and dscale)
+};
+constexpr int kNormMaxWidth = 8192, kNormGateMaxWidth = 1024;
+constexpr int kNormBwdBlocks = 1024;             // workgroups of a backward, at most
+int norm_residual_bwd_blocks(int64_t rows, int width);
+hipError_t launch_norm_residual(const NormResidualArgs& p, hipStream_t stream);
+hipError_t launch_norm_residual_bwd(const NormResidualArgs& p, hipStream_t stream);
+
+// RMS norm of every head's row, weighted and gated (norm_gate.hip): y = o rstd w
+// act(z); and its gradients.  Rows are [tokens][heads]; w [heads][width] (heads =
+// 1 where all rows share one weight).
+struct NormGateArgs {
+    bool bf16;
+    int gate;                       // prism_gate
+    int64_t tokens;
+    int heads, width;               // width 1..kNormGateMaxWidth
+    float eps;
+    const void *o, *z, *w;
+    void* y;
+    const void* dy;
+    void *d_o, *dz;
+    float* dw;
+    float* ws;                      // norm_gate_bwd_blocks() partials of dw [heads][width]
+};
+int norm_gate_bwd_blocks(int64_t tokens, int heads);
+hipError_t launch_norm_gate(const NormGateArgs& p, hipStream_t stream);
+hipError_t launch_norm_gate_bwd(const NormGateArgs& p, hipStream_t stream);
+
+// Drafted tokens (draft.hip).  launch_draft: o, kw and p of every packed token
+// from the carried state and history, which are only read.  launch_commit: the
+// state and history moved by the first n_accept tokens of each sequence, from
+// the records kw and p (S_out and k_hist_out may be S and k_hist).
+struct DraftArgs {
+    bool bf16;
+    int n_seqs, heads, dk, dv;
+    const void *k, *v, *g, *b;
+    const int32_t* cu_seqlens;
+    const float* S;                 // [n_seqs, H, dk, dv]
+    const void* k_hist;             // [n_seqs, H, 3, dk]
+    float *kw, *p;                  // fp32 [T, H, dk], [T, H, dv]: out of the draft, in of the commit
+    // draft
+    int L = 1;
+    bool gelu = false;
+    const void *q = nullptr, *u = nullptr, *a = nullptr, *h = nullptr, *conv_w = nullptr;
+    void* o = nullptr;
+    // commit
+    const int32_t* n_accept = nullptr;
+    float* S_out = nullptr;
+    void* k_hist_out = nullptr;
+};
+hipError_t launch_draft(const DraftArgs& p, hipStream_t stream);
+hipError_t launch_commit(const DraftArgs& p, hipStream_t stream);
+
+// Verification of drafted tokens (verify.hip).
+struct VerifyArgs {
+    bool bf16;
+    int n_seqs, total_tokens, vocab;
+    const void *p, *q;              // [T, vocab] target and draft (or null) probabilities
+    const int32_t *tokens, *cu_seqlens;
+    const float *u_accept, *u_sample;
+    int32_t *n_accept, *next_token;
+    void* ws;                       // verify_workspace_bytes()
+};
+int verify_chunks(int vocab);
+size_t verify_workspace_bytes(int n_seqs, int vocab);
+hipError_t launch_verify(const VerifyArgs& p, hipStream_t stream);
+
 }  // namespace prism

@@ -1,0 +1,187 @@
+// norm_gate.hip -- what follows the memory-writing operator in a layer: every
+// head's output row o (width elements) is normalised, weighted and multiplied
+// by its gate z,
+//   y = o rstd w act(z),   rstd = 1 / sqrt(mean(o^2) + eps),
+// act = silu or sigmoid, and the gradients: with oh = o rstd, e = dy act(z) w,
+//   do = rstd (e - oh mean(e oh)),   dz = dy oh w act'(z),   dw = sum dy act(z) oh.
+// w is one row for all heads, or one a head; dw is summed accordingly.
+//
+// Bound by HBM (3 streams forward, 5 backward, up to 26 operations an
+// element).  A head's row is a few hundred bytes, held by 8 to 64 lanes, so a
+// wavefront works on several rows at once and the row sums stay within it.
+// With a weight a head a workgroup keeps to one head (w and the column sums
+// stay in its registers); its rows are then H rows apart, each of them at least
+// a whole 64-byte segment at the operator's widths.  Outputs may be the inputs' own buffers.
+#include "common.h"
+#include "kernels.h"
+#include "norm_rows.h"
+
+namespace prism {
+
+using rows::group_sum;
+
+// act(z), and with GRAD act'(z): s = 1 / (1 + e^-z); silu = z s, silu' = s (1 + z (1 - s))
+template <int GATE> __device__ __forceinline__ float gate_act(float z, float& slope)
+{
+    const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
+    if (GATE == 0) {
+        slope = s * (1.f + z * (1.f - s));
+        return z * s;
+    }
+    slope = s * (1.f - s);
+    return s;
+}
+
+template <typename S, int GATE>
+__global__ __launch_bounds__(S::THREADS) void norm_gate_kernel(
+    const typename S::elem* o, const typename S::elem* z, const typename S::elem* w, float eps,
+    int64_t tokens, int heads, int width, typename S::elem* y)
+{
+    __shared__ float red[2 * S::THREADS / 64];
+    const int lane = threadIdx.x % S::LANES, group = threadIdx.x / S::LANES;
+    const int e = blockIdx.x % heads, tb = blockIdx.x / heads, nt = gridDim.x / heads;
+    float wv[S::E];
+    S::load_f32(w + (int64_t)e * width, lane, width, wv);
+    const float inv = 1.f / (float)width;
+    int phase = 0;
+    for (int64_t t = (int64_t)tb * S::GROUPS + group; t < tokens; t += (int64_t)nt * S::GROUPS) {
+        const int64_t at = (t * heads + e) * width;
+        typename S::Raw orr, zr;
+        S::load(o + at, lane, width, orr);
+        S::load(z + at, lane, width, zr);
+        float ov[S::E], zv[S::E];
+        S::unpack(orr, ov);
+        S::unpack(zr, zv);
+        float ss[1] = {0.f};
+#pragma unroll
+        for (int c = 0; c < S::E; ++c)
+            ss[0] += ov[c] * ov[c];
+        group_sum<S::LANES>(ss, red, phase);
+        phase ^= 1;
+        const float rstd = rsqrtf(ss[0] * inv + eps);
+#pragma unroll
+        for (int c = 0; c < S::E; ++c) {
+            float slope;
+            ov[c] = ov[c] * rstd * wv[c] * gate_act<GATE>(zv[c], slope);
+        }
+        S::store(y + at, lane, width, ov);
+    }
+}
+
+template <typename S, int GATE>
+__global__ __launch_bounds__(S::THREADS) void norm_gate_bwd_kernel(
+    const typename S::elem* o, const typename S::elem* z, const typename S::elem* w, float eps,
+    const typename S::elem* dy, int64_t tokens, int heads, int width, typename S::elem* d_o,
+    typename S::elem* dz, float* part)
+{
+    __shared__ float red[2 * 2 * S::THREADS / 64];
+    extern __shared__ float buf[];
+    const int lane = threadIdx.x % S::LANES, group = threadIdx.x / S::LANES;
+    const int e = blockIdx.x % heads, tb = blockIdx.x / heads, nt = gridDim.x / heads;
+    float wv[S::E], aw[S::E];
+    S::load_f32(w + (int64_t)e * width, lane, width, wv);
+#pragma unroll
+    for (int c = 0; c < S::E; ++c)
+        aw[c] = 0.f;
+    const float inv = 1.f / (float)width;
+    int phase = 0;
+    for (int64_t t = (int64_t)tb * S::GROUPS + group; t < tokens; t += (int64_t)nt * S::GROUPS) {
+        const int64_t at = (t * heads + e) * width;
+        typename S::Raw orr, zr, dyr;
+        S::load(o + at, lane, width, orr);
+        S::load(z + at, lane, width, zr);
+        S::load(dy + at, lane, width, dyr);
+        float ov[S::E], zv[S::E], dv[S::E];
+        S::unpack(orr, ov);
+        S::unpack(zr, zv);
+        S::unpack(dyr, dv);
+        float ss[2] = {0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < S::E; ++c) {
+            float slope;
+            const float act = gate_act<GATE>(zv[c], slope);
+            zv[c] = dv[c] * wv[c] * slope * ov[c];       // dz, but for rstd
+            dv[c] *= act;                                // dy act(z)
+            ss[0] += ov[c] * ov[c];
+            ss[1] += dv[c] * wv[c] * ov[c];
+        }
+        group_sum<S::LANES>(ss, red, phase);
+        phase ^= 1;
+        const float rstd = rsqrtf(ss[0] * inv + eps);
+        const float mean = ss[1] * inv * rstd;           // mean(e oh)
+#pragma unroll
+        for (int c = 0; c < S::E; ++c) {
+            const float oh = ov[c] * rstd;
+            aw[c] += dv[c] * oh;
+            ov[c] = rstd * (dv[c] * wv[c] - oh * mean);
+            zv[c] *= rstd;
+        }
+        S::store(d_o + at, lane, width, ov);
+        S::store(dz + at, lane, width, zv);
+    }
+    rows::store_partial<S>(aw, buf, lane, group, width, part + ((int64_t)tb * heads + e) * width);
+}
+
+int norm_gate_bwd_blocks(int64_t tokens, int heads)
+{
+    const int64_t cap = heads < kNormBwdBlocks ? kNormBwdBlocks / heads : 1;
+    return (int)(tokens < 1 ? 1 : tokens < cap ? tokens : cap);
+}
+
+template <typename T, int GATE> static hipError_t launch_fwd(const NormGateArgs& p, hipStream_t stream)
+{
+    if (p.tokens == 0)
+        return hipSuccess;
+    return rows::with_shape<T>(p.width, [&](auto shape) -> hipError_t {
+        typedef decltype(shape) S;
+        if constexpr (S::LANES <= 64) {                  // width <= kNormGateMaxWidth
+            const int64_t want = (p.tokens + S::GROUPS - 1) / S::GROUPS;
+            const int64_t cap = p.heads < 2048 ? 2048 / p.heads : 1;
+            const int64_t nt = want < cap ? want : cap;
+            hipLaunchKernelGGL((norm_gate_kernel<S, GATE>), dim3((unsigned)(nt * p.heads)), dim3(S::THREADS), 0,
+                               stream, (const T*)p.o, (const T*)p.z, (const T*)p.w, p.eps, p.tokens, p.heads,
+                               p.width, (T*)p.y);
+            return hipGetLastError();
+        }
+        return hipErrorInvalidValue;
+    });
+}
+
+template <typename T, int GATE> static hipError_t launch_bwd_t(const NormGateArgs& p, hipStream_t stream)
+{
+    const int nt = norm_gate_bwd_blocks(p.tokens, p.heads);
+    const hipError_t e = rows::with_shape<T>(p.width, [&](auto shape) -> hipError_t {
+        typedef decltype(shape) S;
+        if constexpr (S::LANES <= 64) {
+            hipLaunchKernelGGL((norm_gate_bwd_kernel<S, GATE>), dim3((unsigned)nt * p.heads), dim3(S::THREADS),
+                               S::PARTIAL_LDS, stream, (const T*)p.o, (const T*)p.z,
+                               (const T*)p.w, p.eps, (const T*)p.dy, p.tokens, p.heads, p.width, (T*)p.d_o,
+                               (T*)p.dz, p.ws);
+            return hipGetLastError();
+        }
+        return hipErrorInvalidValue;
+    });
+    if (e != hipSuccess)
+        return e;
+    const int cols = p.heads * p.width;
+    return rows::launch_sum_partials(p.ws, nt, cols, cols, p.dw, nullptr, stream);
+}
+
+template <typename T> static hipError_t launch_T(const NormGateArgs& p, bool bwd, hipStream_t stream)
+{
+    if (bwd)
+        return p.gate == 0 ? launch_bwd_t<T, 0>(p, stream) : launch_bwd_t<T, 1>(p, stream);
+    return p.gate == 0 ? launch_fwd<T, 0>(p, stream) : launch_fwd<T, 1>(p, stream);
+}
+
+hipError_t launch_norm_gate(const NormGateArgs& p, hipStream_t stream)
+{
+    return p.bf16 ? launch_T<uint16_t>(p, false, stream) : launch_T<float>(p, false, stream);
+}
+
+hipError_t launch_norm_gate_bwd(const NormGateArgs& p, hipStream_t stream)
+{
+    return p.bf16 ? launch_T<uint16_t>(p, true, stream) : launch_T<float>(p, true, stream);
+}
+
+}  // namespace prism

@@ -5,6 +5,7 @@
 #include <stdlib.h>
 
 #include "prism.h"
+#include "api_checks.h"
 #include "kernels.h"
 
 // Workspace of prism_fwd_noalloc: a file-scope device array, one copy per GPU
@@ -34,25 +35,6 @@ void* scratch_ptr()
         ptr[dev] = p;
     }
     return ptr[dev];
-}
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-bool dims_ok(const prism_dims* d)
-{
-    return d && d->n_seqs >= 1 && d->total_tokens >= 0 && d->heads >= 1 && d->dk >= 1 &&
-           d->dv >= 1 && (d->dtype == PRISM_F32 || d->dtype == PRISM_BF16);
-}
-
-size_t elem_bytes(const prism_dims* d) { return d->dtype == PRISM_BF16 ? 2 : 4; }
-
-// Pointer must be non-null and 16-byte aligned.
-bool ptr_ok(const void* p) { return p && aligned16(p); }
-
-// Per-token arrays may be NULL when there are no tokens at all.
-bool tok_ok(const prism_dims* d, const void* p)
-{
-    return d->total_tokens == 0 ? aligned16(p) : ptr_ok(p);
 }
 
 int env_int(const char* name, int fallback)
@@ -130,8 +112,6 @@ prism_status check_scan_shape(const prism_dims* d)
     return PRISM_EUNSUPPORTED;
 }
 
-prism_status from_hip(hipError_t e) { return e == hipSuccess ? PRISM_OK : PRISM_EHIP; }
-
 int device_cus()
 {
     int dev = 0, n = 0;
@@ -169,19 +149,12 @@ bool use_two_pass(const prism_dims* d)
            d->total_tokens > 0;
 }
 
-size_t round256(size_t n) { return (n + 255) / 256 * 256; }
-
 size_t kw_bytes(const prism_dims* d)
 {
     size_t n = (size_t)d->total_tokens * (size_t)d->heads * (size_t)d->dk * elem_bytes(d);
     n = (n + 255) / 256 * 256;
     return n < 256 ? 256 : n;
 }
-
-// Optional pointer: null, or 16-byte aligned.
-bool opt_ok(const void* p) { return aligned16(p); }
-
-bool residual_ok(int r) { return r == PRISM_RESIDUAL_LINEAR || r == PRISM_RESIDUAL_GELU; }
 
 prism_status prologue_impl(const prism_dims* d, const void* k, const void* u, const void* a,
                            const void* h, const void* b, const void* conv_w, const void* k_hist,

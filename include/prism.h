@@ -1,6 +1,6 @@
 /*
- * prism.h -- C ABI of libprism: the forward pass of PRISM's memory-writing
- * operator on AMD Instinct MI355X (gfx950).
+ * prism.h -- C ABI of libprism: PRISM's memory-writing operator on AMD Instinct
+ * MI355X (gfx950), and the steps of a layer around it.
  *
  * The operator (PRISM: Parallel Residual Iterative Sequence Model) keeps, per
  * (sequence, head), a state S in R^{dk x dv} that starts at zero (or at a
@@ -407,6 +407,188 @@ prism_status prism_bwd_ckpt(const prism_dims* d,
                             void* da, void* dh, float* dconv_w, float* dS_init,
                             const void* checkpoints, void* workspace, size_t workspace_bytes,
                             void* stream);
+
+/* ------------------------------------------------------------------------
+ * The layer around the operator: the norms before and after it, with their
+ * gradients, and the decoding of drafted tokens.  The pages describe the
+ * operator alone; these entry points are the steps that a layer made of it
+ * needs next to it.  The conventions above hold (dense row-major device
+ * pointers, 16-byte aligned, asynchronous, all checks before any launch).
+ * ------------------------------------------------------------------------ */
+
+typedef struct {
+    int64_t rows;          /* rows of the tensors, >= 0 and a multiple of heads */
+    int32_t heads;         /* rows of the weight: row i of the tensors takes row i % heads
+                              (1: one weight for all) */
+    int32_t width;         /* elements per row, >= 1 */
+    int32_t dtype;         /* prism_dtype of every float tensor but the fp32 gradients */
+} prism_norm_dims;
+
+/* Activation of the gate of prism_norm_gate: z / (1 + e^-z) or 1 / (1 + e^-z). */
+typedef enum { PRISM_GATE_SILU = 0, PRISM_GATE_SIGMOID = 1 } prism_gate;
+
+/* Bytes of device workspace prism_norm_residual_bwd and prism_norm_gate_bwd need
+ * (fp32 partial sums of the weights' gradients, one set per workgroup).  0 for
+ * invalid dims. */
+size_t prism_norm_workspace_bytes(const prism_norm_dims* d);
+
+/*
+ * The step between two blocks: the residual add of the block before, scaled per
+ * channel, and the RMS norm in front of the next one,
+ *   r = x + scale * y,    n = r / sqrt(mean(r^2) + eps) * w       (per row).
+ *
+ *   x         [rows, width]  residual stream
+ *   y         [rows, width]  the block's output, or NULL (r = x)
+ *   scale     [width]        per-channel residual scale, or NULL (one); needs y
+ *   w         [width]        weight of the norm
+ *   eps       >= 0, finite
+ *   r         out [rows, width]: the new residual stream; may be NULL when y is
+ *   n         out [rows, width]
+ * r and n are each rounded once, from fp32: n is formed from r before its
+ * rounding.  Either output may be the buffer of an input (x, y), not of the
+ * other output.  d->heads must be 1; width <= 8192, else PRISM_EUNSUPPORTED.
+ * Per-row arrays may be NULL when rows == 0.
+ */
+prism_status prism_norm_residual(const prism_norm_dims* d, const void* x, const void* y,
+                                 const void* scale, const void* w, float eps,
+                                 void* r, void* n, void* stream);
+
+/*
+ * Gradients of prism_norm_residual, from the r that it stored:
+ *   t = dL/dr of both uses of r;   dx = t, dy = scale * t, dscale = sum_rows t * y,
+ *   dw = sum_rows dn * r / sqrt(mean(r^2) + eps).
+ *
+ *   dn        [rows, width]  gradient of n
+ *   dr        [rows, width]  gradient that reaches r otherwise, or NULL (zero)
+ *   dx        out [rows, width]
+ *   dy        out [rows, width] or NULL (not written); without a scale it equals dx
+ *   dw        out fp32 [width]
+ *   dscale    out fp32 [width] or NULL (not formed, y is not read); needs scale and y
+ *   workspace prism_norm_workspace_bytes(d) bytes
+ * dx and dy may be the buffers of dn, dr, r or y, not of each other.  The column
+ * sums are added in a fixed order: the same call gives the same bits.
+ */
+prism_status prism_norm_residual_bwd(const prism_norm_dims* d, const void* r, const void* y,
+                                     const void* scale, const void* w, float eps,
+                                     const void* dn, const void* dr, void* dx, void* dy,
+                                     float* dw, float* dscale,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * What follows the operator: every head's output row is normalised, weighted and
+ * multiplied by its gate,
+ *   y = o / sqrt(mean(o^2) + eps) * w * act(z)       (per row of `width` elements).
+ *
+ *   o, z      [rows, width]   with rows = T * H for o [T, H, dv]
+ *   w         [heads, width]  heads = H: a weight a head; 1: one for all
+ *   gate      prism_gate
+ *   y         out [rows, width]; may be the buffer of o or z
+ * width <= 1024, else PRISM_EUNSUPPORTED.
+ */
+prism_status prism_norm_gate(const prism_norm_dims* d, const void* o, const void* z, const void* w,
+                             float eps, int gate, void* y, void* stream);
+
+/*
+ * Gradients of prism_norm_gate for the gradient dy [rows, width] of y: d_o, dz
+ * [rows, width], dw fp32 [heads, width].  d_o and dz may be the buffers of o, z
+ * or dy, not of each other.  workspace: prism_norm_workspace_bytes(d) bytes; the
+ * same call gives the same bits.
+ */
+prism_status prism_norm_gate_bwd(const prism_norm_dims* d, const void* o, const void* z,
+                                 const void* w, float eps, int gate, const void* dy,
+                                 void* d_o, void* dz, float* dw,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The operator over the drafted tokens of every sequence, from a carried state
+ * that stays as it is: what prism_fwd_resume computes from S and k_hist, but
+ * neither is moved, since it is not known yet how many of the tokens stay, and a
+ * recurrent state cannot be rolled back.  Sequence n brings the packed tokens
+ * cu_seqlens[n] .. cu_seqlens[n + 1] - 1 (in serving: the last token it has, then
+ * the drafted ones; none is fine).  Meant for a few tokens a sequence; any
+ * number is served, 16 at a time.
+ *
+ *   q .. conv_w, cu_seqlens, L, residual   as in prism_fwd_resume
+ *   S           fp32 [n_seqs, H, dk, dv]   state before the first token, read only
+ *   k_hist      [n_seqs, H, 3, dk]         history before it, read only
+ *   o           out [T, H, dv], input dtype
+ *   kw          out fp32 [T, H, dk]        the write keys, and
+ *   p           out fp32 [T, H, dv]        S_{t-1}^T k_t: what prism_decode_commit needs
+ *                                          to move the state by any number of the tokens
+ * The write key is kept in fp32 (as in prism_decode_step).  dk, dv in {64, 128},
+ * else PRISM_EUNSUPPORTED.  A token's outputs depend on the tokens up to it only,
+ * also where later ones hold infinities or NaN.  No workspace.
+ */
+prism_status prism_decode_draft(const prism_dims* d,
+                                const void* q, const void* k, const void* v,
+                                const void* u, const void* g, const void* b,
+                                const void* a, const void* h, const void* conv_w,
+                                const int32_t* cu_seqlens, int L, int residual,
+                                const float* S, const void* k_hist,
+                                void* o, float* kw, float* p, void* stream);
+
+/*
+ * The state and history of every sequence moved by the first n_accept[n] of its
+ * drafted tokens (0 .. its length; values outside are clamped to that), from
+ * the records of prism_decode_draft on the same k, v, g, b, S and k_hist:
+ *   S_t = g_t (S_{t-1} - b_t k_t p_t^T) + kw_t v_t^T.
+ *
+ *   k, v, g, b, cu_seqlens   as passed to prism_decode_draft
+ *   n_accept    int32 [n_seqs], device
+ *   kw, p       its records, read only
+ *   S, k_hist   the state and history it read
+ *   S_out       out fp32 [n_seqs, H, dk, dv]; may be S (in place)
+ *   k_hist_out  out [n_seqs, H, 3, dk]; may be k_hist
+ * A sequence that keeps no token keeps its state and history, bit for bit.
+ */
+prism_status prism_decode_commit(const prism_dims* d,
+                                 const void* k, const void* v, const void* g, const void* b,
+                                 const int32_t* cu_seqlens, const int32_t* n_accept,
+                                 const float* kw, const float* p,
+                                 const float* S, const void* k_hist,
+                                 float* S_out, void* k_hist_out, void* stream);
+
+typedef struct {
+    int32_t n_seqs;        /* >= 1 */
+    int32_t total_tokens;  /* T = cu_seqlens[n_seqs], >= 0 */
+    int32_t vocab;         /* >= 1 */
+    int32_t dtype;         /* prism_dtype of p and q */
+} prism_verify_dims;
+
+/* Bytes of device workspace prism_verify_draft needs; 0 for invalid dims. */
+size_t prism_verify_workspace_bytes(const prism_verify_dims* d);
+
+/*
+ * Which drafted tokens stay, and the token after them.  Sequence n fed the
+ * packed tokens c0 .. c1 - 1 (cu_seqlens): one that it already had, then the
+ * drafted ones.  Row t of p and q is the distribution of the token after token
+ * t, the target's and the draft model's.  A drafted token x at position t is kept
+ * while u_accept[t] * q[t-1][x] < p[t-1][x] and all before it were.  The next token
+ * is drawn with u_sample[n] from max(p - q, 0) of the row before the first token that
+ * is not kept, or from p of the last row: the smallest index whose cumulative
+ * weight exceeds u_sample times the total, among those with weight (the last
+ * such index if none does).
+ *
+ *   p           [T, vocab]
+ *   q           [T, vocab], or NULL: drafts without a distribution (q = 1 at the drafted
+ *               token; after a rejection the weights are p without that token)
+ *   tokens      int32 [T]      the fed tokens; one outside 0 .. vocab - 1 is not kept
+ *   u_accept    fp32 [T]       in [0, 1); the first of each sequence is not read
+ *   u_sample    fp32 [n_seqs]  in [0, 1)
+ *   n_accept    out int32 [n_seqs]: the fed tokens that stay, the first included (0 for
+ *               an empty sequence): the count prism_decode_commit takes
+ *   next_token  out int32 [n_seqs] (-1 for an empty sequence)
+ *   workspace   prism_verify_workspace_bytes(d) bytes
+ * p and q need not be normalised.  Weights that are not positive and finite (NaN
+ * too) count as none; a row of max(p - q, 0) without weight falls back to p, and a
+ * row of p without weight gives -1.  Products and sums are formed in 64 bits.
+ * vocab <= 2^28, else PRISM_EUNSUPPORTED.
+ */
+prism_status prism_verify_draft(const prism_verify_dims* d, const void* p, const void* q,
+                                const int32_t* tokens, const int32_t* cu_seqlens,
+                                const float* u_accept, const float* u_sample,
+                                int32_t* n_accept, int32_t* next_token,
+                                void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Diagnostic: the number of bounded in-kernel waits that gave up since the

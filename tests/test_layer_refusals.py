@@ -1,0 +1,187 @@
+"""Arguments that the layer operators refuse, before anything is launched: the C
+entry points' return codes and the binding's exceptions.  No GPU needed."""
+import ctypes
+
+import pytest
+
+torch = pytest.importorskip("torch")
+FAKE = 0x10000          # aligned, never dereferenced: every call below fails validation first
+
+
+@pytest.fixture(scope="module")
+def B():
+    from gated_delta_rule_prologue_amd import binding
+    binding.lib()
+    return binding
+
+
+def nd(B, rows=8, heads=1, width=64, dtype=1):
+    return ctypes.byref(B.NormDims(rows, heads, width, dtype))
+
+
+def test_norm_workspace_bytes(B):
+    """Per workgroup (one a row or token up to 1024 in all) an fp32 partial: dw and dscale
+    of width, or dw of heads rows."""
+    up = lambda x: (x + 255) // 256 * 256
+    b = lambda *a: B.norm_workspace_bytes(B.NormDims(*a))
+    assert b(8, 1, 64, 1) == up(2 * 8 * 64 * 4)
+    assert b(100000, 1, 768, 1) == up(2 * 1024 * 768 * 4)
+    assert b(0, 1, 64, 0) == up(2 * 64 * 4)
+    assert b(6000, 6, 128, 1) == up(2 * 1024 * 128 * 4)         # the residual norm's is larger
+    assert b(3 * 5000, 5000, 8, 1) == up(5000 * 8 * 4)
+    for bad in ((-1, 1, 64, 1), (8, 0, 64, 1), (8, 3, 64, 1), (8, 1, 0, 1), (8, 1, 64, 2),
+                (1 << 61, 1, 64, 1), (1 << 30, 1 << 30, 64, 1)):
+        assert b(*bad) == 0, bad
+
+
+def test_norm_residual_refuses(B):
+    f = B.lib().prism_norm_residual
+
+    def call(d=None, x=FAKE, y=FAKE, scale=FAKE, w=FAKE, eps=1e-6, r=FAKE, n=FAKE):
+        return f(d if d is not None else nd(B), x, y, scale, w, eps, r, n, None)
+
+    for kw in (dict(x=None), dict(x=FAKE + 2), dict(w=None), dict(n=None), dict(n=FAKE + 8),
+               dict(y=FAKE + 4), dict(scale=FAKE + 2), dict(r=FAKE + 8), dict(y=None),       # scale without y
+               dict(r=None),                                                                # y without r
+               dict(eps=-1e-6), dict(eps=float("nan")), dict(eps=float("inf"))):
+        assert call(**kw) == B.PRISM_EINVAL, kw
+    for d in (nd(B, rows=-1), nd(B, width=0), nd(B, dtype=3), nd(B, heads=2)):
+        assert call(d) == B.PRISM_EINVAL
+    assert f(None, *[FAKE] * 4, 1e-6, FAKE, FAKE, None) == B.PRISM_EINVAL
+    assert call(nd(B, width=8193)) == B.PRISM_EUNSUPPORTED
+
+
+def test_norm_residual_bwd_refuses(B):
+    f = B.lib().prism_norm_residual_bwd
+
+    def call(d=None, r=FAKE, y=FAKE, scale=FAKE, w=FAKE, eps=1e-6, dn=FAKE, dr=None, dx=FAKE, dy=FAKE,
+             dw=FAKE, ds=FAKE, ws=FAKE, nb=1 << 30):
+        return f(d if d is not None else nd(B), r, y, scale, w, eps, dn, dr, dx, dy, dw, ds, ws, nb, None)
+
+    for kw in (dict(r=None), dict(w=None), dict(dn=None), dict(dx=None), dict(dw=None), dict(ws=None),
+               dict(nb=16), dict(y=None), dict(scale=None), dict(dr=FAKE + 2), dict(dy=FAKE + 2),
+               dict(ds=FAKE + 4), dict(eps=-1.0)):
+        assert call(**kw) == B.PRISM_EINVAL, kw
+    assert call(nd(B, heads=2)) == B.PRISM_EINVAL
+    assert call(nd(B, width=9000)) == B.PRISM_EUNSUPPORTED
+
+
+def test_norm_gate_refuses(B):
+    fwd, bwd = B.lib().prism_norm_gate, B.lib().prism_norm_gate_bwd
+
+    def call(d=None, o=FAKE, z=FAKE, w=FAKE, eps=1e-6, gate=0, y=FAKE):
+        return fwd(d if d is not None else nd(B), o, z, w, eps, gate, y, None)
+
+    def grad(d=None, o=FAKE, z=FAKE, w=FAKE, eps=1e-6, gate=1, dy=FAKE, do=FAKE, dz=FAKE, dw=FAKE, ws=FAKE,
+             nb=1 << 30):
+        return bwd(d if d is not None else nd(B), o, z, w, eps, gate, dy, do, dz, dw, ws, nb, None)
+
+    for kw in (dict(o=None), dict(z=None), dict(w=None), dict(y=None), dict(z=FAKE + 2), dict(gate=2),
+               dict(gate=-1), dict(eps=-1.0)):
+        assert call(**kw) == B.PRISM_EINVAL, kw
+    for kw in (dict(o=None), dict(dy=None), dict(do=None), dict(dz=None), dict(dw=None), dict(ws=None),
+               dict(nb=16), dict(gate=2)):
+        assert grad(**kw) == B.PRISM_EINVAL, kw
+    for d in (nd(B, rows=7, heads=2), nd(B, heads=0), nd(B, width=0)):
+        assert call(d) == B.PRISM_EINVAL and grad(d) == B.PRISM_EINVAL
+    assert call(nd(B, width=1025)) == B.PRISM_EUNSUPPORTED
+    assert grad(nd(B, width=1025)) == B.PRISM_EUNSUPPORTED
+
+
+def test_decode_draft_refuses(B):
+    f = B.lib().prism_decode_draft
+    names = ["q", "k", "v", "u", "g", "b", "a", "h", "conv_w", "cu"]
+    outs = ["S", "hist", "o", "kw", "p"]
+
+    def call(d=None, L=3, residual=0, **over):
+        a = {n: FAKE for n in names + outs}
+        a.update(over)
+        return f(ctypes.byref(d or B.make_dims(4, 12, 2, 64, 64, 1)), *(a[n] for n in names), L, residual,
+                 *(a[n] for n in outs), None)
+
+    for n in names + outs:
+        assert call(**{n: None}) == B.PRISM_EINVAL, n
+        assert call(**{n: FAKE + 2}) == B.PRISM_EINVAL, n
+    for kw in (dict(L=0), dict(L=17), dict(residual=2), dict(residual=-1)):
+        assert call(**kw) == B.PRISM_EINVAL, kw
+    assert call(B.make_dims(0, 12, 2, 64, 64, 1)) == B.PRISM_EINVAL
+    assert call(B.make_dims(4, -1, 2, 64, 64, 1)) == B.PRISM_EINVAL
+    assert call(B.make_dims(4, 12, 2, 96, 64, 1)) == B.PRISM_EUNSUPPORTED
+    assert call(B.make_dims(4, 12, 2, 64, 256, 0)) == B.PRISM_EUNSUPPORTED
+    assert call(B.make_dims(1 << 20, 12, 1 << 20, 64, 64, 0)) == B.PRISM_EUNSUPPORTED
+    # no tokens: nothing to do, and nothing is launched
+    none = {n: None for n in ("q", "k", "v", "u", "g", "b", "a", "h", "o", "kw", "p")}
+    assert call(B.make_dims(4, 0, 2, 64, 64, 1), **none) == B.PRISM_OK
+
+
+def test_decode_commit_refuses(B):
+    f = B.lib().prism_decode_commit
+    names = ["k", "v", "g", "b", "cu", "n_accept", "kw", "p", "S", "hist", "S_out", "hist_out"]
+
+    def call(d=None, **over):
+        a = {n: FAKE for n in names}
+        a.update(over)
+        return f(ctypes.byref(d or B.make_dims(4, 12, 2, 64, 64, 1)), *(a[n] for n in names), None)
+
+    for n in names:
+        assert call(**{n: None}) == B.PRISM_EINVAL, n
+        assert call(**{n: FAKE + 4}) == B.PRISM_EINVAL, n
+    assert call(B.make_dims(4, 12, 2, 64, 32, 1)) == B.PRISM_EUNSUPPORTED
+    assert call(B.make_dims(4, 12, 0, 64, 64, 1)) == B.PRISM_EINVAL
+
+
+def test_verify_refuses(B):
+    f = B.lib().prism_verify_draft
+    names = ["p", "q", "tokens", "cu", "u_accept", "u_sample", "n_accept", "next", "ws"]
+
+    def call(d=(4, 12, 1000, 0), nb=1 << 30, **over):
+        a = {n: FAKE for n in names}
+        a.update(over)
+        return f(ctypes.byref(B.VerifyDims(*d)), *(a[n] for n in names), nb, None)
+
+    for n in names:
+        if n != "q":
+            assert call(**{n: None}) == B.PRISM_EINVAL, n
+        assert call(**{n: FAKE + 4}) == B.PRISM_EINVAL, n
+    assert call(nb=16) == B.PRISM_EINVAL
+    for d in ((0, 12, 1000, 0), (4, -1, 1000, 0), (4, 12, 0, 0), (4, 12, 1000, 2)):
+        assert call(d) == B.PRISM_EINVAL, d
+        assert B.verify_workspace_bytes(B.VerifyDims(*d)) == 0
+    assert call((1, 1, (1 << 28) + 1, 0)) == B.PRISM_EUNSUPPORTED
+    assert B.verify_workspace_bytes(B.VerifyDims(3, 9, 4097, 0)) == 256
+
+
+def test_binding_refuses_before_calling(B):
+    """What the binding refuses by itself: host tensors, and the arguments it looks at
+    before any address."""
+    bf = torch.bfloat16
+    x, w = torch.zeros(4, 64, dtype=bf), torch.zeros(64, dtype=bf)
+    with pytest.raises(ValueError, match="device"):
+        B.norm_residual(x, w)
+    with pytest.raises(ValueError, match="heads"):
+        B.norm_gate(torch.zeros(4, 3, 64, dtype=bf), torch.zeros(4, 3, 64, dtype=bf), torch.zeros(2, 64, dtype=bf))
+    with pytest.raises(ValueError, match="gate"):
+        B.norm_gate(x, x, w, gate="tanh")
+    with pytest.raises(ValueError, match="scale without y"):
+        B.norm_residual(x, w, scale=w)
+    with pytest.raises(ValueError, match="scale without y"):
+        B.norm_residual_bwd(x, w, x, scale=w)
+    with pytest.raises(ValueError, match="same buffer"):
+        B.norm_residual(x, w, y=x.clone(), r=(r := torch.zeros_like(x)), n=r)
+    with pytest.raises(TypeError, match="unsupported dtype"):
+        B.norm_residual(x.half(), w)
+    cu = torch.tensor([0, 4], dtype=torch.int32)
+    q, v = torch.zeros(4, 2, 64, dtype=bf), torch.zeros(4, 2, 128, dtype=bf)
+    th, cw = torch.zeros(4, 2, dtype=bf), torch.zeros(2, 64, 4, dtype=bf)
+    S, hist = torch.zeros(1, 2, 64, 128), torch.zeros(1, 2, 3, 64, dtype=bf)
+    with pytest.raises(ValueError, match="residual"):
+        B.decode_draft(q, q, v, None, th, th, None, None, cw, cu, 1, S, hist, residual="relu")
+    with pytest.raises(ValueError, match="L must"):
+        B.decode_draft(q, q, v, None, th, th, None, None, cw, cu, 17, S, hist)
+    with pytest.raises(ValueError, match="cu_seqlens"):
+        B.decode_commit(q, v, th, th, cu.long(), cu[:1], S, S, S, hist)
+    p = torch.zeros(4, 10)
+    with pytest.raises(ValueError, match="p must be"):
+        B.verify_draft(p[0], cu, cu, p[:, 0], p[0, :1])
+    with pytest.raises(ValueError, match="same buffer"):
+        B.verify_draft(p, cu, cu, p[:, 0], p[0, :1], n_accept=(m := torch.zeros(1, dtype=torch.int32)), next_token=m)
