@@ -15,9 +15,10 @@ with a residual choice), ``scan_wait_giveups`` -> prism_scan_wait_giveups.
 The layer around the operator: ``norm_residual`` / ``norm_residual_bwd`` ->
 prism_norm_residual(_bwd), ``norm_gate`` / ``norm_gate_bwd`` -> prism_norm_gate(_bwd),
 ``decode_draft`` -> prism_decode_draft, ``decode_commit`` -> prism_decode_commit,
-``verify_draft`` -> prism_verify_draft.  These run on the device of their tensors
-whichever is current, on ``stream`` or that device's current stream; what they
-allocate belongs to the stream they run on.
+``verify_draft`` -> prism_verify_draft.  These calls are checked and marshalled in C++
+(csrc/torch_calls.cpp) and run on the device of their tensors whichever is
+current, on ``stream`` or that device's current stream; what they allocate
+belongs to the stream they run on.
 """
 from __future__ import annotations
 
@@ -492,74 +493,35 @@ def scan_wait_giveups(reset: bool = True) -> int:
 
 # ---------------------------------------------------------------- the layer around the operator
 
-def _elsewhere(t: torch.Tensor, stream) -> bool:
-    """Whether a call has to leave the current device or stream for its tensors'."""
-    return stream is not None or (t.is_cuda and t.device.index != torch.cuda.current_device())
+_calls = None
 
 
-class _There:
-    """Makes a tensor's device current, and ``stream`` (a torch stream, or a raw
-    handle; None: the device's current one) its current stream."""
-
-    def __init__(self, t: torch.Tensor, stream):
-        if not t.is_cuda:
-            raise ValueError("libprism takes device tensors")
-        self.device = torch.cuda.device(t.device)
-        if stream is None:
-            stream = torch.cuda.current_stream(t.device)
-        elif not hasattr(stream, "cuda_stream"):
-            stream = (torch.cuda.ExternalStream(int(stream), device=t.device) if stream
-                      else torch.cuda.default_stream(t.device))
-        elif stream.device != t.device:
-            raise ValueError(f"stream of {stream.device} for tensors of {t.device}")
-        self.stream = torch.cuda.stream(stream)
-
-    def __enter__(self):
-        self.device.__enter__()
-        self.stream.__enter__()
-
-    def __exit__(self, *exc):
-        self.stream.__exit__(*exc)
-        self.device.__exit__(*exc)
+def _layer():
+    """The module that checks and marshals these calls (csrc/torch_calls.cpp)."""
+    global _calls
+    if _calls is None:
+        lib()
+        try:
+            from . import _calls as module
+        except ImportError as err:
+            raise RuntimeError("_calls.so is not built: run __graft_entry__.build() (or python -m "
+                               "gated_delta_rule_prologue_amd.build)") from err
+        module.set_error(PrismError)
+        _calls = module
+    return _calls
 
 
-def _arg(name: str, t: Optional[torch.Tensor], shape, dtype, like: torch.Tensor) -> int:
-    """Address of a tensor of exactly this shape and dtype, on ``like``'s device."""
-    if t is None:
-        raise ValueError(f"{name} is required")
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
-    return _ptr(t)
-
-
-def _opt_arg(name: str, t: Optional[torch.Tensor], shape, dtype, like: torch.Tensor):
-    return None if t is None else _arg(name, t, shape, dtype, like)
-
-
-def _scratch(need: int, workspace: Optional[torch.Tensor], like: torch.Tensor):
-    """(address, bytes) of a workspace, allocated on the current stream if none is given."""
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=like.device)
-    elif workspace.device != like.device:
-        raise ValueError(f"workspace is on {workspace.device}, not on {like.device}")
-    nbytes = workspace.numel() * workspace.element_size()
-    if nbytes < need:
-        raise ValueError(f"workspace needs {need} bytes")
-    return workspace, _ptr(workspace), nbytes
-
-
-def _apart(**outs):
-    """Outputs of one call must not share a buffer."""
-    seen = {}
-    for name, t in outs.items():
-        if t is not None and t.numel():
-            other = seen.setdefault(t.data_ptr(), name)
-            if other != name:
-                raise ValueError(f"{other} and {name} are the same buffer")
+def _on(t: torch.Tensor, stream):
+    """Context in which ``stream`` (a torch stream, or a raw handle) is the current stream of
+    ``t``'s device, so that what a call allocates belongs to it."""
+    if not t.is_cuda:
+        raise ValueError("libprism takes device tensors")
+    if not hasattr(stream, "cuda_stream"):
+        stream = (torch.cuda.ExternalStream(int(stream), device=t.device) if stream
+                  else torch.cuda.default_stream(t.device))
+    elif stream.device != t.device:
+        raise ValueError(f"stream of {stream.device} for tensors of {t.device}")
+    return torch.cuda.stream(stream)
 
 
 def norm_workspace_bytes(dims: NormDims) -> int:
@@ -570,11 +532,10 @@ def verify_workspace_bytes(dims: VerifyDims) -> int:
     return int(lib().prism_verify_workspace_bytes(ctypes.byref(dims)))
 
 
-def _rows_of(x: torch.Tensor) -> NormDims:
-    if x.dim() < 1 or x.shape[-1] < 1:
-        raise ValueError("rows of at least one element expected")
-    width = x.shape[-1]
-    return NormDims(x.numel() // width, 1, width, _dtype_code(x))
+def _choice(name: str, table: dict, value) -> int:
+    if value not in table:
+        raise ValueError(f"{name} must be one of {sorted(table)}")
+    return table[value]
 
 
 def norm_residual(x, w, y=None, scale=None, eps: float = 1e-6, r=None, n=None, stream=None):
@@ -582,95 +543,43 @@ def norm_residual(x, w, y=None, scale=None, eps: float = 1e-6, r=None, n=None, s
     last axis (prism_norm_residual): ``x``, ``y`` [..., width], ``w``, ``scale`` [width].
     ``y`` None: r is x itself; ``scale`` None: one.  Returns (n, r); ``r`` and ``n`` may be
     given, also as the buffers of x or y."""
-    if _elsewhere(x, stream):
-        with _There(x, stream):
+    if stream is not None:
+        with _on(x, stream):
             return norm_residual(x, w, y, scale, eps, r, n)
-    d, dt = _rows_of(x), x.dtype
-    vec = (d.width,)
-    if scale is not None and y is None:
-        raise ValueError("scale without y")
-    if n is None:
-        n = torch.empty_like(x)
-    if r is None:
-        r = torch.empty_like(x) if y is not None else None
-    _apart(r=r, n=n)
-    _check("prism_norm_residual", lib().prism_norm_residual(
-        ctypes.byref(d), _arg("x", x, x.shape, dt, x), _opt_arg("y", y, x.shape, dt, x),
-        _opt_arg("scale", scale, vec, dt, x), _arg("w", w, vec, dt, x), eps,
-        _opt_arg("r", r, x.shape, dt, x), _arg("n", n, x.shape, dt, x), _stream(None)))
-    return n, x if r is None else r
+    return _layer().norm_residual(x, w, y, scale, eps, r, n)
 
 
 def norm_residual_bwd(r, w, dn, dr=None, y=None, scale=None, eps: float = 1e-6, workspace=None,
                       want_dscale: bool = True, stream=None) -> dict:
     """Gradients of norm_residual from the r it returned (prism_norm_residual_bwd): ``dn`` of
     n, ``dr`` (optional) of r's other uses.  A dict of x and y [..., width] in the
-    input dtype, w and scale [width] in fp32; y is None without ``y`` and x itself
+    input dtype, w and scale [width] in fp32; y is None without ``y`` and x's tensor
     without ``scale``, scale is None without ``scale`` or with ``want_dscale`` false."""
-    if _elsewhere(r, stream):
-        with _There(r, stream):
+    if stream is not None:
+        with _on(r, stream):
             return norm_residual_bwd(r, w, dn, dr, y, scale, eps, workspace, want_dscale)
-    d, dt = _rows_of(r), r.dtype
-    vec, f32 = (d.width,), torch.float32
-    if scale is not None and y is None:
-        raise ValueError("scale without y")
-    dx = torch.empty_like(r)
-    dy = torch.empty_like(r) if scale is not None else None
-    dw = torch.empty(d.width, dtype=f32, device=r.device)
-    ds = torch.empty(d.width, dtype=f32, device=r.device) if scale is not None and want_dscale else None
-    workspace, wp, wn = _scratch(norm_workspace_bytes(d), workspace, r)
-    _check("prism_norm_residual_bwd", lib().prism_norm_residual_bwd(
-        ctypes.byref(d), _arg("r", r, r.shape, dt, r), _opt_arg("y", y, r.shape, dt, r),
-        _opt_arg("scale", scale, vec, dt, r), _arg("w", w, vec, dt, r), eps,
-        _arg("dn", dn, r.shape, dt, r), _opt_arg("dr", dr, r.shape, dt, r), _ptr(dx), _ptr(dy),
-        _ptr(dw), _ptr(ds), wp, wn, _stream(None)))
-    return {"x": dx, "y": dx if dy is None and y is not None else dy, "w": dw, "scale": ds}
-
-
-def _gate_dims(o: torch.Tensor, w: torch.Tensor, gate: str) -> NormDims:
-    if gate not in GATE:
-        raise ValueError(f"gate must be one of {sorted(GATE)}")
-    d = _rows_of(o)
-    if w.dim() == 2:                                     # a weight a head: o is [..., H, width]
-        if o.dim() < 2 or w.shape[0] != o.shape[-2]:
-            raise ValueError(f"w {tuple(w.shape)} needs {w.shape[0]} heads, o is {tuple(o.shape)}")
-        d.heads = max(1, w.shape[0])
-    return d
+    dx, dy, dw, ds = _layer().norm_residual_bwd(r, w, dn, dr, y, scale, eps, workspace, want_dscale)
+    return {"x": dx, "y": dy, "w": dw, "scale": ds}
 
 
 def norm_gate(o, z, w, eps: float = 1e-6, gate: str = "silu", y=None, stream=None) -> torch.Tensor:
     """y = o / sqrt(mean(o^2) + eps) * w * act(z) over the last axis (prism_norm_gate): ``o``,
     ``z`` [..., H, width], ``w`` [H, width] or [width] (one for all heads), ``gate`` "silu"
     or "sigmoid".  ``y`` may be given, also as the buffer of o or z."""
-    if _elsewhere(o, stream):
-        with _There(o, stream):
+    if stream is not None:
+        with _on(o, stream):
             return norm_gate(o, z, w, eps, gate, y)
-    d, dt = _gate_dims(o, w, gate), o.dtype
-    if y is None:
-        y = torch.empty_like(o)
-    wshape = (d.heads, d.width) if w.dim() == 2 else (d.width,)
-    _check("prism_norm_gate", lib().prism_norm_gate(
-        ctypes.byref(d), _arg("o", o, o.shape, dt, o), _arg("z", z, o.shape, dt, o),
-        _arg("w", w, wshape, dt, o), eps, GATE[gate], _arg("y", y, o.shape, dt, o), _stream(None)))
-    return y
+    return _layer().norm_gate(o, z, w, eps, _choice("gate", GATE, gate), y)
 
 
 def norm_gate_bwd(o, z, w, dy, eps: float = 1e-6, gate: str = "silu", workspace=None,
                   stream=None) -> dict:
     """Gradients of norm_gate for the gradient ``dy`` of y (prism_norm_gate_bwd): a dict of o,
     z (input dtype) and w (fp32, w's shape)."""
-    if _elsewhere(o, stream):
-        with _There(o, stream):
+    if stream is not None:
+        with _on(o, stream):
             return norm_gate_bwd(o, z, w, dy, eps, gate, workspace)
-    d, dt = _gate_dims(o, w, gate), o.dtype
-    wshape = (d.heads, d.width) if w.dim() == 2 else (d.width,)
-    d_o, dz = torch.empty_like(o), torch.empty_like(o)
-    dw = torch.empty(wshape, dtype=torch.float32, device=o.device)
-    workspace, wp, wn = _scratch(norm_workspace_bytes(d), workspace, o)
-    _check("prism_norm_gate_bwd", lib().prism_norm_gate_bwd(
-        ctypes.byref(d), _arg("o", o, o.shape, dt, o), _arg("z", z, o.shape, dt, o),
-        _arg("w", w, wshape, dt, o), eps, GATE[gate], _arg("dy", dy, o.shape, dt, o), _ptr(d_o),
-        _ptr(dz), _ptr(dw), wp, wn, _stream(None)))
+    d_o, dz, dw = _layer().norm_gate_bwd(o, z, w, dy, eps, _choice("gate", GATE, gate), workspace)
     return {"o": d_o, "z": dz, "w": dw}
 
 
@@ -680,36 +589,14 @@ def decode_draft(q, k, v, u, g, b, a, h, conv_w, cu_seqlens, L: int, S, k_hist, 
     stays as it is (prism_decode_draft): tensors packed as in fwd_resume, ``S`` fp32 [N,
     H, dk, dv] and ``k_hist`` [N, H, 3, dk] read only.  Returns (o, kw, p): the outputs
     [T, H, dv] and the fp32 records [T, H, dk], [T, H, dv] for decode_commit."""
-    if _elsewhere(q, stream):
-        with _There(q, stream):
+    if stream is not None:
+        with _on(q, stream):
             return decode_draft(q, k, v, u, g, b, a, h, conv_w, cu_seqlens, L, S, k_hist, o, kw, p,
                                 residual)
-    if residual not in RESIDUAL:
-        raise ValueError(f"residual must be one of {sorted(RESIDUAL)}")
-    if v.dim() != 3:
-        raise ValueError("v must be [T, H, dv]")
     if not 1 <= L <= MAX_LEVELS:
         raise ValueError(f"L must be in 1..{MAX_LEVELS}")
-    d, dt, f32 = _dims_of(q, v, cu_seqlens), q.dtype, torch.float32
-    n, T, H, dk, dv = d.n_seqs, d.total_tokens, d.heads, d.dk, d.dv
-    tk, tv, th, lev = (T, H, dk), (T, H, dv), (T, H), (T, H, L - 1, dk)
-    if o is None:
-        o = torch.empty_like(v)
-    if kw is None:
-        kw = torch.empty(tk, dtype=f32, device=q.device)
-    if p is None:
-        p = torch.empty(tv, dtype=f32, device=q.device)
-    _apart(o=o, kw=kw, p=p)
-    up, ap, hp = ((_arg("u", u, lev, dt, q), _arg("a", a, lev, dt, q), _arg("h", h, lev, dt, q))
-                  if L > 1 else (None, None, None))
-    _check("prism_decode_draft", lib().prism_decode_draft(
-        ctypes.byref(d), _arg("q", q, tk, dt, q), _arg("k", k, tk, dt, q), _arg("v", v, tv, dt, q), up,
-        _arg("g", g, th, dt, q), _arg("b", b, th, dt, q), ap, hp,
-        _arg("conv_w", conv_w, (H, dk, 4), dt, q), _arg("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, q),
-        L, RESIDUAL[residual], _arg("S", S, (n, H, dk, dv), f32, q),
-        _arg("k_hist", k_hist, (n, H, 3, dk), dt, q), _arg("o", o, tv, dt, q), _arg("kw", kw, tk, f32, q),
-        _arg("p", p, tv, f32, q), _stream(None)))
-    return o, kw, p
+    return _layer().decode_draft(q, k, v, u, g, b, a, h, conv_w, cu_seqlens, L, S, k_hist, o, kw, p,
+                                 _choice("residual", RESIDUAL, residual))
 
 
 def decode_commit(k, v, g, b, cu_seqlens, n_accept, kw, p, S, k_hist, S_out=None, k_hist_out=None,
@@ -717,25 +604,10 @@ def decode_commit(k, v, g, b, cu_seqlens, n_accept, kw, p, S, k_hist, S_out=None
     """The state and history moved by the first ``n_accept`` (int32 [N], device) drafted tokens of
     every sequence, from decode_draft's records ``kw`` and ``p`` (prism_decode_commit).  In
     place unless ``S_out`` / ``k_hist_out`` are given.  Returns (S_out, k_hist_out)."""
-    if _elsewhere(k, stream):
-        with _There(k, stream):
+    if stream is not None:
+        with _on(k, stream):
             return decode_commit(k, v, g, b, cu_seqlens, n_accept, kw, p, S, k_hist, S_out, k_hist_out)
-    if v.dim() != 3:
-        raise ValueError("v must be [T, H, dv]")
-    d, dt, f32 = _dims_of(k, v, cu_seqlens), k.dtype, torch.float32
-    n, T, H, dk, dv = d.n_seqs, d.total_tokens, d.heads, d.dk, d.dv
-    S_out = S if S_out is None else S_out
-    k_hist_out = k_hist if k_hist_out is None else k_hist_out
-    state, hist = (n, H, dk, dv), (n, H, 3, dk)
-    _check("prism_decode_commit", lib().prism_decode_commit(
-        ctypes.byref(d), _arg("k", k, (T, H, dk), dt, k), _arg("v", v, (T, H, dv), dt, k),
-        _arg("g", g, (T, H), dt, k), _arg("b", b, (T, H), dt, k),
-        _arg("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, k),
-        _arg("n_accept", n_accept, (n,), torch.int32, k), _arg("kw", kw, (T, H, dk), f32, k),
-        _arg("p", p, (T, H, dv), f32, k), _arg("S", S, state, f32, k),
-        _arg("k_hist", k_hist, hist, dt, k), _arg("S_out", S_out, state, f32, k),
-        _arg("k_hist_out", k_hist_out, hist, dt, k), _stream(None)))
-    return S_out, k_hist_out
+    return _layer().decode_commit(k, v, g, b, cu_seqlens, n_accept, kw, p, S, k_hist, S_out, k_hist_out)
 
 
 def verify_draft(p, tokens, cu_seqlens, u_accept, u_sample, q=None, n_accept=None, next_token=None,
@@ -743,30 +615,12 @@ def verify_draft(p, tokens, cu_seqlens, u_accept, u_sample, q=None, n_accept=Non
     """Which drafted tokens stay, and the next token of every sequence (prism_verify_draft):
     ``p`` and ``q`` [T, vocab] (``q`` None: drafts without a distribution), ``tokens`` int32 [T],
     ``u_accept`` fp32 [T], ``u_sample`` fp32 [N].  Returns (n_accept, next_token), int32 [N]."""
-    if _elsewhere(p, stream):
-        with _There(p, stream):
+    if stream is not None:
+        with _on(p, stream):
             return verify_draft(p, tokens, cu_seqlens, u_accept, u_sample, q, n_accept, next_token,
                                 workspace)
-    if p.dim() != 2:
-        raise ValueError("p must be [T, vocab]")
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
-        raise ValueError("cu_seqlens must be int32 [n_seqs + 1] with n_seqs >= 1")
-    T, V = p.shape
-    n, i32, f32 = cu_seqlens.numel() - 1, torch.int32, torch.float32
-    d = VerifyDims(n, T, V, _dtype_code(p))
-    if n_accept is None:
-        n_accept = torch.empty(n, dtype=i32, device=p.device)
-    if next_token is None:
-        next_token = torch.empty(n, dtype=i32, device=p.device)
-    _apart(n_accept=n_accept, next_token=next_token)
-    workspace, wp, wn = _scratch(verify_workspace_bytes(d), workspace, p)
-    _check("prism_verify_draft", lib().prism_verify_draft(
-        ctypes.byref(d), _arg("p", p, (T, V), p.dtype, p), _opt_arg("q", q, (T, V), p.dtype, p),
-        _arg("tokens", tokens, (T,), i32, p), _arg("cu_seqlens", cu_seqlens, (n + 1,), i32, p),
-        _arg("u_accept", u_accept, (T,), f32, p), _arg("u_sample", u_sample, (n,), f32, p),
-        _arg("n_accept", n_accept, (n,), i32, p), _arg("next_token", next_token, (n,), i32, p), wp, wn,
-        _stream(None)))
-    return n_accept, next_token
+    return _layer().verify_draft(p, tokens, cu_seqlens, u_accept, u_sample, q, n_accept, next_token,
+                                 workspace)
 
 
 def to_device(inp, device="cuda") -> dict:

@@ -2,13 +2,16 @@
 
 Each source compiles to an object under ``_build/`` in parallel, then the
 objects link into ``gated_delta_rule_prologue_amd/libprism.so``.  The library
-exports only the C ABI of ``include/prism.h``.
+exports only the C ABI of ``include/prism.h``.  The Python calls of the layer
+operators (``csrc/torch_calls.cpp``) build into ``_calls.so`` beside it, a CPython
+module linked to it and to torch.
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 try:
@@ -22,6 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libprism.so")
+CALLS = os.path.join(PKG, "_calls.so")
 SOURCES = ["prism_api.hip", "prologue.hip", "prologue_bf16.hip", "prologue_f32.hip",
            "prologue_bf16_ext.hip", "prologue_f32_ext.hip", "chunk_scan.hip",
            "chunk_scan_bf16.hip", "decode.hip", "long_seq.hip", "backward.hip",
@@ -62,6 +66,22 @@ def _run(cmd, verbose):
         print(out, flush=True)
 
 
+def _calls_cmd(out: str, link: bool):
+    """Compile (or link) torch_calls.cpp: host code only."""
+    import torch
+    torch_dir = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD, "torch_calls.o")
+    if not link:
+        inc = [INCLUDE, os.path.join(torch_dir, "include"), sysconfig.get_paths()["include"],
+               os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include")]
+        abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+        return ["g++", "-O2", "-std=c++17", "-fPIC", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+                f"-D_GLIBCXX_USE_CXX11_ABI={abi}", *("-isystem" + d for d in inc), "-Wall", "-c",
+                os.path.join(CSRC, "torch_calls.cpp"), "-o", obj]
+    return ["g++", "-shared", obj, "-o", out, LIB, "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python",
+            "-ltorch_cpu", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
+
+
 def build(verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     hipcc = _hipcc()
@@ -71,6 +91,7 @@ def build(verbose: bool = False, extra_flags=()) -> str:
         obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
         objs.append(obj)
         cmds.append([hipcc, *HIPCC_FLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj])
+    cmds.append(_calls_cmd(CALLS, link=False))
     # device assembly of the MFMA kernels, for the machine-code check below
     asm = {src: os.path.join(BUILD, os.path.splitext(src)[0] + ".s") for src in CHECKED}
     for src, out in asm.items():
@@ -91,8 +112,12 @@ def build(verbose: bool = False, extra_flags=()) -> str:
             raise RuntimeError(f"{src}: a DPP source is read fewer than two wait states after "
                                f"its VALU write (see check_isa.py):\n{lines}")
     tmp = LIB + ".tmp%d" % os.getpid()
-    _run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp], verbose)
+    _run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-Wl,-soname,libprism.so", *objs,
+          "-o", tmp], verbose)
     os.replace(tmp, LIB)
+    tmp = CALLS + ".tmp%d" % os.getpid()
+    _run(_calls_cmd(tmp, link=True), verbose)
+    os.replace(tmp, CALLS)
     return LIB
 
 
