@@ -3,8 +3,8 @@
 // were kept (speculative decoding: a recurrent state cannot be rolled back, so
 // it is only moved once it is known how far).
 //
-// Per (sequence, head) chain and drafted tokens t = 0..M-1 (at most 16 at a
-// time; more are walked in blocks of 16), with S the carried state and
+// Per (sequence, head) chain and drafted tokens t = 0..M-1 (at most 8 at a
+// time; more are walked in blocks of 8), with S the carried state and
 //   kw_t = the write key of the operator (ShortConv anchor, residual chain),
 //   p_t  = S_{t-1}^T k_t,
 //   S_t  = g_t (S_{t-1} - b_t k_t p_t^T) + kw_t v_t^T,   o_t = S_t^T q_t:
@@ -16,6 +16,8 @@
 //   O         = diag(gamma_i) Q S - C P + E V
 //   A_ij = rho(i-1, j) g_j b_j <k_j, k_i>, B_ij = rho(i-1, j) <kw_j, k_i>   (j < i)
 //   C_ij = rho(i, j) g_j b_j <k_j, q_i>,   E_ij = rho(i, j) <kw_j, q_i>     (j <= i)
+// In one product, with T = (I + A)^-1 and the rows of K and Q stacked:
+//   [P; O] = W ([gamma K S; gamma Q S] + [B; E] V),   W = [[T, 0], [-C T, I]].
 // The products of gates are formed directly (never a quotient), so a gate of
 // exactly zero is served.  kw and p are left as records, in fp32, from which
 // the commit moves the state by m kept tokens without solving anything:
@@ -34,13 +36,18 @@
 // 16 R + 4 kq + r and the columns 2 j, 2 j + 1 of its wavefront, so a row of
 // the tile is read in 128-byte pieces.  That is the accumulator layout of a
 // 16x16 tile and, register r taken as one 16x16x4 step whose contraction index
-// kq names row 4 kq + r, the second operand's too: S enters K S and receives
-// K^T X with no exchange between lanes.  The first operand of step r then
-// wants channel 4 kq + r, so one 16-byte LDS read serves four steps.  The same
-// holds for P, which comes out of one product and enters the next.
-// Token t sits in tile row 4 (t % 4) + t / 4: step r of a contraction over
-// tokens covers tokens 4 r .. 4 r + 3, so steps beyond the last token are left
-// out.
+// kq names row 4 kq + r, the second operand's too: S enters [K; Q] S and receives
+// [K; KW]^T [X; Y] with no exchange between lanes.  The first operand of step r
+// then wants channel 4 kq + r, so one 16-byte LDS read serves four steps.  The
+// same holds for [P; O], which comes out of one product and enters the next.
+// Eight tokens fill a 16-row tile with K over Q, and one 16x16 product of
+// [K; Q] with [K; KW] gives the dot products of all four triangular matrices.
+// Token t sits in row 4 (t % 2) + t / 2 of its half: step r of a contraction over
+// tokens covers tokens 2 r and 2 r + 1, so steps beyond the last token are left out.
+// The write keys are formed by the whole workgroup (one thread per token and
+// four channels, every load of it issued before the state's and before the first
+// wait); after one barrier each wavefront forms the small matrices for itself
+// (16 to 32 matrix instructions) instead of waiting for another one's.
 #include "common.h"
 #include "kernels.h"
 
@@ -48,7 +55,7 @@ namespace prism {
 
 namespace {
 
-constexpr int kBlock = 16;                       // tokens per pass, at most
+constexpr int kBlock = 8;                        // tokens per pass, at most
 constexpr float kLarge = 1073741824.f;           // 2^30
 
 __device__ __forceinline__ f32x4_t mfma4(float a, float b, f32x4_t c)
@@ -56,44 +63,91 @@ __device__ __forceinline__ f32x4_t mfma4(float a, float b, f32x4_t c)
     return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
-// tile row of a token and back (its own inverse)
-__device__ __forceinline__ int slot_of(int t) { return 4 * (t & 3) + (t >> 2); }
-
-__device__ __forceinline__ float2 load2(const uint16_t* p)
-{
-    const uint32_t x = *reinterpret_cast<const uint32_t*>(p);
-    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
-}
-__device__ __forceinline__ float2 load2(const float* p) { return *reinterpret_cast<const float2*>(p); }
-__device__ __forceinline__ void store2(uint16_t* p, float a, float b)
-{
-    *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(a, b);
-}
-__device__ __forceinline__ void store2(float* p, float a, float b)
-{
-    *reinterpret_cast<float2*>(p) = make_float2(a, b);
-}
+// row of a token within its half of a tile, and back
+__device__ __forceinline__ int slot_of(int t) { return 4 * (t & 1) + (t >> 1); }
+__device__ __forceinline__ int token_of(int s) { return 2 * (s & 3) + (s >> 2); }
 
 typedef __attribute__((ext_vector_type(2))) float f32x2_t;
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2_t;
 
-// S += K^T X + KW^T Y of one block, with the rows of K and KW (fp32, [slot][LD]) in LDS; `steps` = ceil(tokens / 4)
-template <int RT, int LD>
-__device__ __forceinline__ void add_tokens(f32x4_t (&s)[RT][2], const float* sK, const float* sKW, int steps,
-                                           int kq, int j, const f32x4_t (&x)[2],
-                                           const f32x4_t (&y)[2])
+// Four elements of the storage type, raw and as fp32; two elements as fp32.
+template <typename T> struct Four;
+template <> struct Four<uint16_t> {
+    typedef u32x2_t raw;
+    __device__ static f32x4_t f32(raw x)
+    {
+        return {__uint_as_float(x[0] << 16), __uint_as_float(x[0] & 0xffff0000u), __uint_as_float(x[1] << 16),
+                __uint_as_float(x[1] & 0xffff0000u)};
+    }
+    __device__ static f32x2_t load2(const uint16_t* p)
+    {
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(p);
+        return {__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)};
+    }
+    __device__ static void store2(uint16_t* p, float a, float b)
+    {
+        *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(a, b);
+    }
+};
+template <> struct Four<float> {
+    typedef f32x4_t raw;
+    __device__ static f32x4_t f32(raw x) { return x; }
+    __device__ static f32x2_t load2(const float* p) { return *reinterpret_cast<const f32x2_t*>(p); }
+    __device__ static void store2(float* p, float a, float b) { *reinterpret_cast<f32x2_t*>(p) = f32x2_t{a, b}; }
+};
+template <typename T> __device__ __forceinline__ typename Four<T>::raw load4(const T* p)
 {
+    return *reinterpret_cast<const typename Four<T>::raw*>(p);
+}
+
+__device__ __forceinline__ bool tame4(f32x4_t x)
+{
+    return fabsf(x[0]) <= kLarge && fabsf(x[1]) <= kLarge && fabsf(x[2]) <= kLarge && fabsf(x[3]) <= kLarge;
+}
+
+__device__ __forceinline__ float lane_value(float x, int lane)
+{
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), lane));
+}
+
+// An element at a 32-bit byte offset a lane from a base that is the same for the
+// whole wavefront (which then stays in scalar registers).
+template <typename V, typename P> __device__ __forceinline__ const V* at_offset(const P* base, uint32_t bytes)
+{
+    return reinterpret_cast<const V*>(reinterpret_cast<const char*>(base) + bytes);
+}
+template <typename V, typename P> __device__ __forceinline__ V* at_offset(P* base, uint32_t bytes)
+{
+    return reinterpret_cast<V*>(reinterpret_cast<char*>(base) + bytes);
+}
+
+// Row 4 kq of S (uniform; the caller adds 16 R + r rows), columns col and col + 1:
+// nontemporal, since the state is read once and written once per step.
+template <int DV> __device__ __forceinline__ f32x2_t state_load(const float* S, int kq, int col)
+{
+    return __builtin_nontemporal_load(at_offset<f32x2_t>(S, (uint32_t)(4 * kq * DV + col) * 4));
+}
+
+// S <- gam S + [K; KW]^T [X; Y] for the rows of [K; KW] in LDS (fp32, 16 rows of
+// LD); xy is [X; Y] as a tile; `steps` = ceil(tokens / 2)
+template <int RT, int LD>
+__device__ __forceinline__ void add_tokens(f32x4_t (&s)[RT][2], float gam, const float* rows, int steps, int kq,
+                                           int j, const f32x4_t (&xy)[2])
+{
+#pragma unroll
+    for (int R = 0; R < RT; ++R)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            s[R][c] *= gam;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         if (r < steps) {
 #pragma unroll
             for (int R = 0; R < RT; ++R) {
-                const int at = (4 * kq + r) * LD + 16 * R + j;
-                const float ka = sK[at], kwa = sKW[at];
+                const float x = rows[(4 * kq + r) * LD + 16 * R + j];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    s[R][c] = mfma4(ka, x[c][r], s[R][c]);
-                    s[R][c] = mfma4(kwa, y[c][r], s[R][c]);
-                }
+                for (int c = 0; c < 2; ++c)
+                    s[R][c] = mfma4(x, xy[c][r], s[R][c]);
             }
         }
     }
@@ -101,20 +155,82 @@ __device__ __forceinline__ void add_tokens(f32x4_t (&s)[RT][2], const float* sK,
 
 }  // namespace
 
-template <typename T, int DK, int DV>
-__global__ __launch_bounds__(2 * DV) void draft_kernel(
+// The write key of one token in four channels, to kw_out (fp32).  LEV levels of u, a,
+// h are loaded at a time (LEV = 0: L = 1), every load issued before the first use.
+template <typename T, int DK, int LEV, bool GELU>
+__device__ __forceinline__ void form_write_key(const T* k, const T* u, const T* a, const T* h, const T* b,
+                                               const T* conv_w, const T* k_hist, int64_t chain, int64_t c0, int H,
+                                               int e, int L, int t, int ch, float* kw_out)
+{
+    using F = Four<T>;
+    using Raw = typename F::raw;
+    constexpr int LV = LEV > 0 ? LEV : 1;
+    const int64_t row = (c0 + t) * H + e, lev = row * (L - 1) * DK + ch;
+    Raw ar[LV], ur[LV], hr[LV], pr[3], wr[4];
+    auto fetch = [&](int l0) {                           // slots beyond the last re-read it
+#pragma unroll
+        for (int l = 0; l < LEV; ++l) {
+            const int sl = l0 + l < L - 2 ? l0 + l : L - 2, hl = sl < L - 3 ? sl : L > 2 ? L - 3 : 0;
+            ar[l] = __builtin_nontemporal_load(reinterpret_cast<const Raw*>(a + lev + (int64_t)sl * DK));
+            ur[l] = __builtin_nontemporal_load(reinterpret_cast<const Raw*>(u + lev + (int64_t)sl * DK));
+            hr[l] = __builtin_nontemporal_load(reinterpret_cast<const Raw*>(h + lev + (int64_t)hl * DK));
+        }
+    };
+    fetch(0);
+    const Raw kr = load4(k + row * DK + ch);
+#pragma unroll
+    for (int d = 1; d <= 3; ++d) {
+        const int pos = t - d;
+        pr[d - 1] = load4(pos >= 0 ? k + ((c0 + pos) * H + e) * DK + ch : k_hist + (chain * 3 + 3 + pos) * DK + ch);
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+        wr[x] = load4(conv_w + ((int64_t)e * DK + ch + x) * 4);
+    const float bt = to_f32(b[row]);
+
+    const f32x4_t kt = F::f32(kr), x1 = F::f32(pr[0]), x2 = F::f32(pr[1]), x3 = F::f32(pr[2]);
+    f32x4_t r, acc;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const f32x4_t w = F::f32(wr[x]);
+        r[x] = w[3] * kt[x] + w[2] * x1[x] + w[1] * x2[x] + w[0] * x3[x];
+        acc[x] = bt * kt[x];
+    }
+    for (int l0 = 0; LEV > 0 && l0 < L - 1; l0 += LV) {
+        if (l0 > 0)
+            fetch(l0);
+#pragma unroll
+        for (int l = 0; l < LEV; ++l) {
+            if (l0 + l < L - 1) {
+                const f32x4_t av = F::f32(ar[l]), uv = F::f32(ur[l]), hv = F::f32(hr[l]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    acc[x] += av[x] * r[x] * uv[x];
+                if (l0 + l < L - 2) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        r[x] = GELU ? r[x] - av[x] * gelu_as(hv[x] * r[x]) : r[x] * (1.f - av[x] * hv[x]);
+                }
+            }
+        }
+    }
+    *reinterpret_cast<f32x4_t*>(kw_out + row * DK + ch) = acc;
+}
+
+template <typename T, int DK, int DV, int LEV>
+__global__ __launch_bounds__(2 * DV, 2) void draft_kernel(
     const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ u,
     const T* __restrict__ a, const T* __restrict__ h, const T* __restrict__ g, const T* __restrict__ b,
     const T* __restrict__ conv_w, const int32_t* __restrict__ cu, int H, int L, bool gelu,
-    const float* __restrict__ S, const T* __restrict__ k_hist, T* __restrict__ o, float* __restrict__ kw_out,
+    const float* __restrict__ S, const T* __restrict__ k_hist, T* __restrict__ o, float* kw_out,
     float* __restrict__ p_out)
 {
-    constexpr int NTH = 2 * DV, W = NTH / 64, RT = DK / 16, LD = DK + 4;
-    constexpr int VE = Vec16<T>::N, CG = DK / VE;        // channels per access, accesses per row
-    __shared__ __align__(16) float sK[kBlock * LD], sQ[kBlock * LD], sKW[kBlock * LD];
-    __shared__ __align__(16) float sM[4][16][20];        // A (then its inverse), B, -C, E by tile row
-    __shared__ __align__(16) float sG[kBlock];
-    __shared__ float sB[kBlock], sRho[kBlock][kBlock + 1], sGam[kBlock + 1];
+    using F = Four<T>;
+    constexpr int NTH = 2 * DV, W = NTH / 64, RT = DK / 16, LD = DK + 4, CG = DK / 4;
+    constexpr int ITEMS = (kBlock * CG + NTH - 1) / NTH;         // pieces of the tile rows a thread stages
+    // rows 0..7 Q, 8..15 K, 16..23 KW: rows 8.. are [K; KW], row (i + 8) % 16 of [K; Q] is i
+    __shared__ __align__(16) float sRows[24 * LD];
+    __shared__ __align__(16) float sM[W][2][16][20];     // a wavefront's [A B; C E], then W
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, kq = lane >> 4, j = lane & 15;
     const int64_t chain = blockIdx.x;
@@ -124,261 +240,250 @@ __global__ __launch_bounds__(2 * DV) void draft_kernel(
     const int len = cu[n + 1] - (int)c0;
     if (len <= 0)
         return;
+    const int col = 32 * wave + 2 * j;
+    const uint32_t vrow = (uint32_t)H * DV;
 
-    f32x4_t s[RT][2];
-    const float* Sc = S + chain * DK * DV + 32 * wave + 2 * j;
+    if (gelu && LEV > 0) {
+        for (int i = tid; i < len * CG; i += NTH)
+            form_write_key<T, DK, LEV, true>(k, u, a, h, b, conv_w, k_hist, chain, c0, H, e, L, i / CG, (i % CG) * 4,
+                                             kw_out);
+    } else {
+        for (int i = tid; i < len * CG; i += NTH)
+            form_write_key<T, DK, LEV, false>(k, u, a, h, b, conv_w, k_hist, chain, c0, H, e, L, i / CG, (i % CG) * 4,
+                                              kw_out);
+    }
+    __syncthreads();                                     // the write keys of the chain are in kw_out
+
+    // a pass's rows of K, Q and KW on their way into LDS (zeros past its tokens)
+    typename F::raw kr[ITEMS], qr[ITEMS];
+    f32x4_t wr[ITEMS];
+    auto fetch_rows = [&](int base, int m) {
 #pragma unroll
-    for (int R = 0; R < RT; ++R)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const f32x2_t x = __builtin_nontemporal_load(
-                reinterpret_cast<const f32x2_t*>(Sc + (16 * R + 4 * kq + r) * DV));
-            s[R][0][r] = x[0];
-            s[R][1][r] = x[1];
+        for (int x = 0; x < ITEMS; ++x) {
+            const int i = tid + x * NTH, t = i / CG;
+            kr[x] = qr[x] = typename F::raw{};
+            wr[x] = f32x4_t{};
+            if (t < m) {
+                const int64_t at = ((c0 + base + t) * H + e) * DK + (i % CG) * 4;
+                kr[x] = load4(k + at);
+                qr[x] = load4(q + at);
+                wr[x] = *reinterpret_cast<const f32x4_t*>(kw_out + at);
+            }
         }
+    };
 
     // A token's zeros in the triangular matrices would turn an infinity or a NaN
     // of a later token into a NaN of its own, so a sequence with a value beyond
     // kLarge (whose products may overflow too) takes its tokens one at a time.
-    int cap = kBlock;
-    for (int base = 0; base < len;) {
-        const int m = len - base < cap ? len - base : cap;
-        const int steps = (m + 3) >> 2;
+    int cap = kBlock, base = 0, m = len < cap ? len : cap;
+    fetch_rows(0, m);
+    f32x2_t s[RT][4];                                    // as read: row 16 R + 4 kq + r, two columns
+#pragma unroll
+    for (int R = 0; R < RT; ++R)                         // behind the rows: in flight while those are worked on
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            s[R][r] = state_load<DV>(S + (chain * DK + 16 * R + r) * DV, kq, col);
+    for (;;) {
+        const int steps = (m + 1) >> 1;
         bool tame = true;
-        if (base > 0)
-            __syncthreads();                             // the block before is done with the LDS
-        if (tid < kBlock) {
-            const bool on = tid < m;
-            const int64_t at = (c0 + base + tid) * H + e;
-            const float gt = on ? to_f32(g[at]) : 1.f, bt = on ? to_f32(b[at]) : 0.f;
-            sG[tid] = gt;
-            sB[tid] = bt;
-            tame = fabsf(gt) <= kLarge && fabsf(bt) <= kLarge;
-        }
-        // write keys: one thread per (token, VE channels)
-        for (int i = tid; i < kBlock * CG; i += NTH) {
-            const int t = i / CG, ch = (i % CG) * VE, to = slot_of(t) * LD + ch;
-            float kt[VE], qt[VE], acc[VE];
 #pragma unroll
-            for (int x = 0; x < VE; ++x)
-                kt[x] = qt[x] = acc[x] = 0.f;
-            if (t < m) {
-                const int64_t row = (c0 + base + t) * H + e;
-                Vec16<T>::load(k + row * DK + ch, kt);
-                Vec16<T>::load(q + row * DK + ch, qt);
-                float past[3][VE], w[4 * VE];
-#pragma unroll
-                for (int d = 1; d <= 3; ++d) {
-                    const int pos = base + t - d;
-                    Vec16<T>::load(pos >= 0 ? k + (row - (int64_t)d * H) * DK + ch
-                                            : k_hist + (chain * 3 + 3 + pos) * DK + ch, past[d - 1]);
-                }
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    Vec16<T>::load(conv_w + ((int64_t)e * DK + ch) * 4 + x * VE, w + x * VE);
-                const float bt = to_f32(b[row]);
-                float r[VE];
-#pragma unroll
-                for (int x = 0; x < VE; ++x) {
-                    r[x] = w[4 * x + 3] * kt[x] + w[4 * x + 2] * past[0][x] + w[4 * x + 1] * past[1][x] +
-                           w[4 * x] * past[2][x];
-                    acc[x] = bt * kt[x];
-                }
-                const int64_t lev = row * (L - 1) * DK + ch;
-#pragma unroll 2
-                for (int l = 0; l < L - 1; ++l) {
-                    float av[VE], uv[VE], hv[VE];
-                    Vec16<T>::load(a + lev + (int64_t)l * DK, av);
-                    Vec16<T>::load(u + lev + (int64_t)l * DK, uv);
-                    const bool more = l < L - 2;
-                    if (more)
-                        Vec16<T>::load(h + lev + (int64_t)l * DK, hv);
-#pragma unroll
-                    for (int x = 0; x < VE; ++x) {
-                        acc[x] += av[x] * r[x] * uv[x];
-                        if (more)
-                            r[x] = gelu ? r[x] - av[x] * gelu_as(hv[x] * r[x]) : r[x] * (1.f - av[x] * hv[x]);
-                    }
-                }
-#pragma unroll
-                for (int x = 0; x < VE; x += 4)
-                    *reinterpret_cast<f32x4_t*>(kw_out + row * DK + ch + x) =
-                        f32x4_t{acc[x], acc[x + 1], acc[x + 2], acc[x + 3]};
+        for (int x = 0; x < ITEMS; ++x) {
+            const int i = tid + x * NTH, t = i / CG, to = slot_of(t) * LD + (i % CG) * 4;
+            if (kBlock * CG >= NTH || t < kBlock) {
+                const f32x4_t kt = F::f32(kr[x]);
+                *reinterpret_cast<f32x4_t*>(sRows + to) = F::f32(qr[x]);
+                *reinterpret_cast<f32x4_t*>(sRows + 8 * LD + to) = kt;
+                *reinterpret_cast<f32x4_t*>(sRows + 16 * LD + to) = wr[x];
+                tame = tame && tame4(kt) && tame4(wr[x]);
             }
-#pragma unroll
-            for (int x = 0; x < VE; x += 4) {
-                *reinterpret_cast<f32x4_t*>(sK + to + x) = f32x4_t{kt[x], kt[x + 1], kt[x + 2], kt[x + 3]};
-                *reinterpret_cast<f32x4_t*>(sQ + to + x) = f32x4_t{qt[x], qt[x + 1], qt[x + 2], qt[x + 3]};
-                *reinterpret_cast<f32x4_t*>(sKW + to + x) = f32x4_t{acc[x], acc[x + 1], acc[x + 2], acc[x + 3]};
-            }
-#pragma unroll
-            for (int x = 0; x < VE; ++x)
-                tame = tame && fabsf(kt[x]) <= kLarge && fabsf(acc[x]) <= kLarge;
         }
-        // value rows: register r holds token 4 r + kq, both columns
+        // gates: lane t holds token t's; then every lane has all of them
+        float gl = 1.f, bl = 0.f;
+        if ((lane & 7) < m) {
+            const int64_t at = (c0 + base + (lane & 7)) * H + e;
+            gl = to_f32(g[at]);
+            bl = to_f32(b[at]);
+            tame = tame && fabsf(gl) <= kLarge && fabsf(bl) <= kLarge;
+        }
+        // value rows: register r holds row 4 (kq % 2) + r, token 2 r + kq % 2, in both halves
         f32x4_t vv[2] = {};
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int t = 4 * r + kq;
+            const int t = 2 * r + (kq & 1);
             if (t < m) {
-                const float2 x = load2(v + ((c0 + base + t) * H + e) * DV + 32 * wave + 2 * j);
-                vv[0][r] = x.x;
-                vv[1][r] = x.y;
-                tame = tame && fabsf(x.x) <= kLarge && fabsf(x.y) <= kLarge;
+                const f32x2_t x = F::load2(at_offset<T>(v + ((c0 + base) * H + e) * DV,
+                                                              (t * vrow + col) * (uint32_t)sizeof(T)));
+                vv[0][r] = x[0];
+                vv[1][r] = x[1];
+                tame = tame && fabsf(x[0]) <= kLarge && fabsf(x[1]) <= kLarge;
             }
         }
         if (__syncthreads_or(!tame) && cap > 1) {
-            cap = 1;
-            continue;
+            cap = m = 1;
+            fetch_rows(base, m);
+            continue;                                    // nobody has read the LDS yet
         }
-        // products of gates: thread t takes column t of rho
-        if (tid < kBlock) {
-            float gg[kBlock], x = 1.f, gam = 1.f;
+        float gg[kBlock], bb[kBlock];
 #pragma unroll
-            for (int i = 0; i < kBlock; i += 4)
-                *reinterpret_cast<f32x4_t*>(gg + i) = *reinterpret_cast<const f32x4_t*>(sG + i);
-#pragma unroll
-            for (int i = 0; i < kBlock; ++i) {
-                x = i > tid ? x * gg[i] : 1.f;
-                gam = i < tid ? gam * gg[i] : gam;
-                sRho[i][tid] = x;                        // rho(i, tid); 1 up to i = tid
-            }
-            sGam[tid] = gam;                             // the product of the gates before tid
-            if (tid == kBlock - 1)
-                sGam[kBlock] = gam * gg[kBlock - 1];
+        for (int t = 0; t < kBlock; ++t) {
+            gg[t] = lane_value(gl, t);
+            bb[t] = lane_value(bl, t);
         }
-        __syncthreads();
-        // the four products of tokens with tokens, 4 / W of them a wavefront
-#pragma unroll
-        for (int x = 0; x < 4 / W; ++x) {
-            const int mat = wave + x * W;                // K K^T, K KW^T, Q K^T, Q KW^T
-            const float* pa = (mat < 2 ? sK : sQ) + j * LD + 4 * kq;
-            const float* pb = (mat & 1 ? sKW : sK) + j * LD + 4 * kq;
-            f32x4_t d0 = {}, d1 = {};
-#pragma unroll
-            for (int R = 0; R < RT; ++R) {
-                const f32x4_t fa = *reinterpret_cast<const f32x4_t*>(pa + 16 * R);
-                const f32x4_t fb = *reinterpret_cast<const f32x4_t*>(pb + 16 * R);
-                d0 = mfma4(fa[0], fb[0], d0);
-                d1 = mfma4(fa[1], fb[1], d1);
-                d0 = mfma4(fa[2], fb[2], d0);
-                d1 = mfma4(fa[3], fb[3], d1);
-            }
-            d0 += d1;
-            const int tj = slot_of(j);
-            const float gb = sG[tj] * sB[tj];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int ti = 4 * r + kq;               // the token of tile row 4 kq + r
-                float x = 0.f;                           // selected, not scaled: later tokens may be infinite
-                if (mat < 2 && tj < ti && ti < m)
-                    x = sRho[ti - 1][tj] * (mat == 0 ? gb : 1.f) * d0[r];
-                if (mat >= 2 && tj <= ti && ti < m)
-                    x = sRho[ti][tj] * (mat == 2 ? -gb : 1.f) * d0[r];
-                sM[mat][4 * kq + r][j] = x;
-            }
-        }
-        __syncthreads();
-        // (I + A)^-1, one column a lane, by substitution over the tokens
-        if (tid < kBlock) {
-            float col[kBlock];
-#pragma unroll
-            for (int i = 0; i < kBlock; ++i) {
-                float row[kBlock];                       // A's row of token i, by tile column
-#pragma unroll
-                for (int l = 0; l < kBlock; l += 4)
-                    *reinterpret_cast<f32x4_t*>(row + l) =
-                        *reinterpret_cast<const f32x4_t*>(&sM[0][slot_of(i)][l]);
-                float x = i == tid ? 1.f : 0.f;
-#pragma unroll
-                for (int l = 0; l < i; ++l)
-                    x -= row[slot_of(l)] * col[l];
-                col[i] = x;
-            }
-            __builtin_amdgcn_wave_barrier();             // every lane has read A
-#pragma unroll
-            for (int i = 0; i < kBlock; ++i)
-                sM[0][slot_of(i)][slot_of(tid)] = col[i];
-        }
-        // K S and Q S
-        f32x4_t ks[2] = {}, qs[2] = {};
+        // [K; Q] [K; KW]^T
+        f32x4_t d0 = {}, d1 = {};
+        const float* pa = sRows + ((j + 8) & 15) * LD + 4 * kq;      // row j of [K; Q]
+        const float* pb = sRows + (j + 8) * LD + 4 * kq;             // row j of [K; KW]
 #pragma unroll
         for (int R = 0; R < RT; ++R) {
-            const f32x4_t fk = *reinterpret_cast<const f32x4_t*>(sK + j * LD + 16 * R + 4 * kq);
-            const f32x4_t fq = *reinterpret_cast<const f32x4_t*>(sQ + j * LD + 16 * R + 4 * kq);
+            const f32x4_t fa = *reinterpret_cast<const f32x4_t*>(pa + 16 * R);
+            const f32x4_t fb = *reinterpret_cast<const f32x4_t*>(pb + 16 * R);
+            d0 = mfma4(fa[0], fb[0], d0);
+            d1 = mfma4(fa[1], fb[1], d1);
+            d0 = mfma4(fa[2], fb[2], d0);
+            d1 = mfma4(fa[3], fb[3], d1);
+        }
+        d0 += d1;
+        // element (i, j): token ti of row i against token tj of column j, times the gates
+        // between them: for a row of K those before ti, for a row of Q those up to ti
+        const int tj = token_of(j & 7);
+        float rho[4] = {}, gam[4], run = 0.f, all = 1.f, own = 0.f;
+#pragma unroll
+        for (int t = 0; t < kBlock; ++t) {
+            const float before = all, upto = run;        // products of the gates before t; from tj + 1 before t
+            all *= gg[t];
+            run = t == tj ? 1.f : run * gg[t];           // 0 before tj, rho(t, tj) from there on
+            own = t == tj ? gg[t] * bb[t] : own;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (t == 2 * r + (kq & 1)) {
+                    rho[r] = kq < 2 ? upto : run;
+                    gam[r] = kq < 2 ? before : all;
+                }
+        }
+        __builtin_amdgcn_sched_barrier(0);               // keep the stages' LDS reads apart: registers
+        float(*M0)[20] = sM[wave][0], (*M1)[20] = sM[wave][1];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int ti = 2 * r + (kq & 1);
+            float x = 0.f;                               // selected, not scaled: see above
+            if (ti < m && (kq < 2 ? tj < ti : tj <= ti))
+                x = rho[r] * (j < 8 ? own : 1.f) * d0[r];
+            M0[4 * kq + r][j] = x;
+        }
+        // T by substitution, column tj' = slot lane % 8 on every group of 8 lanes; row lane / 8 of
+        // T and of -C T is kept
+        {
+            const int c = lane & 7, gr = lane >> 3;
+            float tc[kBlock];                            // T's column, by token
+#pragma unroll
+            for (int i = 0; i < kBlock; ++i) {
+                float x = token_of(c) == i ? 1.f : 0.f;
+                const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(&M0[slot_of(i)][0]);
+                const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(&M0[slot_of(i)][4]);
+#pragma unroll
+                for (int l = 0; l < i; ++l)
+                    x -= ((l & 1) ? hi[l >> 1] : lo[l >> 1]) * tc[l];
+                tc[i] = x;
+            }
+            const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(&M0[8 + gr][0]);
+            const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(&M0[8 + gr][4]);
+            float ct = 0.f, tt = 0.f;
+#pragma unroll
+            for (int l = 0; l < kBlock; ++l) {
+                ct -= ((l & 1) ? hi[l >> 1] : lo[l >> 1]) * tc[l];
+                tt = slot_of(l) == gr ? tc[l] : tt;
+            }
+            M1[gr][c] = tt;
+            M1[gr][8 + c] = 0.f;
+            M1[8 + gr][c] = ct;
+            M1[8 + gr][8 + c] = gr == c ? 1.f : 0.f;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // [K; Q] S
+        f32x4_t x[2] = {};
+#pragma unroll
+        for (int R = 0; R < RT; ++R) {
+            const f32x4_t fa = *reinterpret_cast<const f32x4_t*>(pa + 16 * R);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    ks[c] = mfma4(fk[r], s[R][c][r], ks[c]);
-                    qs[c] = mfma4(fq[r], s[R][c][r], qs[c]);
-                }
+                for (int c = 0; c < 2; ++c)
+                    x[c] = mfma4(fa[r], s[R][r][c], x[c]);
         }
-        __syncthreads();
-        f32x4_t pp[2] = {};
-        {
-            const f32x4_t fb = *reinterpret_cast<const f32x4_t*>(&sM[1][j][4 * kq]);
-            const f32x4_t ft = *reinterpret_cast<const f32x4_t*>(&sM[0][j][4 * kq]);
-            const f32x4_t fc = *reinterpret_cast<const f32x4_t*>(&sM[2][j][4 * kq]);
-            const f32x4_t fe = *reinterpret_cast<const f32x4_t*>(&sM[3][j][4 * kq]);
+        // + [B; E] V (columns 8.. of the first matrix; the second half of vv repeats the first)
+        const f32x4_t fv = *reinterpret_cast<const f32x4_t*>(&M0[j][8 + 4 * (kq & 1)]);
+        const f32x4_t fw = *reinterpret_cast<const f32x4_t*>(&M1[j][4 * kq]);
+        f32x4_t y[2] = {};
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < 2; ++c) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    ks[c][r] *= sGam[4 * r + kq];
-                    qs[c][r] *= sGam[4 * r + kq + 1];
-                }
+            for (int r = 0; r < 4; ++r)
+                x[c][r] *= gam[r];
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (r < steps)
-                        ks[c] = mfma4(fb[r], vv[c][r], ks[c]);
+            for (int r = 0; r < 4; ++r)
+                if (r < steps)
+                    x[c] = mfma4(kq < 2 ? fv[r] : 0.f, vv[c][r], x[c]);
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (r < steps)
-                        pp[c] = mfma4(ft[r], ks[c][r], pp[c]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (r < steps) {
-                        qs[c] = mfma4(fc[r], pp[c][r], qs[c]);
-                        qs[c] = mfma4(fe[r], vv[c][r], qs[c]);
-                    }
-            }
+            for (int r = 0; r < 4; ++r)
+                if (r < steps)
+                    y[c] = mfma4(fw[r], x[c][r], y[c]);
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int t = 4 * r + kq;
+            const int t = 2 * r + (kq & 1);
             if (t < m) {
-                const int64_t at = ((c0 + base + t) * H + e) * DV + 32 * wave + 2 * j;
-                store2(o + at, qs[0][r], qs[1][r]);
-                store2(p_out + at, pp[0][r], pp[1][r]);
+                const int64_t row = ((c0 + base) * H + e) * DV;
+                const uint32_t at = t * vrow + col;
+                if (kq < 2)
+                    *at_offset<f32x2_t>(p_out + row, at * 4) = f32x2_t{y[0][r], y[1][r]};
+                else
+                    F::store2(at_offset<T>(o + row, at * (uint32_t)sizeof(T)), y[0][r], y[1][r]);
             }
         }
-        if (base + m < len) {                            // the state enters the next block
-            const float gam = sGam[kBlock];
-            f32x4_t x[2], y[2];
+        if (base + m >= len)
+            break;
+        {                                                // the state enters the next pass
+            f32x4_t xy[2];
+            float after = 1.f, fx[kBlock], fy[kBlock];
+#pragma unroll
+            for (int t = kBlock - 1; t >= 0; --t) {
+                fy[t] = after;                           // the product of the gates after t
+                after *= gg[t];
+                fx[t] = -after * bb[t];
+            }
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int t = 4 * r + kq;
-                const float rho = sRho[kBlock - 1][t], gb = -rho * sG[t] * sB[t];
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    x[c][r] = t < m ? gb * pp[c][r] : 0.f;
-                    y[c][r] = rho * vv[c][r];
-                }
-            }
-#pragma unroll
-            for (int R = 0; R < RT; ++R)
+                const int t = 2 * r + (kq & 1);
+                const float f = kq & 1 ? (kq < 2 ? fx[2 * r + 1] : fy[2 * r + 1]) : (kq < 2 ? fx[2 * r] : fy[2 * r]);
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
-                    s[R][c] *= gam;
-            add_tokens<RT, LD>(s, sK, sKW, steps, kq, j, x, y);
+                    xy[c][r] = t < m ? f * (kq < 2 ? y[c][r] : vv[c][r]) : 0.f;
+            }
+            // S <- after S + [K; KW]^T [X; Y]
+#pragma unroll
+            for (int R = 0; R < RT; ++R) {
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    f32x4_t d = {};
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        d = mfma4(sRows[(8 + 4 * kq + r) * LD + 16 * R + j], xy[c][r], d);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        s[R][r][c] = after * s[R][r][c] + d[r];
+                }
+            }
         }
         base += m;
+        m = len - base < cap ? len - base : cap;
+        fetch_rows(base, m);
+        __syncthreads();                                 // this pass is done with the LDS
     }
 }
 
 // S_out and hist_out may be S and hist: a thread has read what it overwrites.
-// blockIdx.y is a band of DK / gridDim.y state rows.
+// blockIdx.y is a band of ROWS state rows.
 template <typename T, int DK, int DV, int ROWS>
 __global__ __launch_bounds__(2 * DV) void commit_kernel(
     const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ g, const T* __restrict__ b,
@@ -386,10 +491,9 @@ __global__ __launch_bounds__(2 * DV) void commit_kernel(
     const float* __restrict__ kw, const float* __restrict__ p, const float* S, const T* hist, float* S_out,
     T* hist_out)
 {
-    constexpr int NTH = 2 * DV, RT = ROWS / 16, LD = ROWS + 4;
-    constexpr int VE = Vec16<T>::N;
-    __shared__ __align__(16) float sK[kBlock * LD], sKW[kBlock * LD];
-    __shared__ float sG[kBlock], sB[kBlock], sRho[kBlock + 1];
+    using F = Four<T>;
+    constexpr int NTH = 2 * DV, RT = ROWS / 16, LD = ROWS + 4, CG = ROWS / 4;
+    __shared__ __align__(16) float sRows[16 * LD];       // rows of K, then of KW
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, kq = lane >> 4, j = lane & 15;
     const int64_t chain = blockIdx.x;
@@ -404,13 +508,12 @@ __global__ __launch_bounds__(2 * DV) void commit_kernel(
         return;
 
     f32x4_t s[RT][2];
-    const int64_t at0 = (chain * DK + row0) * DV + 32 * wave + 2 * j;
+    const int col = 32 * wave + 2 * j;
 #pragma unroll
     for (int R = 0; R < RT; ++R)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const f32x2_t x = __builtin_nontemporal_load(
-                reinterpret_cast<const f32x2_t*>(S + at0 + (16 * R + 4 * kq + r) * DV));
+            const f32x2_t x = state_load<DV>(S + (chain * DK + row0 + 16 * R + r) * DV, kq, col);
             s[R][0][r] = x[0];
             s[R][1][r] = x[1];
         }
@@ -429,70 +532,57 @@ __global__ __launch_bounds__(2 * DV) void commit_kernel(
 
     for (int base = 0; base < len; base += kBlock) {
         const int m = len - base < kBlock ? len - base : kBlock;
-        const int steps = (m + 3) >> 2;
+        const int steps = (m + 1) >> 1;
         if (base > 0)
-            __syncthreads();
-        if (tid < kBlock) {
-            const bool on = tid < m;
-            const int64_t at = (c0 + base + tid) * H + e;
-            sG[tid] = on ? to_f32(g[at]) : 1.f;
-            sB[tid] = on ? to_f32(b[at]) : 0.f;
-        }
-        for (int i = tid; i < 4 * steps * (ROWS / VE); i += NTH) {
-            const int t = i / (ROWS / VE), ch = (i % (ROWS / VE)) * VE, to = slot_of(t) * LD + ch;
-            float kt[VE], wt[VE];
-#pragma unroll
-            for (int x = 0; x < VE; ++x)
-                kt[x] = wt[x] = 0.f;
+            __syncthreads();                             // the pass before is done with the LDS
+        for (int i = tid; i < 2 * steps * CG; i += NTH) {
+            const int t = i / CG, ch = (i % CG) * 4, to = slot_of(t) * LD + ch;
+            f32x4_t kt = {}, wt = {};
             if (t < m) {
                 const int64_t at = ((c0 + base + t) * H + e) * DK + row0 + ch;
-                Vec16<T>::load(k + at, kt);
-#pragma unroll
-                for (int x = 0; x < VE; x += 4)
-                    Vec16<float>::load(kw + at + x, wt + x);
+                kt = F::f32(load4(k + at));
+                wt = load4(kw + at);
             }
-#pragma unroll
-            for (int x = 0; x < VE; x += 4) {
-                *reinterpret_cast<f32x4_t*>(sK + to + x) = f32x4_t{kt[x], kt[x + 1], kt[x + 2], kt[x + 3]};
-                *reinterpret_cast<f32x4_t*>(sKW + to + x) = f32x4_t{wt[x], wt[x + 1], wt[x + 2], wt[x + 3]};
-            }
+            *reinterpret_cast<f32x4_t*>(sRows + to) = kt;
+            *reinterpret_cast<f32x4_t*>(sRows + 8 * LD + to) = wt;
         }
-        f32x4_t x[2] = {}, y[2] = {};
+        float gl = 1.f, bl = 0.f;
+        if ((lane & 7) < m) {
+            const int64_t at = (c0 + base + (lane & 7)) * H + e;
+            gl = to_f32(g[at]);
+            bl = to_f32(b[at]);
+        }
+        f32x4_t xy[2] = {};                              // p over v
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int t = 4 * r + kq;
+            const int t = 2 * r + (kq & 1);
             if (t < m) {
-                const int64_t at = ((c0 + base + t) * H + e) * DV + 32 * wave + 2 * j;
-                const float2 pv = load2(p + at), vv = load2(v + at);
-                x[0][r] = pv.x; x[1][r] = pv.y;
-                y[0][r] = vv.x; y[1][r] = vv.y;
+                const int64_t at = ((c0 + base + t) * H + e) * DV + col;
+                f32x2_t x;
+                if (kq < 2)
+                    x = *reinterpret_cast<const f32x2_t*>(p + at);
+                else
+                    x = F::load2(v + at);
+                xy[0][r] = x[0];
+                xy[1][r] = x[1];
             }
         }
         __syncthreads();
-        if (tid <= kBlock) {                             // the product of the gates tid..m-1
-            float f = 1.f;
-            for (int i = tid; i < kBlock; ++i)
-                f *= sG[i];
-            sRho[tid] = f;
+        float after = 1.f;
+        float f[4];
+#pragma unroll
+        for (int t = kBlock - 1; t >= 0; --t) {
+            const float gt = lane_value(gl, t), bt = lane_value(bl, t);
+            const float fy = after;                      // the product of the gates after t
+            after *= gt;
+            f[t >> 1] = (kq & 1) == (t & 1) ? (kq < 2 ? -after * bt : fy) : f[t >> 1];
         }
-        __syncthreads();
-        const float gam = sRho[0];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int t = 4 * r + kq;
-            const float fx = -sRho[t] * sB[t], fy = sRho[t + 1];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                x[c][r] *= fx;
-                y[c][r] *= fy;
-            }
+            xy[0][r] *= f[r];
+            xy[1][r] *= f[r];
         }
-#pragma unroll
-        for (int R = 0; R < RT; ++R)
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-                s[R][c] *= gam;
-        add_tokens<RT, LD>(s, sK, sKW, steps, kq, j, x, y);
+        add_tokens<RT, LD>(s, after, sRows, steps, kq, j, xy);
     }
 #pragma unroll
     for (int R = 0; R < RT; ++R)
@@ -500,18 +590,28 @@ __global__ __launch_bounds__(2 * DV) void commit_kernel(
         for (int r = 0; r < 4; ++r) {
             const f32x2_t x = {s[R][0][r], s[R][1][r]};
             __builtin_nontemporal_store(
-                x, reinterpret_cast<f32x2_t*>(S_out + at0 + (16 * R + 4 * kq + r) * DV));
+                x, at_offset<f32x2_t>(S_out + (chain * DK + row0 + 16 * R + r) * DV, (uint32_t)(4 * kq * DV + col) * 4));
         }
 }
 
-template <typename T, int DK, int DV>
-static hipError_t launch_draft_t(const DraftArgs& p, hipStream_t stream)
+template <typename T, int DK, int DV, int LEV>
+static hipError_t launch_draft_lev(const DraftArgs& p, hipStream_t stream)
 {
-    hipLaunchKernelGGL((draft_kernel<T, DK, DV>), dim3((unsigned)((int64_t)p.n_seqs * p.heads)), dim3(2 * DV), 0,
+    hipLaunchKernelGGL((draft_kernel<T, DK, DV, LEV>), dim3((unsigned)((int64_t)p.n_seqs * p.heads)), dim3(2 * DV), 0,
                        stream, (const T*)p.q, (const T*)p.k, (const T*)p.v, (const T*)p.u, (const T*)p.a,
                        (const T*)p.h, (const T*)p.g, (const T*)p.b, (const T*)p.conv_w, p.cu_seqlens, p.heads,
                        p.L, p.gelu, p.S, (const T*)p.k_hist, (T*)p.o, p.kw, p.p);
     return hipGetLastError();
+}
+
+// Levels loaded at a time: all of them up to L = 4 and up to L = 8, seven at a time
+// beyond.
+template <typename T, int DK, int DV>
+static hipError_t launch_draft_t(const DraftArgs& p, hipStream_t stream)
+{
+    if (p.L == 1)
+        return launch_draft_lev<T, DK, DV, 0>(p, stream);
+    return p.L <= 4 ? launch_draft_lev<T, DK, DV, 3>(p, stream) : launch_draft_lev<T, DK, DV, 7>(p, stream);
 }
 
 template <typename T, int DK, int DV>
