@@ -128,6 +128,22 @@ template <int DV> __device__ __forceinline__ f32x2_t state_load(const float* S, 
     return __builtin_nontemporal_load(at_offset<f32x2_t>(S, (uint32_t)(4 * kq * DV + col) * 4));
 }
 
+// The factors of p (rows kq < 2) and v in [X; Y] of up to 8 tokens whose gates lane t
+// holds (1 and 0 past the last): -between rho(last, t) g_t b_t and between rho(last, t).
+// Returns between times all their gates.
+__device__ __forceinline__ float scale_tokens(float gl, float bl, int kq, float between, float (&f)[4])
+{
+    float after = between;                               // times the product of the gates after t
+#pragma unroll
+    for (int t = kBlock - 1; t >= 0; --t) {
+        const float y = after;
+        after *= lane_value(gl, t);
+        const float x = -after * lane_value(bl, t);
+        f[t >> 1] = (t & 1) == 1 || (kq & 1) == 0 ? (kq < 2 ? x : y) : f[t >> 1];
+    }
+    return after;
+}
+
 // S <- gam S + [K; KW]^T [X; Y] for the rows of [K; KW] in LDS (fp32, 16 rows of
 // LD); xy is [X; Y] as a tile; `steps` = ceil(tokens / 2)
 template <int RT, int LD>
@@ -254,10 +270,13 @@ __global__ __launch_bounds__(2 * DV, 2) void draft_kernel(
     }
     __syncthreads();                                     // the write keys of the chain are in kw_out
 
-    // a pass's rows of K, Q and KW on their way into LDS (zeros past its tokens)
+    // what a pass reads of its tokens: the rows of K, Q and KW on their way into LDS
+    // (zeros past its tokens), its gates (lane t holds token t's) and its value rows:
+    // register r holds row 4 (kq % 2) + r, token 2 r + kq % 2, in both halves
     typename F::raw kr[ITEMS], qr[ITEMS];
-    f32x4_t wr[ITEMS];
-    auto fetch_rows = [&](int base, int m) {
+    f32x4_t wr[ITEMS], vv[2];
+    float gl, bl;
+    auto fetch = [&](int base, int m) {
 #pragma unroll
         for (int x = 0; x < ITEMS; ++x) {
             const int i = tid + x * NTH, t = i / CG;
@@ -270,22 +289,51 @@ __global__ __launch_bounds__(2 * DV, 2) void draft_kernel(
                 wr[x] = *reinterpret_cast<const f32x4_t*>(kw_out + at);
             }
         }
+        gl = 1.f;
+        bl = 0.f;
+        if ((lane & 7) < m) {
+            const int64_t at = (c0 + base + (lane & 7)) * H + e;
+            gl = to_f32(g[at]);
+            bl = to_f32(b[at]);
+        }
+        vv[0] = vv[1] = f32x4_t{};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int t = 2 * r + (kq & 1);
+            if (t < m) {
+                const f32x2_t x = F::load2(v + ((c0 + base + t) * H + e) * DV + col);
+                vv[0][r] = x[0];
+                vv[1][r] = x[1];
+            }
+        }
+    };
+    // the state is streamed: tiles R .. R + PRE - 1 in flight, each row 16 R + 4 kq + r in two columns
+    constexpr int PRE = RT < 4 ? RT : 4;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<float*>(S + chain * DK * DV), 0, DK * DV * 4, 0x00020000);
+    const int sat = (4 * kq * DV + col) * 4;
+    f32x2_t s[PRE][4];
+    auto fetch_state = [&](int R) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            s[R % PRE][r] = __builtin_bit_cast(
+                f32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rs, sat, (16 * R + r) * DV * 4, 2));
     };
 
     // A token's zeros in the triangular matrices would turn an infinity or a NaN
     // of a later token into a NaN of its own, so a sequence with a value beyond
     // kLarge (whose products may overflow too) takes its tokens one at a time.
-    int cap = kBlock, base = 0, m = len < cap ? len : cap;
-    fetch_rows(0, m);
-    f32x2_t s[RT][4];                                    // as read: row 16 R + 4 kq + r, two columns
-#pragma unroll
-    for (int R = 0; R < RT; ++R)                         // behind the rows: in flight while those are worked on
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            s[R][r] = state_load<DV>(S + (chain * DK + 16 * R + r) * DV, kq, col);
-    for (;;) {
+    int cap = kBlock, m;
+    for (int base = 0; base < len; base += m) {
+        m = len - base < cap ? len - base : cap;
         const int steps = (m + 1) >> 1;
-        bool tame = true;
+        if (base > 0)
+            __syncthreads();                             // the pass before is done with the LDS
+        fetch(base, m);
+#pragma unroll
+        for (int R = 0; R < PRE; ++R)                    // behind the rows: in flight while those are worked on
+            fetch_state(R);
+        bool tame = fabsf(gl) <= kLarge && fabsf(bl) <= kLarge && tame4(vv[0]) && tame4(vv[1]);
 #pragma unroll
         for (int x = 0; x < ITEMS; ++x) {
             const int i = tid + x * NTH, t = i / CG, to = slot_of(t) * LD + (i % CG) * 4;
@@ -297,31 +345,10 @@ __global__ __launch_bounds__(2 * DV, 2) void draft_kernel(
                 tame = tame && tame4(kt) && tame4(wr[x]);
             }
         }
-        // gates: lane t holds token t's; then every lane has all of them
-        float gl = 1.f, bl = 0.f;
-        if ((lane & 7) < m) {
-            const int64_t at = (c0 + base + (lane & 7)) * H + e;
-            gl = to_f32(g[at]);
-            bl = to_f32(b[at]);
-            tame = tame && fabsf(gl) <= kLarge && fabsf(bl) <= kLarge;
-        }
-        // value rows: register r holds row 4 (kq % 2) + r, token 2 r + kq % 2, in both halves
-        f32x4_t vv[2] = {};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int t = 2 * r + (kq & 1);
-            if (t < m) {
-                const f32x2_t x = F::load2(at_offset<T>(v + ((c0 + base) * H + e) * DV,
-                                                              (t * vrow + col) * (uint32_t)sizeof(T)));
-                vv[0][r] = x[0];
-                vv[1][r] = x[1];
-                tame = tame && fabsf(x[0]) <= kLarge && fabsf(x[1]) <= kLarge;
-            }
-        }
         if (__syncthreads_or(!tame) && cap > 1) {
-            cap = m = 1;
-            fetch_rows(base, m);
-            continue;                                    // nobody has read the LDS yet
+            cap = 1;
+            m = 0;                                       // the same tokens again
+            continue;
         }
         float gg[kBlock], bb[kBlock];
 #pragma unroll
@@ -341,6 +368,8 @@ __global__ __launch_bounds__(2 * DV, 2) void draft_kernel(
             d1 = mfma4(fa[1], fb[1], d1);
             d0 = mfma4(fa[2], fb[2], d0);
             d1 = mfma4(fa[3], fb[3], d1);
+            if (R % 4 == 3)
+                __builtin_amdgcn_sched_barrier(0);       // not all the LDS reads at once: registers
         }
         d0 += d1;
         // element (i, j): token ti of row i against token tj of column j, times the gates
@@ -360,7 +389,7 @@ __global__ __launch_bounds__(2 * DV, 2) void draft_kernel(
                     gam[r] = kq < 2 ? before : all;
                 }
         }
-        __builtin_amdgcn_sched_barrier(0);               // keep the stages' LDS reads apart: registers
+        __builtin_amdgcn_sched_barrier(0);
         float(*M0)[20] = sM[wave][0], (*M1)[20] = sM[wave][1];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -384,6 +413,8 @@ __global__ __launch_bounds__(2 * DV, 2) void draft_kernel(
                 for (int l = 0; l < i; ++l)
                     x -= ((l & 1) ? hi[l >> 1] : lo[l >> 1]) * tc[l];
                 tc[i] = x;
+                if (i % 4 == 3)
+                    __builtin_amdgcn_sched_barrier(0);
             }
             const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(&M0[8 + gr][0]);
             const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(&M0[8 + gr][4]);
@@ -408,17 +439,78 @@ __global__ __launch_bounds__(2 * DV, 2) void draft_kernel(
             for (int r = 0; r < 4; ++r)
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
-                    x[c] = mfma4(fa[r], s[R][r][c], x[c]);
+                    x[c] = mfma4(fa[r], s[R % PRE][r][c], x[c]);
+            if (R + PRE < RT)
+                fetch_state(R + PRE);
+            if (R % 4 == 3)
+                __builtin_amdgcn_sched_barrier(0);
         }
-        // + [B; E] V (columns 8.. of the first matrix; the second half of vv repeats the first)
+        // columns 8.. of the first matrix ([B; E]; the second half of vv repeats the first), and W
         const f32x4_t fv = *reinterpret_cast<const f32x4_t*>(&M0[j][8 + 4 * (kq & 1)]);
         const f32x4_t fw = *reinterpret_cast<const f32x4_t*>(&M1[j][4 * kq]);
+        if (base > 0) {
+            // the tokens of earlier passes, 8 at a time from the latest: their part of the state
+            // is [K'; KW']^T [X'; Y'], so that they add ([K; Q] [K'; KW']^T) [X'; Y'] of 16x16
+            f32x4_t z[2] = {};
+            float between = 1.f;                         // the product of the gates from here to this pass
+            for (int cb = (base - 1) / kBlock * kBlock; cb >= 0; cb -= kBlock) {
+                const int mc = base - cb < kBlock ? base - cb : kBlock;
+                float gc = 1.f, bc = 0.f;
+                if ((lane & 7) < mc) {
+                    const int64_t at = (c0 + cb + (lane & 7)) * H + e;
+                    gc = to_f32(g[at]);
+                    bc = to_f32(b[at]);
+                }
+                f32x4_t xy[2] = {}, d = {};
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int t = 2 * r + (kq & 1);
+                    if (t < mc) {                        // p: what this lane has stored itself
+                        const int64_t at = ((c0 + cb + t) * H + e) * DV + col;
+                        const f32x2_t y = kq < 2 ? *reinterpret_cast<const f32x2_t*>(p_out + at) : F::load2(v + at);
+                        xy[0][r] = y[0];
+                        xy[1][r] = y[1];
+                    }
+                }
+                const int tc = token_of(j & 7);
+                const int64_t row = ((c0 + cb + (tc < mc ? tc : 0)) * H + e) * DK + 4 * kq;
+#pragma unroll
+                for (int R = 0; R < RT; ++R) {
+                    const f32x4_t fa = *reinterpret_cast<const f32x4_t*>(pa + 16 * R);
+                    f32x4_t fb = {};
+                    if (tc < mc)
+                        fb = j < 8 ? F::f32(load4(k + row + 16 * R)) : load4(kw_out + row + 16 * R);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        d = mfma4(fa[r], fb[r], d);
+                    if (R % 2 == 1)
+                        __builtin_amdgcn_sched_barrier(0);
+                }
+                float f[4];
+                between = scale_tokens(gc, bc, kq, between, f);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    xy[0][r] *= f[r];
+                    xy[1][r] *= f[r];
+                    M0[4 * kq + r][j] = d[r];
+                }
+                const f32x4_t fd = *reinterpret_cast<const f32x4_t*>(&M0[j][4 * kq]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        z[c] = mfma4(fd[r], xy[c][r], z[c]);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                x[c] = between * x[c] + z[c];
+        }
         f32x4_t y[2] = {};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                x[c][r] *= gam[r];
+            for (int r = 0; r < 4; ++r)                  // rows past the tokens stay out of the next product
+                x[c][r] = 2 * r + (kq & 1) < m ? gam[r] * x[c][r] : 0.f;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 if (r < steps)
@@ -440,45 +532,6 @@ __global__ __launch_bounds__(2 * DV, 2) void draft_kernel(
                     F::store2(at_offset<T>(o + row, at * (uint32_t)sizeof(T)), y[0][r], y[1][r]);
             }
         }
-        if (base + m >= len)
-            break;
-        {                                                // the state enters the next pass
-            f32x4_t xy[2];
-            float after = 1.f, fx[kBlock], fy[kBlock];
-#pragma unroll
-            for (int t = kBlock - 1; t >= 0; --t) {
-                fy[t] = after;                           // the product of the gates after t
-                after *= gg[t];
-                fx[t] = -after * bb[t];
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = 2 * r + (kq & 1);
-                const float f = kq & 1 ? (kq < 2 ? fx[2 * r + 1] : fy[2 * r + 1]) : (kq < 2 ? fx[2 * r] : fy[2 * r]);
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    xy[c][r] = t < m ? f * (kq < 2 ? y[c][r] : vv[c][r]) : 0.f;
-            }
-            // S <- after S + [K; KW]^T [X; Y]
-#pragma unroll
-            for (int R = 0; R < RT; ++R) {
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    f32x4_t d = {};
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        d = mfma4(sRows[(8 + 4 * kq + r) * LD + 16 * R + j], xy[c][r], d);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        s[R][r][c] = after * s[R][r][c] + d[r];
-                }
-            }
-        }
-        base += m;
-        m = len - base < cap ? len - base : cap;
-        fetch_rows(base, m);
-        __syncthreads();                                 // this pass is done with the LDS
     }
 }
 
@@ -568,15 +621,8 @@ __global__ __launch_bounds__(2 * DV) void commit_kernel(
             }
         }
         __syncthreads();
-        float after = 1.f;
         float f[4];
-#pragma unroll
-        for (int t = kBlock - 1; t >= 0; --t) {
-            const float gt = lane_value(gl, t), bt = lane_value(bl, t);
-            const float fy = after;                      // the product of the gates after t
-            after *= gt;
-            f[t >> 1] = (kq & 1) == (t & 1) ? (kq < 2 ? -after * bt : fy) : f[t >> 1];
-        }
+        const float after = scale_tokens(gl, bl, kq, 1.f, f);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             xy[0][r] *= f[r];
