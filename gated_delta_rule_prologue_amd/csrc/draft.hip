@@ -63,42 +63,85 @@ __device__ __forceinline__ f32x4_t mfma4(float a, float b, f32x4_t c)
     return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
+// A value whose uses stay where they are: what derives from it is computed anew in each
+// pass of a loop instead of being kept in registers around it.
+__device__ __forceinline__ int opaque(int x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // row of a token within its half of a tile, and back
 __device__ __forceinline__ int slot_of(int t) { return 4 * (t & 1) + (t >> 1); }
 __device__ __forceinline__ int token_of(int s) { return 2 * (s & 3) + (s >> 2); }
 
 typedef __attribute__((ext_vector_type(2))) float f32x2_t;
 typedef __attribute__((ext_vector_type(2))) uint32_t u32x2_t;
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
 
-// Four elements of the storage type, raw and as fp32; two elements as fp32.
-template <typename T> struct Four;
-template <> struct Four<uint16_t> {
-    typedef u32x2_t raw;
-    __device__ static f32x4_t f32(raw x)
+// Device memory read and written at 32-bit byte offsets a lane from a base that is
+// the same for the whole wavefront (a buffer resource in scalar registers), bounded:
+// reads past the end give zeros, writes there are dropped, so tokens past the last
+// need no branch.
+struct Span {
+    __amdgpu_buffer_rsrc_t r;
+    __device__ Span(const void* p, int64_t bytes)
+        : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000))
+    {
+    }
+};
+
+// One, two and four elements of the storage type: raw, and as fp32.
+template <typename T> struct Elems;
+template <> struct Elems<uint16_t> {
+    typedef u32x2_t raw4;
+    typedef uint32_t raw2;
+    typedef uint16_t raw1;
+    template <int AUX = 0> __device__ static raw4 load4(const Span& b, uint32_t at)
+    {
+        return __builtin_bit_cast(raw4, __builtin_amdgcn_raw_buffer_load_b64(b.r, at, 0, AUX));
+    }
+    __device__ static raw2 load2(const Span& b, uint32_t at) { return __builtin_amdgcn_raw_buffer_load_b32(b.r, at, 0, 0); }
+    __device__ static raw1 load1(const Span& b, uint32_t at) { return __builtin_amdgcn_raw_buffer_load_b16(b.r, at, 0, 0); }
+    __device__ static f32x4_t f32(raw4 x)
     {
         return {__uint_as_float(x[0] << 16), __uint_as_float(x[0] & 0xffff0000u), __uint_as_float(x[1] << 16),
                 __uint_as_float(x[1] & 0xffff0000u)};
     }
-    __device__ static f32x2_t load2(const uint16_t* p)
+    __device__ static f32x2_t f32(raw2 x) { return {__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)}; }
+    __device__ static float f32(raw1 x) { return bf16_to_f32(x); }
+    __device__ static void store2(const Span& b, uint32_t at, float x, float y)
     {
-        const uint32_t x = *reinterpret_cast<const uint32_t*>(p);
-        return {__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)};
-    }
-    __device__ static void store2(uint16_t* p, float a, float b)
-    {
-        *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(a, b);
+        __builtin_amdgcn_raw_buffer_store_b32(pack_bf16x2(x, y), b.r, at, 0, 0);
     }
 };
-template <> struct Four<float> {
-    typedef f32x4_t raw;
-    __device__ static f32x4_t f32(raw x) { return x; }
-    __device__ static f32x2_t load2(const float* p) { return *reinterpret_cast<const f32x2_t*>(p); }
-    __device__ static void store2(float* p, float a, float b) { *reinterpret_cast<f32x2_t*>(p) = f32x2_t{a, b}; }
+template <> struct Elems<float> {
+    typedef u32x4_t raw4;
+    typedef u32x2_t raw2;
+    typedef uint32_t raw1;
+    template <int AUX = 0> __device__ static raw4 load4(const Span& b, uint32_t at)
+    {
+        return __builtin_bit_cast(raw4, __builtin_amdgcn_raw_buffer_load_b128(b.r, at, 0, AUX));
+    }
+    template <int AUX = 0> __device__ static raw2 load2(const Span& b, uint32_t at)
+    {
+        return __builtin_bit_cast(raw2, __builtin_amdgcn_raw_buffer_load_b64(b.r, at, 0, AUX));
+    }
+    __device__ static raw1 load1(const Span& b, uint32_t at) { return __builtin_amdgcn_raw_buffer_load_b32(b.r, at, 0, 0); }
+    __device__ static f32x4_t f32(raw4 x) { return __builtin_bit_cast(f32x4_t, x); }
+    __device__ static f32x2_t f32(raw2 x) { return __builtin_bit_cast(f32x2_t, x); }
+    __device__ static float f32(raw1 x) { return __uint_as_float(x); }
+    __device__ static void store2(const Span& b, uint32_t at, float x, float y)
+    {
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, f32x2_t{x, y}), b.r, at, 0, 0);
+    }
+    __device__ static void store4(const Span& b, uint32_t at, f32x4_t x)
+    {
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, x), b.r, at, 0, 0);
+    }
 };
-template <typename T> __device__ __forceinline__ typename Four<T>::raw load4(const T* p)
-{
-    return *reinterpret_cast<const typename Four<T>::raw*>(p);
-}
+typedef Elems<float> E32;
+constexpr int kOnce = 2;                         // nontemporal: read once per call
 
 __device__ __forceinline__ bool tame4(f32x4_t x)
 {
@@ -108,24 +151,6 @@ __device__ __forceinline__ bool tame4(f32x4_t x)
 __device__ __forceinline__ float lane_value(float x, int lane)
 {
     return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), lane));
-}
-
-// An element at a 32-bit byte offset a lane from a base that is the same for the
-// whole wavefront (which then stays in scalar registers).
-template <typename V, typename P> __device__ __forceinline__ const V* at_offset(const P* base, uint32_t bytes)
-{
-    return reinterpret_cast<const V*>(reinterpret_cast<const char*>(base) + bytes);
-}
-template <typename V, typename P> __device__ __forceinline__ V* at_offset(P* base, uint32_t bytes)
-{
-    return reinterpret_cast<V*>(reinterpret_cast<char*>(base) + bytes);
-}
-
-// Row 4 kq of S (uniform; the caller adds 16 R + r rows), columns col and col + 1:
-// nontemporal, since the state is read once and written once per step.
-template <int DV> __device__ __forceinline__ f32x2_t state_load(const float* S, int kq, int col)
-{
-    return __builtin_nontemporal_load(at_offset<f32x2_t>(S, (uint32_t)(4 * kq * DV + col) * 4));
 }
 
 // The factors of p (rows kq < 2) and v in [X; Y] of up to 8 tokens whose gates lane t
@@ -171,181 +196,232 @@ __device__ __forceinline__ void add_tokens(f32x4_t (&s)[RT][2], float gam, const
 
 }  // namespace
 
-// The write key of one token in four channels, to kw_out (fp32).  LEV levels of u, a,
-// h are loaded at a time (LEV = 0: L = 1), every load issued before the first use.
-template <typename T, int DK, int LEV, bool GELU>
-__device__ __forceinline__ void form_write_key(const T* k, const T* u, const T* a, const T* h, const T* b,
-                                               const T* conv_w, const T* k_hist, int64_t chain, int64_t c0, int H,
-                                               int e, int L, int t, int ch, float* kw_out)
-{
-    using F = Four<T>;
-    using Raw = typename F::raw;
-    constexpr int LV = LEV > 0 ? LEV : 1;
-    const int64_t row = (c0 + t) * H + e, lev = row * (L - 1) * DK + ch;
-    Raw ar[LV], ur[LV], hr[LV], pr[3], wr[4];
-    auto fetch = [&](int l0) {                           // slots beyond the last re-read it
-#pragma unroll
-        for (int l = 0; l < LEV; ++l) {
-            const int sl = l0 + l < L - 2 ? l0 + l : L - 2, hl = sl < L - 3 ? sl : L > 2 ? L - 3 : 0;
-            ar[l] = __builtin_nontemporal_load(reinterpret_cast<const Raw*>(a + lev + (int64_t)sl * DK));
-            ur[l] = __builtin_nontemporal_load(reinterpret_cast<const Raw*>(u + lev + (int64_t)sl * DK));
-            hr[l] = __builtin_nontemporal_load(reinterpret_cast<const Raw*>(h + lev + (int64_t)hl * DK));
-        }
-    };
-    fetch(0);
-    const Raw kr = load4(k + row * DK + ch);
-#pragma unroll
-    for (int d = 1; d <= 3; ++d) {
-        const int pos = t - d;
-        pr[d - 1] = load4(pos >= 0 ? k + ((c0 + pos) * H + e) * DK + ch : k_hist + (chain * 3 + 3 + pos) * DK + ch);
+// The arrays of a chain's tokens base .. base + m - 1 (m <= 8), at their head's rows.
+template <typename T, int DK, int DV> struct Pass {
+    Span k, q, v, g, b, kw, p;
+    uint32_t krow, vrow, grow;                           // bytes from token to token
+    __device__ Pass(const T* k_, const T* q_, const T* v_, const T* g_, const T* b_, float* kw_, float* p_, int64_t at,
+                    int m, int H, int e)
+        : k(k_ + (at * H + e) * DK, bytes(m, H, DK, sizeof(T))), q(q_ + (at * H + e) * DK, bytes(m, H, DK, sizeof(T))),
+          v(v_ + (at * H + e) * DV, bytes(m, H, DV, sizeof(T))), g(g_ + at * H + e, bytes(m, H, 1, sizeof(T))),
+          b(b_ + at * H + e, bytes(m, H, 1, sizeof(T))), kw(kw_ + (at * H + e) * DK, bytes(m, H, DK, 4)),
+          p(p_ + (at * H + e) * DV, bytes(m, H, DV, 4)), krow(H * DK), vrow(H * DV), grow(H)
+    {
     }
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-        wr[x] = load4(conv_w + ((int64_t)e * DK + ch + x) * 4);
-    const float bt = to_f32(b[row]);
+    // up to the end of the last token's row
+    __device__ static int64_t bytes(int m, int H, int width, int size) { return ((int64_t)(m - 1) * H + 1) * width * size; }
+};
 
-    const f32x4_t kt = F::f32(kr), x1 = F::f32(pr[0]), x2 = F::f32(pr[1]), x3 = F::f32(pr[2]);
-    f32x4_t r, acc;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-        const f32x4_t w = F::f32(wr[x]);
-        r[x] = w[3] * kt[x] + w[2] * x1[x] + w[1] * x2[x] + w[0] * x3[x];
-        acc[x] = bt * kt[x];
+// The write key of one token (in a pass that starts at token `base` of its sequence) in
+// four channels, to its record in fp32; zeros past the pass.  LEV levels of u, a, h
+// are loaded at a time (LEV = 0: L = 1), every load issued before the first use.
+template <typename T, int DK, int DV, int LEV, bool GELU> struct WriteKey {
+    typedef Elems<T> X;
+    typedef typename X::raw4 raw4;
+    static constexpr int LV = LEV > 0 ? LEV : 1, ES = sizeof(T);
+    const Pass<T, DK, DV>& ps;
+    Span u, a, h, past, hist, w;
+    int base, L;
+
+    __device__ WriteKey(const Pass<T, DK, DV>& ps_, const T* k_, const T* u_, const T* a_, const T* h_, const T* conv_w,
+                        const T* k_hist, int64_t chain, int64_t c0, int base_, int m, int H, int e, int L_)
+        : ps(ps_), u(u_ + lev(c0 + base_, H, e, L_), lev_bytes(m, H, L_)),
+          a(a_ + lev(c0 + base_, H, e, L_), lev_bytes(m, H, L_)), h(h_ + lev(c0 + base_, H, e, L_), lev_bytes(m, H, L_)),
+          // the rows before a token: of the sequence, or (for its first three) carried
+          past(k_ + ((c0 + (base_ > 3 ? base_ - 3 : 0)) * H + e) * DK,
+               ps_.bytes(m + (base_ > 3 ? 3 : base_), H, DK, ES)),
+          hist(k_hist + chain * 3 * DK, base_ == 0 ? 3 * DK * ES : 0), w(conv_w + (int64_t)e * DK * 4, DK * 4 * ES),
+          base(base_), L(L_)
+    {
     }
-    for (int l0 = 0; LEV > 0 && l0 < L - 1; l0 += LV) {
-        if (l0 > 0)
-            fetch(l0);
+    __device__ static int64_t lev(int64_t at, int H, int e, int L) { return (at * H + e) * (L - 1) * DK; }
+    __device__ static int64_t lev_bytes(int m, int H, int L) { return Pass<T, DK, DV>::bytes(m, H, (L - 1) * DK, ES); }
+
+    raw4 ar[LV], ur[LV], hr[LV], pr[3], hi[3], wr[4], kr;
+    typename X::raw1 br;
+    __device__ void fetch_levels(uint32_t t, uint32_t ch, int l0)
+    {
+        const uint32_t at = (t * ps.krow * (L - 1) + ch) * ES;
 #pragma unroll
-        for (int l = 0; l < LEV; ++l) {
-            if (l0 + l < L - 1) {
-                const f32x4_t av = F::f32(ar[l]), uv = F::f32(ur[l]), hv = F::f32(hr[l]);
+        for (int l = 0; l < LEV; ++l) {                  // slots beyond the last re-read it; h's last is not used
+            const int sl = l0 + l < L - 2 ? l0 + l : L - 2, hl = sl < L - 3 ? sl : L > 2 ? L - 3 : 0;
+            ar[l] = X::template load4<kOnce>(a, at + sl * DK * ES);
+            ur[l] = X::template load4<kOnce>(u, at + sl * DK * ES);
+            hr[l] = X::template load4<kOnce>(h, at + hl * DK * ES);
+        }
+    }
+    __device__ void fetch(uint32_t t, uint32_t ch)
+    {
+        fetch_levels(t, ch, 0);
+        kr = X::load4(ps.k, (t * ps.krow + ch) * ES);
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    acc[x] += av[x] * r[x] * uv[x];
-                if (l0 + l < L - 2) {
+        for (int d = 1; d <= 3; ++d) {
+            const uint32_t row = base > 3 ? t + 3 - d : t + base - d;    // wraps past the end below the first row
+            pr[d - 1] = X::load4(past, (row * ps.krow + ch) * ES);
+            hi[d - 1] = X::load4(hist, ((t + 3 - d) * DK + ch) * ES);    // empty but for the first pass
+        }
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        r[x] = GELU ? r[x] - av[x] * gelu_as(hv[x] * r[x]) : r[x] * (1.f - av[x] * hv[x]);
+        for (int x = 0; x < 4; ++x)
+            wr[x] = X::load4(w, (ch + x) * 4 * ES);
+        br = X::load1(ps.b, t * ps.grow * ES);
+    }
+    __device__ f32x4_t form(uint32_t t, uint32_t ch, f32x4_t& kt)
+    {
+        kt = X::f32(kr);
+        f32x4_t x[3], r, acc;
+#pragma unroll
+        for (int d = 0; d < 3; ++d)                      // one of the two is zero
+            x[d] = X::f32(pr[d] | hi[d]);
+        const float bt = X::f32(br);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const f32x4_t wc = X::f32(wr[c]);
+            r[c] = wc[3] * kt[c] + wc[2] * x[0][c] + wc[1] * x[1][c] + wc[0] * x[2][c];
+            acc[c] = bt * kt[c];
+        }
+        for (int l0 = 0; LEV > 0 && l0 < L - 1; l0 += LV) {
+            if (l0 > 0)
+                fetch_levels(t, ch, l0);
+#pragma unroll
+            for (int l = 0; l < LEV; ++l) {
+                if (l0 + l < L - 1) {
+                    const f32x4_t av = X::f32(ar[l]), uv = X::f32(ur[l]), hv = X::f32(hr[l]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        acc[c] += av[c] * r[c] * uv[c];
+                    if (l0 + l < L - 2) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            r[c] = GELU ? r[c] - av[c] * gelu_as(hv[c] * r[c]) : r[c] * (1.f - av[c] * hv[c]);
+                    }
                 }
             }
         }
+        E32::store4(ps.kw, (t * ps.krow + ch) * 4, acc);
+        return acc;
     }
-    *reinterpret_cast<f32x4_t*>(kw_out + row * DK + ch) = acc;
-}
+};
 
-template <typename T, int DK, int DV, int LEV>
-__global__ __launch_bounds__(2 * DV, 2) void draft_kernel(
+template <typename T, int DK, int DV, int LEV, bool GELU>
+__global__ __launch_bounds__(2 * DV, sizeof(T) == 2 ? 4 : 3) void draft_kernel(
     const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ u,
     const T* __restrict__ a, const T* __restrict__ h, const T* __restrict__ g, const T* __restrict__ b,
-    const T* __restrict__ conv_w, const int32_t* __restrict__ cu, int H, int L, bool gelu,
-    const float* __restrict__ S, const T* __restrict__ k_hist, T* __restrict__ o, float* kw_out,
-    float* __restrict__ p_out)
+    const T* __restrict__ conv_w, const int32_t* __restrict__ cu, int H, int L,
+    const float* __restrict__ S, const T* __restrict__ k_hist, T* __restrict__ o, float* kw_out, float* p_out)
 {
-    using F = Four<T>;
-    constexpr int NTH = 2 * DV, W = NTH / 64, RT = DK / 16, LD = DK + 4, CG = DK / 4;
+    typedef Elems<T> X;
+    constexpr int NTH = 2 * DV, W = NTH / 64, RT = DK / 16, LD = DK + 4, CG = DK / 4, ES = sizeof(T);
     constexpr int ITEMS = (kBlock * CG + NTH - 1) / NTH;         // pieces of the tile rows a thread stages
     // rows 0..7 Q, 8..15 K, 16..23 KW: rows 8.. are [K; KW], row (i + 8) % 16 of [K; Q] is i
     __shared__ __align__(16) float sRows[24 * LD];
     __shared__ __align__(16) float sM[W][2][16][20];     // a wavefront's [A B; C E], then W
+    __shared__ int sWild[W];
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, kq = lane >> 4, j = lane & 15;
     const int64_t chain = blockIdx.x;
     const int e = (int)(chain % H);
     const int64_t n = chain / H;
+
+    // the state is streamed: tiles R .. R + PRE - 1 in flight, rows 16 R + 4 kq + r, two
+    // columns a lane; the first EARLY are on their way before the sequence is looked up
+    // (fewer where the write key's loads need the registers)
+    constexpr int PRE = RT < 4 ? RT : 4, EARLY = LEV > 3 ? PRE / 2 : PRE;
+    const Span state(S + chain * DK * DV, DK * DV * 4);
+    E32::raw2 s[PRE][4];
+    auto fetch_state = [&](int R, int tid) {
+        const int at = ((tid & 48) / 4 * DV + 32 * (tid >> 6) + 2 * (tid & 15)) * 4;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            s[R % PRE][r] = E32::template load2<kOnce>(state, at + (16 * R + r) * DV * 4);
+    };
+#pragma unroll
+    for (int R = 0; R < EARLY; ++R)
+        fetch_state(R, threadIdx.x);
+
     const int64_t c0 = cu[n];
     const int len = cu[n + 1] - (int)c0;
     if (len <= 0)
         return;
-    const int col = 32 * wave + 2 * j;
-    const uint32_t vrow = (uint32_t)H * DV;
-
-    if (gelu && LEV > 0) {
-        for (int i = tid; i < len * CG; i += NTH)
-            form_write_key<T, DK, LEV, true>(k, u, a, h, b, conv_w, k_hist, chain, c0, H, e, L, i / CG, (i % CG) * 4,
-                                             kw_out);
-    } else {
-        for (int i = tid; i < len * CG; i += NTH)
-            form_write_key<T, DK, LEV, false>(k, u, a, h, b, conv_w, k_hist, chain, c0, H, e, L, i / CG, (i % CG) * 4,
-                                              kw_out);
-    }
-    __syncthreads();                                     // the write keys of the chain are in kw_out
-
-    // what a pass reads of its tokens: the rows of K, Q and KW on their way into LDS
-    // (zeros past its tokens), its gates (lane t holds token t's) and its value rows:
-    // register r holds row 4 (kq % 2) + r, token 2 r + kq % 2, in both halves
-    typename F::raw kr[ITEMS], qr[ITEMS];
-    f32x4_t wr[ITEMS], vv[2];
-    float gl, bl;
-    auto fetch = [&](int base, int m) {
-#pragma unroll
-        for (int x = 0; x < ITEMS; ++x) {
-            const int i = tid + x * NTH, t = i / CG;
-            kr[x] = qr[x] = typename F::raw{};
-            wr[x] = f32x4_t{};
-            if (t < m) {
-                const int64_t at = ((c0 + base + t) * H + e) * DK + (i % CG) * 4;
-                kr[x] = load4(k + at);
-                qr[x] = load4(q + at);
-                wr[x] = *reinterpret_cast<const f32x4_t*>(kw_out + at);
-            }
-        }
-        gl = 1.f;
-        bl = 0.f;
-        if ((lane & 7) < m) {
-            const int64_t at = (c0 + base + (lane & 7)) * H + e;
-            gl = to_f32(g[at]);
-            bl = to_f32(b[at]);
-        }
-        vv[0] = vv[1] = f32x4_t{};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int t = 2 * r + (kq & 1);
-            if (t < m) {
-                const f32x2_t x = F::load2(v + ((c0 + base + t) * H + e) * DV + col);
-                vv[0][r] = x[0];
-                vv[1][r] = x[1];
-            }
-        }
-    };
-    // the state is streamed: tiles R .. R + PRE - 1 in flight, each row 16 R + 4 kq + r in two columns
-    constexpr int PRE = RT < 4 ? RT : 4;
-    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<float*>(S + chain * DK * DV), 0, DK * DV * 4, 0x00020000);
-    const int sat = (4 * kq * DV + col) * 4;
-    f32x2_t s[PRE][4];
-    auto fetch_state = [&](int R) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            s[R % PRE][r] = __builtin_bit_cast(
-                f32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rs, sat, (16 * R + r) * DV * 4, 2));
-    };
 
     // A token's zeros in the triangular matrices would turn an infinity or a NaN
     // of a later token into a NaN of its own, so a sequence with a value beyond
     // kLarge (whose products may overflow too) takes its tokens one at a time.
-    int cap = kBlock, m;
+    int cap = kBlock, m = 0;
+    bool staged = false;                                 // whether the write keys are formed
     for (int base = 0; base < len; base += m) {
+        const int tid = opaque(threadIdx.x), lane = tid & 63, kq = lane >> 4, j = lane & 15;
+        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = 32 * wave + 2 * j;
         m = len - base < cap ? len - base : cap;
         const int steps = (m + 1) >> 1;
-        if (base > 0)
-            __syncthreads();                             // the pass before is done with the LDS
-        fetch(base, m);
+        const Pass<T, DK, DV> ps(k, q, v, g, b, kw_out, p_out, c0 + base, m, H, e);
+        if (staged)
+            __syncthreads();                             // the pass before is done with the LDS; kw_out is written
+        // gates (lane t holds token t's) and value rows: register r holds row 4 (kq % 2) + r, token
+        // 2 r + kq % 2, in both halves
+        const typename X::raw1 gr = X::load1(ps.g, (lane & 7) * ps.grow * ES),
+                               br = X::load1(ps.b, (lane & 7) * ps.grow * ES);
+        typename X::raw2 vr[4];
 #pragma unroll
-        for (int R = 0; R < PRE; ++R)                    // behind the rows: in flight while those are worked on
-            fetch_state(R);
-        bool tame = fabsf(gl) <= kLarge && fabsf(bl) <= kLarge && tame4(vv[0]) && tame4(vv[1]);
+        for (int r = 0; r < 4; ++r)
+            vr[r] = X::load2(ps.v, ((2 * r + (kq & 1)) * ps.vrow + col) * ES);
+        bool tame = true;
 #pragma unroll
         for (int x = 0; x < ITEMS; ++x) {
-            const int i = tid + x * NTH, t = i / CG, to = slot_of(t) * LD + (i % CG) * 4;
+            const int i = tid + x * NTH, t = i / CG, ch = (i % CG) * 4;
+            f32x4_t kt, wt;
+            const typename X::raw4 qr = X::load4(ps.q, (t * ps.krow + ch) * ES);
+            if (!staged) {
+                WriteKey<T, DK, DV, LEV, GELU> key(ps, k, u, a, h, conv_w, k_hist, chain, c0, base, m, H, e, L);
+                key.fetch(t, ch);
+                wt = key.form(t, ch, kt);
+            } else {
+                kt = X::f32(X::load4(ps.k, (t * ps.krow + ch) * ES));
+                wt = E32::f32(E32::load4(ps.kw, (t * ps.krow + ch) * 4));
+            }
             if (kBlock * CG >= NTH || t < kBlock) {
-                const f32x4_t kt = F::f32(kr[x]);
-                *reinterpret_cast<f32x4_t*>(sRows + to) = F::f32(qr[x]);
-                *reinterpret_cast<f32x4_t*>(sRows + 8 * LD + to) = kt;
-                *reinterpret_cast<f32x4_t*>(sRows + 16 * LD + to) = wr[x];
-                tame = tame && tame4(kt) && tame4(wr[x]);
+                float* to = sRows + slot_of(t) * LD + ch;
+                *reinterpret_cast<f32x4_t*>(to) = X::f32(qr);
+                *reinterpret_cast<f32x4_t*>(to + 8 * LD) = kt;
+                *reinterpret_cast<f32x4_t*>(to + 16 * LD) = wt;
+                tame = tame && tame4(kt) && tame4(wt);
             }
         }
-        if (__syncthreads_or(!tame) && cap > 1) {
+        if (!staged) {
+            for (int at = kBlock; at < len; at += kBlock) {
+                const int mt = len - at < kBlock ? len - at : kBlock;
+                const Pass<T, DK, DV> later(k, q, v, g, b, kw_out, p_out, c0 + at, mt, H, e);
+                WriteKey<T, DK, DV, LEV, GELU> key(later, k, u, a, h, conv_w, k_hist, chain, c0, at, mt, H, e, L);
+#pragma unroll 1
+                for (int i = opaque(tid); i < kBlock * CG; i += NTH) {
+                    f32x4_t kt;
+                    key.fetch(i / CG, (i % CG) * 4);
+                    key.form(i / CG, (i % CG) * 4, kt);
+                }
+            }
+        }
+#pragma unroll
+        for (int R = 0; R < PRE; ++R)
+            if (staged || R >= EARLY)
+                fetch_state(R, tid);
+        staged = true;
+        const float gl = (lane & 7) < m ? X::f32(gr) : 1.f, bl = X::f32(br);
+        f32x4_t vv[2];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const f32x2_t x = X::f32(vr[r]);
+            vv[0][r] = x[0];
+            vv[1][r] = x[1];
+        }
+        tame = tame && fabsf(gl) <= kLarge && fabsf(bl) <= kLarge && tame4(vv[0]) && tame4(vv[1]);
+        if (lane == 0)
+            sWild[wave] = 0;
+        if (__ballot(!tame) && lane == 0)
+            sWild[wave] = 1;
+        lds_barrier();                                   // the state's loads stay in flight
+        int wild = 0;
+#pragma unroll
+        for (int x = 0; x < W; ++x)
+            wild |= sWild[x];
+        if (wild && cap > 1) {
             cap = 1;
             m = 0;                                       // the same tokens again
             continue;
@@ -439,9 +515,9 @@ __global__ __launch_bounds__(2 * DV, 2) void draft_kernel(
             for (int r = 0; r < 4; ++r)
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
-                    x[c] = mfma4(fa[r], s[R % PRE][r][c], x[c]);
+                    x[c] = mfma4(fa[r], __uint_as_float(s[R % PRE][r][c]), x[c]);
             if (R + PRE < RT)
-                fetch_state(R + PRE);
+                fetch_state(R + PRE, tid);
             if (R % 4 == 3)
                 __builtin_amdgcn_sched_barrier(0);
         }
@@ -455,31 +531,25 @@ __global__ __launch_bounds__(2 * DV, 2) void draft_kernel(
             float between = 1.f;                         // the product of the gates from here to this pass
             for (int cb = (base - 1) / kBlock * kBlock; cb >= 0; cb -= kBlock) {
                 const int mc = base - cb < kBlock ? base - cb : kBlock;
-                float gc = 1.f, bc = 0.f;
-                if ((lane & 7) < mc) {
-                    const int64_t at = (c0 + cb + (lane & 7)) * H + e;
-                    gc = to_f32(g[at]);
-                    bc = to_f32(b[at]);
-                }
-                f32x4_t xy[2] = {}, d = {};
+                const int lane = opaque(threadIdx.x) & 63, kq = lane >> 4, j = lane & 15;
+                const float* pa = sRows + ((j + 8) & 15) * LD + 4 * kq;
+                const Pass<T, DK, DV> pc(k, q, v, g, b, kw_out, p_out, c0 + cb, mc, H, e);
+                const float gc = (lane & 7) < mc ? X::f32(X::load1(pc.g, (lane & 7) * pc.grow * ES)) : 1.f;
+                const float bc = X::f32(X::load1(pc.b, (lane & 7) * pc.grow * ES));
+                f32x4_t xy[2], d = {};
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int t = 2 * r + (kq & 1);
-                    if (t < mc) {                        // p: what this lane has stored itself
-                        const int64_t at = ((c0 + cb + t) * H + e) * DV + col;
-                        const f32x2_t y = kq < 2 ? *reinterpret_cast<const f32x2_t*>(p_out + at) : F::load2(v + at);
-                        xy[0][r] = y[0];
-                        xy[1][r] = y[1];
-                    }
+                for (int r = 0; r < 4; ++r) {            // p: what this lane has stored itself
+                    const uint32_t at = (2 * r + (kq & 1)) * pc.vrow + col;
+                    const f32x2_t y = kq < 2 ? E32::f32(E32::load2(pc.p, at * 4)) : X::f32(X::load2(pc.v, at * ES));
+                    xy[0][r] = y[0];
+                    xy[1][r] = y[1];
                 }
-                const int tc = token_of(j & 7);
-                const int64_t row = ((c0 + cb + (tc < mc ? tc : 0)) * H + e) * DK + 4 * kq;
+                const uint32_t row = token_of(j & 7) * pc.krow + 4 * kq;
 #pragma unroll
                 for (int R = 0; R < RT; ++R) {
                     const f32x4_t fa = *reinterpret_cast<const f32x4_t*>(pa + 16 * R);
-                    f32x4_t fb = {};
-                    if (tc < mc)
-                        fb = j < 8 ? F::f32(load4(k + row + 16 * R)) : load4(kw_out + row + 16 * R);
+                    const f32x4_t fb = j < 8 ? X::f32(X::load4(pc.k, (row + 16 * R) * ES))
+                                             : E32::f32(E32::load4(pc.kw, (row + 16 * R) * 4));
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         d = mfma4(fa[r], fb[r], d);
@@ -520,17 +590,14 @@ __global__ __launch_bounds__(2 * DV, 2) void draft_kernel(
                 if (r < steps)
                     y[c] = mfma4(fw[r], x[c][r], y[c]);
         }
+        const Span out(o + ((c0 + base) * H + e) * DV, ps.bytes(m, H, DV, ES));
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int t = 2 * r + (kq & 1);
-            if (t < m) {
-                const int64_t row = ((c0 + base) * H + e) * DV;
-                const uint32_t at = t * vrow + col;
-                if (kq < 2)
-                    *at_offset<f32x2_t>(p_out + row, at * 4) = f32x2_t{y[0][r], y[1][r]};
-                else
-                    F::store2(at_offset<T>(o + row, at * (uint32_t)sizeof(T)), y[0][r], y[1][r]);
-            }
+            const uint32_t at = (2 * r + (kq & 1)) * ps.vrow + col;
+            if (kq < 2)
+                E32::store2(ps.p, at * 4, y[0][r], y[1][r]);
+            else
+                X::store2(out, at * ES, y[0][r], y[1][r]);
         }
     }
 }
@@ -538,14 +605,14 @@ __global__ __launch_bounds__(2 * DV, 2) void draft_kernel(
 // S_out and hist_out may be S and hist: a thread has read what it overwrites.
 // blockIdx.y is a band of ROWS state rows.
 template <typename T, int DK, int DV, int ROWS>
-__global__ __launch_bounds__(2 * DV) void commit_kernel(
+__global__ __launch_bounds__(2 * DV, 4) void commit_kernel(
     const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ g, const T* __restrict__ b,
     const int32_t* __restrict__ cu, const int32_t* __restrict__ n_accept, int H,
     const float* __restrict__ kw, const float* __restrict__ p, const float* S, const T* hist, float* S_out,
     T* hist_out)
 {
-    using F = Four<T>;
-    constexpr int NTH = 2 * DV, RT = ROWS / 16, LD = ROWS + 4, CG = ROWS / 4;
+    typedef Elems<T> X;
+    constexpr int NTH = 2 * DV, RT = ROWS / 16, LD = ROWS + 4, CG = ROWS / 4, ES = sizeof(T);
     __shared__ __align__(16) float sRows[16 * LD];       // rows of K, then of KW
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, kq = lane >> 4, j = lane & 15;
@@ -562,11 +629,13 @@ __global__ __launch_bounds__(2 * DV) void commit_kernel(
 
     f32x4_t s[RT][2];
     const int col = 32 * wave + 2 * j;
+    const Span from(S + (chain * DK + row0) * DV, ROWS * DV * 4), to(S_out + (chain * DK + row0) * DV, ROWS * DV * 4);
+    const uint32_t sat = (4 * kq * DV + col) * 4;
 #pragma unroll
     for (int R = 0; R < RT; ++R)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const f32x2_t x = state_load<DV>(S + (chain * DK + row0 + 16 * R + r) * DV, kq, col);
+            const f32x2_t x = E32::f32(E32::template load2<kOnce>(from, sat + (16 * R + r) * DV * 4));
             s[R][0][r] = x[0];
             s[R][1][r] = x[1];
         }
@@ -586,39 +655,26 @@ __global__ __launch_bounds__(2 * DV) void commit_kernel(
     for (int base = 0; base < len; base += kBlock) {
         const int m = len - base < kBlock ? len - base : kBlock;
         const int steps = (m + 1) >> 1;
+        const Pass<T, DK, DV> ps(k, k, v, g, b, const_cast<float*>(kw), const_cast<float*>(p), c0 + base, m, H, e);
         if (base > 0)
             __syncthreads();                             // the pass before is done with the LDS
         for (int i = tid; i < 2 * steps * CG; i += NTH) {
-            const int t = i / CG, ch = (i % CG) * 4, to = slot_of(t) * LD + ch;
-            f32x4_t kt = {}, wt = {};
-            if (t < m) {
-                const int64_t at = ((c0 + base + t) * H + e) * DK + row0 + ch;
-                kt = F::f32(load4(k + at));
-                wt = load4(kw + at);
-            }
-            *reinterpret_cast<f32x4_t*>(sRows + to) = kt;
-            *reinterpret_cast<f32x4_t*>(sRows + 8 * LD + to) = wt;
+            const int t = i / CG, ch = (i % CG) * 4;
+            const uint32_t at = t * ps.krow + row0 + ch;
+            float* row = sRows + slot_of(t) * LD + ch;
+            const f32x4_t kt = X::f32(X::load4(ps.k, at * ES)), wt = E32::f32(E32::load4(ps.kw, at * 4));
+            *reinterpret_cast<f32x4_t*>(row) = kt;
+            *reinterpret_cast<f32x4_t*>(row + 8 * LD) = wt;
         }
-        float gl = 1.f, bl = 0.f;
-        if ((lane & 7) < m) {
-            const int64_t at = (c0 + base + (lane & 7)) * H + e;
-            gl = to_f32(g[at]);
-            bl = to_f32(b[at]);
-        }
-        f32x4_t xy[2] = {};                              // p over v
+        const float gl = (lane & 7) < m ? X::f32(X::load1(ps.g, (lane & 7) * ps.grow * ES)) : 1.f;
+        const float bl = X::f32(X::load1(ps.b, (lane & 7) * ps.grow * ES));
+        f32x4_t xy[2];                                   // p over v
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int t = 2 * r + (kq & 1);
-            if (t < m) {
-                const int64_t at = ((c0 + base + t) * H + e) * DV + col;
-                f32x2_t x;
-                if (kq < 2)
-                    x = *reinterpret_cast<const f32x2_t*>(p + at);
-                else
-                    x = F::load2(v + at);
-                xy[0][r] = x[0];
-                xy[1][r] = x[1];
-            }
+            const uint32_t at = (2 * r + (kq & 1)) * ps.vrow + col;
+            const f32x2_t x = kq < 2 ? E32::f32(E32::load2(ps.p, at * 4)) : X::f32(X::load2(ps.v, at * ES));
+            xy[0][r] = x[0];
+            xy[1][r] = x[1];
         }
         __syncthreads();
         float f[4];
@@ -633,31 +689,36 @@ __global__ __launch_bounds__(2 * DV) void commit_kernel(
 #pragma unroll
     for (int R = 0; R < RT; ++R)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const f32x2_t x = {s[R][0][r], s[R][1][r]};
-            __builtin_nontemporal_store(
-                x, at_offset<f32x2_t>(S_out + (chain * DK + row0 + 16 * R + r) * DV, (uint32_t)(4 * kq * DV + col) * 4));
-        }
+        for (int r = 0; r < 4; ++r)
+            __builtin_amdgcn_raw_buffer_store_b64(
+                __builtin_bit_cast(u32x2_t, f32x2_t{s[R][0][r], s[R][1][r]}), to.r, sat + (16 * R + r) * DV * 4, 0, kOnce);
 }
 
-template <typename T, int DK, int DV, int LEV>
+template <typename T, int DK, int DV, int LEV, bool GELU>
 static hipError_t launch_draft_lev(const DraftArgs& p, hipStream_t stream)
 {
-    hipLaunchKernelGGL((draft_kernel<T, DK, DV, LEV>), dim3((unsigned)((int64_t)p.n_seqs * p.heads)), dim3(2 * DV), 0,
+    hipLaunchKernelGGL((draft_kernel<T, DK, DV, LEV, GELU>), dim3((unsigned)((int64_t)p.n_seqs * p.heads)), dim3(2 * DV), 0,
                        stream, (const T*)p.q, (const T*)p.k, (const T*)p.v, (const T*)p.u, (const T*)p.a,
                        (const T*)p.h, (const T*)p.g, (const T*)p.b, (const T*)p.conv_w, p.cu_seqlens, p.heads,
-                       p.L, p.gelu, p.S, (const T*)p.k_hist, (T*)p.o, p.kw, p.p);
+                       p.L, p.S, (const T*)p.k_hist, (T*)p.o, p.kw, p.p);
     return hipGetLastError();
 }
 
-// Levels loaded at a time: all of them up to L = 4 and up to L = 8, seven at a time
-// beyond.
+// Levels loaded at a time: all of them up to L = 4 and (bf16) up to L = 8, seven at a
+// time beyond; fp32 takes three at a time, whose loads fill as many registers.  The
+// two chains are the same up to L = 2.
 template <typename T, int DK, int DV>
 static hipError_t launch_draft_t(const DraftArgs& p, hipStream_t stream)
 {
     if (p.L == 1)
-        return launch_draft_lev<T, DK, DV, 0>(p, stream);
-    return p.L <= 4 ? launch_draft_lev<T, DK, DV, 3>(p, stream) : launch_draft_lev<T, DK, DV, 7>(p, stream);
+        return launch_draft_lev<T, DK, DV, 0, false>(p, stream);
+    const bool gelu = p.gelu && p.L > 2;
+    if constexpr (sizeof(T) == 2) {
+        if (p.L > 4)
+            return gelu ? launch_draft_lev<T, DK, DV, 7, true>(p, stream)
+                        : launch_draft_lev<T, DK, DV, 7, false>(p, stream);
+    }
+    return gelu ? launch_draft_lev<T, DK, DV, 3, true>(p, stream) : launch_draft_lev<T, DK, DV, 3, false>(p, stream);
 }
 
 template <typename T, int DK, int DV>

@@ -33,6 +33,15 @@ bool verify_dims_ok(const prism_verify_dims* d)
 // one grid dimension holds the workgroups
 bool grid_ok(int64_t blocks) { return blocks <= INT32_MAX; }
 
+// The kernels of drafted tokens reach 8 tokens and the three rows before them from one
+// base with 32-bit offsets.
+bool draft_shape_ok(const prism_dims* d, int64_t levels)
+{
+    const int64_t row = d->dk * levels > d->dv ? d->dk * levels : d->dv;
+    return prism::decode_supported(d->dk, d->dv) && (int64_t)d->heads * row * 11 * 4 <= INT32_MAX &&
+           grid_ok((int64_t)d->n_seqs * d->heads);
+}
+
 }  // namespace
 
 extern "C" {
@@ -165,7 +174,7 @@ prism_status prism_decode_draft(const prism_dims* d, const void* q, const void* 
         return PRISM_EINVAL;
     if (L > 1 && (!tok_ok(d, u) || !tok_ok(d, a) || !tok_ok(d, h)))
         return PRISM_EINVAL;
-    if (!prism::decode_supported(d->dk, d->dv) || !grid_ok((int64_t)d->n_seqs * d->heads))
+    if (!draft_shape_ok(d, L > 1 ? L - 1 : 1))
         return PRISM_EUNSUPPORTED;
     if (d->total_tokens == 0)
         return PRISM_OK;
@@ -199,7 +208,7 @@ prism_status prism_decode_commit(const prism_dims* d, const void* k, const void*
         !ptr_ok(n_accept) || !tok_ok(d, kw) || !tok_ok(d, p_rec) || !ptr_ok(S) || !ptr_ok(k_hist) ||
         !ptr_ok(S_out) || !ptr_ok(k_hist_out))
         return PRISM_EINVAL;
-    if (!prism::decode_supported(d->dk, d->dv) || !grid_ok((int64_t)d->n_seqs * d->heads))
+    if (!draft_shape_ok(d, 1))
         return PRISM_EUNSUPPORTED;
     prism::DraftArgs p;
     p.bf16 = d->dtype == PRISM_BF16;

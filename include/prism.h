@@ -515,8 +515,8 @@ prism_status prism_norm_gate_bwd(const prism_norm_dims* d, const void* o, const 
  *   kw          out fp32 [T, H, dk]        the write keys, and
  *   p           out fp32 [T, H, dv]        S_{t-1}^T k_t: what prism_decode_commit needs
  *                                          to move the state by any number of the tokens
- * The write key is kept in fp32 (as in prism_decode_step).  dk, dv in {64, 128},
- * else PRISM_EUNSUPPORTED.  A token's outputs depend on the tokens up to it only,
+ * The write key is kept in fp32 (as in prism_decode_step).  dk, dv in {64, 128} and
+ * H * max(dk (L - 1), dv) <= 48,000,000, else PRISM_EUNSUPPORTED.  A token's outputs depend on the tokens up to it only,
  * also where later ones hold infinities or NaN.  No workspace.
  */
 prism_status prism_decode_draft(const prism_dims* d,
