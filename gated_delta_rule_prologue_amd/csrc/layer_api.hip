@@ -243,9 +243,10 @@ prism_status prism_verify_draft(const prism_verify_dims* d, const void* p, const
     const bool none = d->total_tokens == 0;              // then the per-token arrays may be null
     if (!(none ? aligned16(p) : ptr_ok(p)) || !opt_ok(q) || !(none ? aligned16(tokens) : ptr_ok(tokens)) ||
         !ptr_ok(cu_seqlens) || !(none ? aligned16(u_accept) : ptr_ok(u_accept)) || !ptr_ok(u_sample) ||
-        !ptr_ok(n_accept) || !ptr_ok(next_token) || !ptr_ok(workspace))
+        !ptr_ok(n_accept) || !ptr_ok(next_token))
         return PRISM_EINVAL;
-    if (workspace_bytes < prism_verify_workspace_bytes(d))
+    const size_t need = prism_verify_workspace_bytes(d);
+    if (need > 0 ? !ptr_ok(workspace) || workspace_bytes < need : !opt_ok(workspace))
         return PRISM_EINVAL;
     if (d->vocab > (1 << 28) || !grid_ok((int64_t)d->n_seqs * prism::verify_chunks(d->vocab)))
         return PRISM_EUNSUPPORTED;

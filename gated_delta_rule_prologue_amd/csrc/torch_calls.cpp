@@ -124,15 +124,17 @@ void apart(const char* a, const void* pa, const char* b, const void* pb)
         fail(PyExc_ValueError, std::string(a) + " and " + b + " are the same buffer");
 }
 
-// The caller's workspace, or one allocated on the current stream.
+// The caller's workspace, or one allocated on the current stream (none if none is needed).
 struct Scratch {
     at::Tensor t;
-    void* p;
-    size_t bytes;
+    void* p = nullptr;
+    size_t bytes = 0;
     Scratch(PyObject* o, size_t need, const at::Tensor& like)
     {
         if (o == Py_None) {
-            t = fresh({(int64_t)(need ? need : 1)}, at::kByte, like);
+            if (need == 0)
+                return;
+            t = fresh({(int64_t)need}, at::kByte, like);
         } else {
             t = tensor("workspace", o);
             if (t.device() != like.device())

@@ -555,7 +555,8 @@ typedef struct {
     int32_t dtype;         /* prism_dtype of p and q */
 } prism_verify_dims;
 
-/* Bytes of device workspace prism_verify_draft needs; 0 for invalid dims. */
+/* Bytes of device workspace prism_verify_draft needs (0 for a small vocabulary: it is
+ * served in one launch, and the workspace may be NULL); 0 for invalid dims. */
 size_t prism_verify_workspace_bytes(const prism_verify_dims* d);
 
 /*

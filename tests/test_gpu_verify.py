@@ -52,7 +52,8 @@ def both(m, use_q=True):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("use_q", [True, False])
-@pytest.mark.parametrize("V", [1, 2, 5, 8, 255, 1000, 4095, 4096, 4097, 8200, 50001])
+@pytest.mark.parametrize("V", [1, 2, 5, 8, 255, 1000, 1023, 1025, 4095, 4096, 4097, 8200, 32768, 32769, 36857, 36860, 36864,
+                               50001])
 def test_vocabularies(dtype, use_q, V):
     m = make([5, 1, 0, 3, 6, 2, 9, 4], V, dtype, seed=V)
     kept, nxt = both(m, use_q)

@@ -134,7 +134,7 @@ def test_verify_refuses(B):
     f = B.lib().prism_verify_draft
     names = ["p", "q", "tokens", "cu", "u_accept", "u_sample", "n_accept", "next", "ws"]
 
-    def call(d=(4, 12, 1000, 0), nb=1 << 30, **over):
+    def call(d=(4, 12, 100000, 0), nb=1 << 30, **over):
         a = {n: FAKE for n in names}
         a.update(over)
         return f(ctypes.byref(B.VerifyDims(*d)), *(a[n] for n in names), nb, None)
@@ -144,11 +144,14 @@ def test_verify_refuses(B):
             assert call(**{n: None}) == B.PRISM_EINVAL, n
         assert call(**{n: FAKE + 4}) == B.PRISM_EINVAL, n
     assert call(nb=16) == B.PRISM_EINVAL
-    for d in ((0, 12, 1000, 0), (4, -1, 1000, 0), (4, 12, 0, 0), (4, 12, 1000, 2)):
+    for d in ((0, 12, 100000, 0), (4, -1, 100000, 0), (4, 12, 0, 0), (4, 12, 100000, 2)):
         assert call(d) == B.PRISM_EINVAL, d
         assert B.verify_workspace_bytes(B.VerifyDims(*d)) == 0
     assert call((1, 1, (1 << 28) + 1, 0)) == B.PRISM_EUNSUPPORTED
-    assert B.verify_workspace_bytes(B.VerifyDims(3, 9, 4097, 0)) == 256
+    # two fp64 sums per 4096 entries (and up to 7 for the row's offset) beyond 32,768 entries
+    assert B.verify_workspace_bytes(B.VerifyDims(3, 9, 32768, 0)) == 0
+    assert B.verify_workspace_bytes(B.VerifyDims(3, 9, 32769, 0)) == 3 * 9 * 16 // 256 * 256 + 256
+    assert B.verify_workspace_bytes(B.VerifyDims(64, 99, 128000, 1)) == 64 * 32 * 16
 
 
 def test_binding_refuses_before_calling(B):
