@@ -43,6 +43,14 @@ __device__ __forceinline__ void lds_barrier()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// A value whose uses stay where they are: what derives from it is computed anew in each
+// pass of a loop instead of being kept in registers around it.
+__device__ __forceinline__ int opaque(int x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // GELU(x) = x Phi(x) = x (1 + erf(x / sqrt 2)) / 2, with erf from the rational
 // approximation of Abramowitz & Stegun, Handbook of Mathematical Functions,
 // formula 7.1.26 (after Hastings): for z >= 0,

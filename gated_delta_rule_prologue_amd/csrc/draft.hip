@@ -63,14 +63,6 @@ __device__ __forceinline__ f32x4_t mfma4(float a, float b, f32x4_t c)
     return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
-// A value whose uses stay where they are: what derives from it is computed anew in each
-// pass of a loop instead of being kept in registers around it.
-__device__ __forceinline__ int opaque(int x)
-{
-    asm volatile("" : "+v"(x));
-    return x;
-}
-
 // row of a token within its half of a tile, and back
 __device__ __forceinline__ int slot_of(int t) { return 4 * (t & 1) + (t >> 1); }
 __device__ __forceinline__ int token_of(int s) { return 2 * (s & 3) + (s >> 2); }

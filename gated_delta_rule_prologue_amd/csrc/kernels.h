@@ -176,7 +176,7 @@ struct NormResidualArgs {
     float* ws;                      // norm_residual_bwd_blocks() partial rows of dw (and dscale)
 };
 constexpr int kNormMaxWidth = 8192, kNormGateMaxWidth = 1024;
-constexpr int kNormBwdBlocks = 1024;             // workgroups of a backward, at most
+constexpr int kNormBwdBlocks = 512;              // workgroups of a backward, at most
 int norm_residual_bwd_blocks(int64_t rows, int width);
 hipError_t launch_norm_residual(const NormResidualArgs& p, hipStream_t stream);
 hipError_t launch_norm_residual_bwd(const NormResidualArgs& p, hipStream_t stream);

@@ -32,19 +32,21 @@ __global__ __launch_bounds__(S::THREADS) void norm_residual_kernel(
     typename S::elem* n_out)
 {
     __shared__ float red[2 * S::THREADS / 64];
-    const int lane = threadIdx.x % S::LANES, group = threadIdx.x / S::LANES;
+    const int64_t first = (int64_t)blockIdx.x * S::GROUPS + threadIdx.x / S::LANES;
+    const S sh(threadIdx.x % S::LANES, width);
     float wv[S::E], sv[S::E];
-    S::load_f32(w, lane, width, wv);
+    sh.load_weight(w, wv);
     if (scale)
-        S::load_f32(scale, lane, width, sv);
+        sh.load_weight(scale, sv);
     const float inv = 1.f / (float)width;
     const int64_t step = (int64_t)gridDim.x * S::GROUPS;
     int phase = 0;
-    for (int64_t i = (int64_t)blockIdx.x * S::GROUPS + group; i < n_rows; i += step) {
+    for (int64_t i = first; i < n_rows; i += step) {
+        const int64_t at = i * width, room = (n_rows - i) * width;
         typename S::Raw xr, yr;
-        S::load(x + i * width, lane, width, xr);
+        sh.load(x + at, room, xr);
         if (y)
-            S::load(y + i * width, lane, width, yr);
+            sh.load(y + at, room, yr);
         float r[S::E];
         S::unpack(xr, r);
         if (y) {
@@ -62,11 +64,11 @@ __global__ __launch_bounds__(S::THREADS) void norm_residual_kernel(
         phase ^= 1;
         const float rstd = rsqrtf(ss[0] * inv + eps);
         if (r_out)
-            S::store(r_out + i * width, lane, width, r);
+            sh.store(r_out + at, r);
 #pragma unroll
         for (int c = 0; c < S::E; ++c)
             r[c] *= rstd * wv[c];
-        S::store(n_out + i * width, lane, width, r);
+        sh.store(n_out + at, r);
     }
 }
 
@@ -78,25 +80,27 @@ __global__ __launch_bounds__(S::THREADS) void norm_residual_bwd_kernel(
 {
     __shared__ float red[2 * 2 * S::THREADS / 64];
     extern __shared__ float buf[];
-    const int lane = threadIdx.x % S::LANES, group = threadIdx.x / S::LANES;
+    const int64_t first = (int64_t)blockIdx.x * S::GROUPS + threadIdx.x / S::LANES;
+    const S sh(threadIdx.x % S::LANES, width);
     float wv[S::E], sv[S::E], aw[S::E], as[S::E];
-    S::load_f32(w, lane, width, wv);
+    sh.load_weight(w, wv);
     if (scale)
-        S::load_f32(scale, lane, width, sv);
+        sh.load_weight(scale, sv);
 #pragma unroll
     for (int c = 0; c < S::E; ++c)
         aw[c] = as[c] = 0.f;
     const float inv = 1.f / (float)width;
     const int64_t step = (int64_t)gridDim.x * S::GROUPS;
     int phase = 0;
-    for (int64_t i = (int64_t)blockIdx.x * S::GROUPS + group; i < n_rows; i += step) {
+    for (int64_t i = first; i < n_rows; i += step) {
+        const int64_t at = i * width, room = (n_rows - i) * width;
         typename S::Raw rr, dnr, drr, yr;
-        S::load(r + i * width, lane, width, rr);
-        S::load(dn + i * width, lane, width, dnr);
+        sh.load(r + at, room, rr);
+        sh.load(dn + at, room, dnr);
         if (dr)
-            S::load(dr + i * width, lane, width, drr);
+            sh.load(dr + at, room, drr);
         if (want_scale)
-            S::load(y + i * width, lane, width, yr);
+            sh.load(y + at, room, yr);
         float rv[S::E], dv[S::E];
         S::unpack(rr, rv);
         S::unpack(dnr, dv);
@@ -129,20 +133,20 @@ __global__ __launch_bounds__(S::THREADS) void norm_residual_bwd_kernel(
             for (int c = 0; c < S::E; ++c)
                 as[c] += t[c] * dv[c];
         }
-        S::store(dx + i * width, lane, width, t);
+        sh.store(dx + at, t);
         if (dy) {
             if (scale)
 #pragma unroll
                 for (int c = 0; c < S::E; ++c)
                     t[c] *= sv[c];
-            S::store(dy + i * width, lane, width, t);
+            sh.store(dy + at, t);
         }
     }
     const int cols = want_scale ? 2 * width : width;
     float* out = part + (int64_t)blockIdx.x * cols;
-    rows::store_partial<S>(aw, buf, lane, group, width, out);
+    rows::store_partial(sh, aw, buf, out);
     if (want_scale)
-        rows::store_partial<S>(as, buf, lane, group, width, out + width);
+        rows::store_partial(sh, as, buf, out + width);
 }
 
 namespace rows {
@@ -185,20 +189,23 @@ hipError_t launch_sum_partials(const float* part, int nb, int cols, int split, f
 
 }  // namespace rows
 
+// Two workgroups a compute unit, and half as many of the wide rows' twice as large ones:
+// more leave more partials to add, fewer leave memory idle (16,384 rows of 768, bf16: 256,
+// 512, 768, 1024 workgroups 40.3, 36.7, 38.7, 40.5 us; 4096 rows of 8192: 95.6, 107,
+// 123, 137 us).
 int norm_residual_bwd_blocks(int64_t n_rows, int width)
 {
-    (void)width;
-    return (int)(n_rows < 1 ? 1 : n_rows < kNormBwdBlocks ? n_rows : kNormBwdBlocks);
+    const int64_t cap = width > 4096 ? kNormBwdBlocks / 2 : kNormBwdBlocks;
+    return (int)(n_rows < 1 ? 1 : n_rows < cap ? n_rows : cap);
 }
 
 template <typename T> static hipError_t launch_fwd(const NormResidualArgs& p, hipStream_t stream)
 {
     if (p.rows == 0)
         return hipSuccess;
-    return rows::with_shape<T>(p.width, [&](auto shape) -> hipError_t {
-        typedef decltype(shape) S;
-        const int64_t want = (p.rows + S::GROUPS - 1) / S::GROUPS;
-        const int64_t cap = 2048 * 256 / S::THREADS;
+    return rows::with_shape<T>(p.width, [&](auto tag) -> hipError_t {
+        typedef typename decltype(tag)::type S;
+        const int64_t want = (p.rows + S::GROUPS - 1) / S::GROUPS, cap = 2048 * 256 / S::THREADS;
         hipLaunchKernelGGL((norm_residual_kernel<S>), dim3((unsigned)(want < cap ? want : cap)),
                            dim3(S::THREADS), 0, stream, (const T*)p.x, (const T*)p.y, (const T*)p.scale,
                            (const T*)p.w, p.eps, p.rows, p.width, (T*)p.r, (T*)p.n);
@@ -210,8 +217,8 @@ template <typename T> static hipError_t launch_bwd_t(const NormResidualArgs& p, 
 {
     const int nb = norm_residual_bwd_blocks(p.rows, p.width);
     const bool ws = p.dscale != nullptr;
-    const hipError_t e = rows::with_shape<T>(p.width, [&](auto shape) -> hipError_t {
-        typedef decltype(shape) S;
+    const hipError_t e = rows::with_shape<T>(p.width, [&](auto tag) -> hipError_t {
+        typedef typename decltype(tag)::type S;
         hipLaunchKernelGGL((norm_residual_bwd_kernel<S>), dim3(nb), dim3(S::THREADS),
                            S::PARTIAL_LDS, stream, (const T*)p.r, (const T*)p.y,
                            (const T*)p.scale, (const T*)p.w, p.eps, (const T*)p.dn, (const T*)p.dr, p.rows,

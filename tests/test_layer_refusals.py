@@ -20,14 +20,15 @@ def nd(B, rows=8, heads=1, width=64, dtype=1):
 
 
 def test_norm_workspace_bytes(B):
-    """Per workgroup (one a row or token up to 1024 in all) an fp32 partial: dw and dscale
+    """Per workgroup (one a row or token up to 512 in all, 256 of rows beyond 4096) an fp32 partial: dw and dscale
     of width, or dw of heads rows."""
     up = lambda x: (x + 255) // 256 * 256
     b = lambda *a: B.norm_workspace_bytes(B.NormDims(*a))
     assert b(8, 1, 64, 1) == up(2 * 8 * 64 * 4)
-    assert b(100000, 1, 768, 1) == up(2 * 1024 * 768 * 4)
+    assert b(100000, 1, 768, 1) == up(2 * 512 * 768 * 4)
     assert b(0, 1, 64, 0) == up(2 * 64 * 4)
-    assert b(6000, 6, 128, 1) == up(2 * 1024 * 128 * 4)         # the residual norm's is larger
+    assert b(100000, 1, 8000, 0) == 2 * 256 * 8000 * 4
+    assert b(6000, 6, 128, 1) == up(2 * 512 * 128 * 4)         # the residual norm's is larger
     assert b(3 * 5000, 5000, 8, 1) == up(5000 * 8 * 4)
     for bad in ((-1, 1, 64, 1), (8, 0, 64, 1), (8, 3, 64, 1), (8, 1, 0, 1), (8, 1, 64, 2),
                 (1 << 61, 1, 64, 1), (1 << 30, 1 << 30, 64, 1)):
