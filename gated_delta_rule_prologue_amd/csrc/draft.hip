@@ -134,6 +134,7 @@ template <> struct Elems<float> {
 };
 typedef Elems<float> E32;
 constexpr int kOnce = 2;                         // nontemporal: read once per call
+constexpr uint32_t kOutside = 0xffffff00u;       // an offset past any span
 
 __device__ __forceinline__ bool tame4(f32x4_t x)
 {
@@ -235,11 +236,11 @@ template <typename T, int DK, int DV, int LEV, bool GELU> struct WriteKey {
     {
         const uint32_t at = (t * ps.krow * (L - 1) + ch) * ES;
 #pragma unroll
-        for (int l = 0; l < LEV; ++l) {                  // slots beyond the last re-read it; h's last is not used
-            const int sl = l0 + l < L - 2 ? l0 + l : L - 2, hl = sl < L - 3 ? sl : L > 2 ? L - 3 : 0;
-            ar[l] = X::template load4<kOnce>(a, at + sl * DK * ES);
-            ur[l] = X::template load4<kOnce>(u, at + sl * DK * ES);
-            hr[l] = X::template load4<kOnce>(h, at + hl * DK * ES);
+        for (int l = 0; l < LEV; ++l) {                  // past the last level: zeros, which change no finite sum
+            const uint32_t la = l0 + l < L - 1 ? at + (l0 + l) * DK * ES : kOutside;
+            ar[l] = X::template load4<kOnce>(a, la);
+            ur[l] = X::template load4<kOnce>(u, la);
+            hr[l] = X::template load4<kOnce>(h, l0 + l < L - 2 ? la : kOutside);
         }
     }
     __device__ void fetch(uint32_t t, uint32_t ch)
@@ -275,17 +276,13 @@ template <typename T, int DK, int DV, int LEV, bool GELU> struct WriteKey {
             if (l0 > 0)
                 fetch_levels(t, ch, l0);
 #pragma unroll
-            for (int l = 0; l < LEV; ++l) {
-                if (l0 + l < L - 1) {
-                    const f32x4_t av = X::f32(ar[l]), uv = X::f32(ur[l]), hv = X::f32(hr[l]);
+            for (int l = 0; l < LEV; ++l) {              // r (1 - a h) = r - (a r) h
+                const f32x4_t av = X::f32(ar[l]), uv = X::f32(ur[l]), hv = X::f32(hr[l]);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        acc[c] += av[c] * r[c] * uv[c];
-                    if (l0 + l < L - 2) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            r[c] = GELU ? r[c] - av[c] * gelu_as(hv[c] * r[c]) : r[c] * (1.f - av[c] * hv[c]);
-                    }
+                for (int c = 0; c < 4; ++c) {
+                    const float ar_c = av[c] * r[c];
+                    acc[c] += ar_c * uv[c];
+                    r[c] -= GELU ? av[c] * gelu_as(hv[c] * r[c]) : ar_c * hv[c];
                 }
             }
         }
@@ -294,12 +291,29 @@ template <typename T, int DK, int DV, int LEV, bool GELU> struct WriteKey {
     }
 };
 
+// The draft kernel's arguments, read from the kernel's argument segment where they are used:
+// held in scalar registers over the pass loop (30 of them beside the buffer resources)
+// they were spilled into vector lanes.
+template <typename T> struct DraftPointers {
+    const T *q, *k, *v, *u, *a, *h, *g, *b, *conv_w;
+    const int32_t* cu;
+    const float* S;
+    const T* k_hist;
+    T* o;
+    float *kw, *p;
+    int H, L;
+};
+template <typename T> using Segment = const __attribute__((address_space(4))) DraftPointers<T>*;
+
+// The same address, whose loads are not moved to where it came from.
+template <typename P> __device__ __forceinline__ P again(P p)
+{
+    asm volatile("" : "+s"(p));
+    return p;
+}
+
 template <typename T, int DK, int DV, int LEV, bool GELU>
-__global__ __launch_bounds__(2 * DV, sizeof(T) == 2 ? 4 : 3) void draft_kernel(
-    const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ u,
-    const T* __restrict__ a, const T* __restrict__ h, const T* __restrict__ g, const T* __restrict__ b,
-    const T* __restrict__ conv_w, const int32_t* __restrict__ cu, int H, int L,
-    const float* __restrict__ S, const T* __restrict__ k_hist, T* __restrict__ o, float* kw_out, float* p_out)
+__global__ __launch_bounds__(2 * DV, sizeof(T) == 2 ? 4 : 3) void draft_kernel(DraftPointers<T>)
 {
     typedef Elems<T> X;
     constexpr int NTH = 2 * DV, W = NTH / 64, RT = DK / 16, LD = DK + 4, CG = DK / 4, ES = sizeof(T);
@@ -309,6 +323,8 @@ __global__ __launch_bounds__(2 * DV, sizeof(T) == 2 ? 4 : 3) void draft_kernel(
     __shared__ __align__(16) float sM[W][2][16][20];     // a wavefront's [A B; C E], then W
     __shared__ int sWild[W];
 
+    const Segment<T> in = (Segment<T>)__builtin_amdgcn_kernarg_segment_ptr();
+    const int H = in->H, L = in->L;
     const int64_t chain = blockIdx.x;
     const int e = (int)(chain % H);
     const int64_t n = chain / H;
@@ -317,7 +333,7 @@ __global__ __launch_bounds__(2 * DV, sizeof(T) == 2 ? 4 : 3) void draft_kernel(
     // columns a lane; the first EARLY are on their way before the sequence is looked up
     // (fewer where the write key's loads need the registers)
     constexpr int PRE = RT < 4 ? RT : 4, EARLY = LEV > 3 ? PRE / 2 : PRE;
-    const Span state(S + chain * DK * DV, DK * DV * 4);
+    const Span state(in->S + chain * DK * DV, DK * DV * 4);
     E32::raw2 s[PRE][4];
     auto fetch_state = [&](int R, int tid) {
         const int at = ((tid & 48) / 4 * DV + 32 * (tid >> 6) + 2 * (tid & 15)) * 4;
@@ -329,8 +345,8 @@ __global__ __launch_bounds__(2 * DV, sizeof(T) == 2 ? 4 : 3) void draft_kernel(
     for (int R = 0; R < EARLY; ++R)
         fetch_state(R, threadIdx.x);
 
-    const int64_t c0 = cu[n];
-    const int len = cu[n + 1] - (int)c0;
+    const int64_t c0 = in->cu[n];
+    const int len = in->cu[n + 1] - (int)c0;
     if (len <= 0)
         return;
 
@@ -344,7 +360,8 @@ __global__ __launch_bounds__(2 * DV, sizeof(T) == 2 ? 4 : 3) void draft_kernel(
         const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = 32 * wave + 2 * j;
         m = len - base < cap ? len - base : cap;
         const int steps = (m + 1) >> 1;
-        const Pass<T, DK, DV> ps(k, q, v, g, b, kw_out, p_out, c0 + base, m, H, e);
+        const Segment<T> ap = again(in);
+        const Pass<T, DK, DV> ps(ap->k, ap->q, ap->v, ap->g, ap->b, ap->kw, ap->p, c0 + base, m, H, e);
         if (staged)
             __syncthreads();                             // the pass before is done with the LDS; kw_out is written
         // gates (lane t holds token t's) and value rows: register r holds row 4 (kq % 2) + r, token
@@ -362,7 +379,8 @@ __global__ __launch_bounds__(2 * DV, sizeof(T) == 2 ? 4 : 3) void draft_kernel(
             f32x4_t kt, wt;
             const typename X::raw4 qr = X::load4(ps.q, (t * ps.krow + ch) * ES);
             if (!staged) {
-                WriteKey<T, DK, DV, LEV, GELU> key(ps, k, u, a, h, conv_w, k_hist, chain, c0, base, m, H, e, L);
+                WriteKey<T, DK, DV, LEV, GELU> key(ps, ap->k, ap->u, ap->a, ap->h, ap->conv_w, ap->k_hist, chain, c0,
+                                                     base, m, H, e, L);
                 key.fetch(t, ch);
                 wt = key.form(t, ch, kt);
             } else {
@@ -380,8 +398,10 @@ __global__ __launch_bounds__(2 * DV, sizeof(T) == 2 ? 4 : 3) void draft_kernel(
         if (!staged) {
             for (int at = kBlock; at < len; at += kBlock) {
                 const int mt = len - at < kBlock ? len - at : kBlock;
-                const Pass<T, DK, DV> later(k, q, v, g, b, kw_out, p_out, c0 + at, mt, H, e);
-                WriteKey<T, DK, DV, LEV, GELU> key(later, k, u, a, h, conv_w, k_hist, chain, c0, at, mt, H, e, L);
+                const Segment<T> al = again(in);
+                const Pass<T, DK, DV> later(al->k, al->q, al->v, al->g, al->b, al->kw, al->p, c0 + at, mt, H, e);
+                WriteKey<T, DK, DV, LEV, GELU> key(later, al->k, al->u, al->a, al->h, al->conv_w, al->k_hist, chain, c0,
+                                                   at, mt, H, e, L);
 #pragma unroll 1
                 for (int i = opaque(tid); i < kBlock * CG; i += NTH) {
                     f32x4_t kt;
@@ -525,7 +545,8 @@ __global__ __launch_bounds__(2 * DV, sizeof(T) == 2 ? 4 : 3) void draft_kernel(
                 const int mc = base - cb < kBlock ? base - cb : kBlock;
                 const int lane = opaque(threadIdx.x) & 63, kq = lane >> 4, j = lane & 15;
                 const float* pa = sRows + ((j + 8) & 15) * LD + 4 * kq;
-                const Pass<T, DK, DV> pc(k, q, v, g, b, kw_out, p_out, c0 + cb, mc, H, e);
+                const Segment<T> ac = again(in);
+                const Pass<T, DK, DV> pc(ac->k, ac->q, ac->v, ac->g, ac->b, ac->kw, ac->p, c0 + cb, mc, H, e);
                 const float gc = (lane & 7) < mc ? X::f32(X::load1(pc.g, (lane & 7) * pc.grow * ES)) : 1.f;
                 const float bc = X::f32(X::load1(pc.b, (lane & 7) * pc.grow * ES));
                 f32x4_t xy[2], d = {};
@@ -582,7 +603,7 @@ __global__ __launch_bounds__(2 * DV, sizeof(T) == 2 ? 4 : 3) void draft_kernel(
                 if (r < steps)
                     y[c] = mfma4(fw[r], x[c][r], y[c]);
         }
-        const Span out(o + ((c0 + base) * H + e) * DV, ps.bytes(m, H, DV, ES));
+        const Span out(again(in)->o + ((c0 + base) * H + e) * DV, ps.bytes(m, H, DV, ES));
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const uint32_t at = (2 * r + (kq & 1)) * ps.vrow + col;
@@ -689,10 +710,11 @@ __global__ __launch_bounds__(2 * DV, 4) void commit_kernel(
 template <typename T, int DK, int DV, int LEV, bool GELU>
 static hipError_t launch_draft_lev(const DraftArgs& p, hipStream_t stream)
 {
-    hipLaunchKernelGGL((draft_kernel<T, DK, DV, LEV, GELU>), dim3((unsigned)((int64_t)p.n_seqs * p.heads)), dim3(2 * DV), 0,
-                       stream, (const T*)p.q, (const T*)p.k, (const T*)p.v, (const T*)p.u, (const T*)p.a,
-                       (const T*)p.h, (const T*)p.g, (const T*)p.b, (const T*)p.conv_w, p.cu_seqlens, p.heads,
-                       p.L, p.S, (const T*)p.k_hist, (T*)p.o, p.kw, p.p);
+    const DraftPointers<T> in = {(const T*)p.q, (const T*)p.k, (const T*)p.v, (const T*)p.u, (const T*)p.a,
+                                 (const T*)p.h, (const T*)p.g, (const T*)p.b, (const T*)p.conv_w, p.cu_seqlens,
+                                 p.S, (const T*)p.k_hist, (T*)p.o, p.kw, p.p, p.heads, p.L};
+    hipLaunchKernelGGL((draft_kernel<T, DK, DV, LEV, GELU>), dim3((unsigned)((int64_t)p.n_seqs * p.heads)), dim3(2 * DV),
+                       0, stream, in);
     return hipGetLastError();
 }
 
