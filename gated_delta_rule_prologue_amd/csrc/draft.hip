@@ -313,7 +313,7 @@ template <typename P> __device__ __forceinline__ P again(P p)
 }
 
 template <typename T, int DK, int DV, int LEV, bool GELU>
-__global__ __launch_bounds__(2 * DV, sizeof(T) == 2 ? 4 : 3) void draft_kernel(DraftPointers<T>)
+__global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
 {
     typedef Elems<T> X;
     constexpr int NTH = 2 * DV, W = NTH / 64, RT = DK / 16, LD = DK + 4, CG = DK / 4, ES = sizeof(T);
