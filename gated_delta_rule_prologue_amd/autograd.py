@@ -21,6 +21,7 @@ The norms around the operator, differentiable in every tensor they take:
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding
 
@@ -96,6 +97,7 @@ class NormResidualFunction(torch.autograd.Function):
         return n, r
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dn, dr=None):
         r, w, y, scale = ctx.saved_tensors
         if dn is None and dr is None:
@@ -127,6 +129,7 @@ class NormGateFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         o, z, w = ctx.saved_tensors
         grads = binding.norm_gate_bwd(o, z, w, _upstream(dy, o), eps=ctx.eps, gate=ctx.gate)

@@ -319,6 +319,20 @@ def test_autograd(dtype):
         assert a.dtype == dt and torch.equal(a, ref[name].to(dt)), name
 
 
+def test_gradients_of_gradients_are_refused():
+    """The backward passes have no gradients of their own: asking for them is an error, never a
+    gradient without its second part."""
+    import torch
+    from gated_delta_rule_prologue_amd import autograd as A
+    gen = torch.Generator().manual_seed(9)
+    x, y, o = (rand(gen, (6, 2, 64), torch.float32).requires_grad_(True) for _ in range(3))
+    w = rand(gen, 64, torch.float32, 0.2, 1.0).requires_grad_(True)
+    for out in (A.norm_residual(x, w, y=y)[0], A.norm_gate(o, x, w)):
+        g, = torch.autograd.grad(out.square().sum(), [x], create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            g.square().sum().backward()
+
+
 def test_binding_refusals_on_device():
     import torch
     from gated_delta_rule_prologue_amd import binding as B
