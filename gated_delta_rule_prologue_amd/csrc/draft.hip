@@ -50,6 +50,7 @@
 // (16 to 32 matrix instructions) instead of waiting for another one's.
 #include "common.h"
 #include "kernels.h"
+#include "prism.h"
 
 namespace prism {
 
@@ -102,6 +103,7 @@ template <> struct Elems<uint16_t> {
     }
     __device__ static f32x2_t f32(raw2 x) { return {__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)}; }
     __device__ static float f32(raw1 x) { return bf16_to_f32(x); }
+    __device__ static void store1(uint16_t* to, float x) { *to = f32_to_bf16(x); }
     __device__ static void store2(const Span& b, uint32_t at, float x, float y)
     {
         __builtin_amdgcn_raw_buffer_store_b32(pack_bf16x2(x, y), b.r, at, 0, 0);
@@ -123,6 +125,7 @@ template <> struct Elems<float> {
     __device__ static f32x4_t f32(raw4 x) { return __builtin_bit_cast(f32x4_t, x); }
     __device__ static f32x2_t f32(raw2 x) { return __builtin_bit_cast(f32x2_t, x); }
     __device__ static float f32(raw1 x) { return __uint_as_float(x); }
+    __device__ static void store1(float* to, float x) { *to = x; }
     __device__ static void store2(const Span& b, uint32_t at, float x, float y)
     {
         __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, f32x2_t{x, y}), b.r, at, 0, 0);
@@ -140,6 +143,10 @@ __device__ __forceinline__ bool tame4(f32x4_t x)
 {
     return fabsf(x[0]) <= kLarge && fabsf(x[1]) <= kLarge && fabsf(x[2]) <= kLarge && fabsf(x[3]) <= kLarge;
 }
+
+// LDS that only this wavefront uses: what its lanes have stored is there for its loads
+// (no instruction: the LDS serves a wavefront in order).
+__device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local"); }
 
 __device__ __forceinline__ float lane_value(float x, int lane)
 {
@@ -349,6 +356,15 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
     const int len = in->cu[n + 1] - (int)c0;
     if (len <= 0)
         return;
+    if (len > PRISM_MAX_DRAFT) {                         // not served
+        for (int64_t i = threadIdx.x; i < (int64_t)len * DK; i += NTH)
+            in->kw[((c0 + i / DK) * H + e) * DK + i % DK] = __builtin_nanf("");
+        for (int64_t i = threadIdx.x; i < (int64_t)len * DV; i += NTH) {
+            in->p[((c0 + i / DV) * H + e) * DV + i % DV] = __builtin_nanf("");
+            X::store1(in->o + ((c0 + i / DV) * H + e) * DV + i % DV, __builtin_nanf(""));
+        }
+        return;
+    }
 
     // A token's zeros in the triangular matrices would turn an infinity or a NaN
     // of a later token into a NaN of its own, so a sequence with a value beyond
@@ -487,6 +503,7 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
                 x = rho[r] * (j < 8 ? own : 1.f) * d0[r];
             M0[4 * kq + r][j] = x;
         }
+        wave_fence();
         // T by substitution, column tj' = slot lane % 8 on every group of 8 lanes; row lane / 8 of
         // T and of -C T is kept
         {
@@ -517,6 +534,7 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
             M1[8 + gr][c] = ct;
             M1[8 + gr][8 + c] = gr == c ? 1.f : 0.f;
         }
+        wave_fence();
         __builtin_amdgcn_sched_barrier(0);
         // [K; Q] S
         f32x4_t x[2] = {};
@@ -577,7 +595,9 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
                     xy[1][r] *= f[r];
                     M0[4 * kq + r][j] = d[r];
                 }
+                wave_fence();
                 const f32x4_t fd = *reinterpret_cast<const f32x4_t*>(&M0[j][4 * kq]);
+                wave_fence();
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
 #pragma unroll

@@ -4,6 +4,8 @@
 // checks and launches on the caller's stream.
 #include <math.h>
 
+#include <initializer_list>
+
 #include "api_checks.h"
 #include "kernels.h"
 #include "prism.h"
@@ -29,6 +31,34 @@ bool verify_dims_ok(const prism_verify_dims* d)
     return d && d->n_seqs >= 1 && d->total_tokens >= 0 && d->vocab >= 1 &&
            (d->dtype == PRISM_F32 || d->dtype == PRISM_BF16);
 }
+
+// The bytes of an array that a call reads or writes; `either`: its whole buffer may be
+// input and output at once.
+struct Region {
+    const void* p;
+    int64_t bytes;
+    bool either = false;
+};
+
+// No output shares a byte with an input or another output, but for buffers that may be both.
+bool apart(std::initializer_list<Region> outs, std::initializer_list<Region> ins)
+{
+    auto meet = [](const Region& x, const Region& y) {
+        return x.p && y.p && x.bytes > 0 && y.bytes > 0 && (uintptr_t)x.p < (uintptr_t)y.p + y.bytes &&
+               (uintptr_t)y.p < (uintptr_t)x.p + x.bytes;
+    };
+    for (const Region* o = outs.begin(); o != outs.end(); ++o) {
+        for (const Region* x = o + 1; x != outs.end(); ++x)
+            if (meet(*o, *x))
+                return false;
+        for (const Region& x : ins)
+            if (meet(*o, x) && !(o->either && x.either && o->p == x.p && o->bytes == x.bytes))
+                return false;
+    }
+    return true;
+}
+
+int64_t size_of(int dtype) { return dtype == PRISM_BF16 ? 2 : 4; }
 
 // one grid dimension holds the workgroups
 bool grid_ok(int64_t blocks) { return blocks <= INT32_MAX; }
@@ -68,6 +98,9 @@ prism_status prism_norm_residual(const prism_norm_dims* d, const void* x, const 
         return PRISM_EINVAL;
     if (d->width > prism::kNormMaxWidth)
         return PRISM_EUNSUPPORTED;
+    const int64_t all = d->rows * d->width * size_of(d->dtype), row = d->width * size_of(d->dtype);
+    if (!apart({{r, all, true}, {n, all, true}}, {{x, all, true}, {y, all, true}, {scale, row}, {w, row}}))
+        return PRISM_EINVAL;
     prism::NormResidualArgs p = {};
     p.bf16 = d->dtype == PRISM_BF16;
     p.rows = d->rows;
@@ -93,7 +126,12 @@ prism_status prism_norm_residual_bwd(const prism_norm_dims* d, const void* r, co
         return PRISM_EINVAL;
     if (d->width > prism::kNormMaxWidth)
         return PRISM_EUNSUPPORTED;
-    if (workspace_bytes < prism_norm_workspace_bytes(d))
+    const int64_t need = prism_norm_workspace_bytes(d);
+    if (workspace_bytes < (size_t)need)
+        return PRISM_EINVAL;
+    const int64_t all = d->rows * d->width * size_of(d->dtype), row = d->width * size_of(d->dtype);
+    if (!apart({{dx, all, true}, {dy, all, true}, {dw, d->width * 4}, {dscale, d->width * 4}, {workspace, need}},
+               {{r, all, true}, {y, all, true}, {dn, all, true}, {dr, all, true}, {scale, row}, {w, row}}))
         return PRISM_EINVAL;
     prism::NormResidualArgs p = {};
     p.bf16 = d->dtype == PRISM_BF16;
@@ -119,6 +157,9 @@ prism_status prism_norm_gate(const prism_norm_dims* d, const void* o, const void
         return PRISM_EINVAL;
     if (d->width > prism::kNormGateMaxWidth)
         return PRISM_EUNSUPPORTED;
+    const int64_t es = size_of(d->dtype), all = d->rows * d->width * es;
+    if (!apart({{y, all, true}}, {{o, all, true}, {z, all, true}, {w, (int64_t)d->heads * d->width * es}}))
+        return PRISM_EINVAL;
     prism::NormGateArgs p = {};
     p.bf16 = d->dtype == PRISM_BF16;
     p.gate = gate;
@@ -142,7 +183,12 @@ prism_status prism_norm_gate_bwd(const prism_norm_dims* d, const void* o, const 
         return PRISM_EINVAL;
     if (d->width > prism::kNormGateMaxWidth)
         return PRISM_EUNSUPPORTED;
-    if (workspace_bytes < prism_norm_workspace_bytes(d))
+    const int64_t need = prism_norm_workspace_bytes(d);
+    if (workspace_bytes < (size_t)need)
+        return PRISM_EINVAL;
+    const int64_t es = size_of(d->dtype), all = d->rows * d->width * es, nw = (int64_t)d->heads * d->width;
+    if (!apart({{d_o, all, true}, {dz, all, true}, {dw, nw * 4}, {workspace, need}},
+               {{o, all, true}, {z, all, true}, {dy, all, true}, {w, nw * es}}))
         return PRISM_EINVAL;
     prism::NormGateArgs p = {};
     p.bf16 = d->dtype == PRISM_BF16;
@@ -174,8 +220,15 @@ prism_status prism_decode_draft(const prism_dims* d, const void* q, const void* 
         return PRISM_EINVAL;
     if (L > 1 && (!tok_ok(d, u) || !tok_ok(d, a) || !tok_ok(d, h)))
         return PRISM_EINVAL;
-    if (!draft_shape_ok(d, L > 1 ? L - 1 : 1))
+    if (!draft_shape_ok(d, L > 1 ? L - 1 : 1) || d->total_tokens > (int64_t)d->n_seqs * PRISM_MAX_DRAFT)
         return PRISM_EUNSUPPORTED;
+    const int64_t es = size_of(d->dtype), th = (int64_t)d->total_tokens * d->heads, nh = (int64_t)d->n_seqs * d->heads;
+    const int64_t lev = L > 1 ? th * (L - 1) * d->dk * es : 0;
+    if (!apart({{o, th * d->dv * es}, {kw, th * d->dk * 4}, {p_rec, th * d->dv * 4}},
+               {{q, th * d->dk * es}, {k, th * d->dk * es}, {v, th * d->dv * es}, {u, lev}, {a, lev}, {h, lev},
+                {g, th * es}, {b, th * es}, {conv_w, (int64_t)d->heads * d->dk * 4 * es},
+                {cu_seqlens, ((int64_t)d->n_seqs + 1) * 4}, {S, nh * d->dk * d->dv * 4}, {k_hist, nh * 3 * d->dk * es}}))
+        return PRISM_EINVAL;
     if (d->total_tokens == 0)
         return PRISM_OK;
     prism::DraftArgs p;
@@ -210,6 +263,13 @@ prism_status prism_decode_commit(const prism_dims* d, const void* k, const void*
         return PRISM_EINVAL;
     if (!draft_shape_ok(d, 1))
         return PRISM_EUNSUPPORTED;
+    const int64_t es = size_of(d->dtype), th = (int64_t)d->total_tokens * d->heads, nh = (int64_t)d->n_seqs * d->heads;
+    const int64_t state = nh * d->dk * d->dv * 4, hist = nh * 3 * d->dk * es;
+    if (!apart({{S_out, state, true}, {k_hist_out, hist, true}},
+               {{S, state, true}, {k_hist, hist, true}, {k, th * d->dk * es}, {v, th * d->dv * es}, {g, th * es},
+                {b, th * es}, {kw, th * d->dk * 4}, {p_rec, th * d->dv * 4}, {n_accept, (int64_t)d->n_seqs * 4},
+                {cu_seqlens, ((int64_t)d->n_seqs + 1) * 4}}))
+        return PRISM_EINVAL;
     prism::DraftArgs p;
     p.bf16 = d->dtype == PRISM_BF16;
     p.n_seqs = d->n_seqs;
@@ -250,6 +310,11 @@ prism_status prism_verify_draft(const prism_verify_dims* d, const void* p, const
         return PRISM_EINVAL;
     if (d->vocab > (1 << 28) || !grid_ok((int64_t)d->n_seqs * prism::verify_chunks(d->vocab)))
         return PRISM_EUNSUPPORTED;
+    const int64_t rows = (int64_t)d->total_tokens * d->vocab * size_of(d->dtype), each = (int64_t)d->n_seqs * 4;
+    if (!apart({{n_accept, each}, {next_token, each}, {workspace, (int64_t)need}},
+               {{p, rows}, {q, rows}, {tokens, (int64_t)d->total_tokens * 4}, {u_accept, (int64_t)d->total_tokens * 4},
+                {u_sample, each}, {cu_seqlens, each + 4}}))
+        return PRISM_EINVAL;
     prism::VerifyArgs a;
     a.bf16 = d->dtype == PRISM_BF16;
     a.n_seqs = d->n_seqs;

@@ -205,6 +205,14 @@ long whole(PyObject* o)
     return x;
 }
 
+bool truth(PyObject* o)
+{
+    const int x = PyObject_IsTrue(o);
+    if (x < 0)
+        throw Raised{};
+    return x;
+}
+
 prism_norm_dims rows_of(const at::Tensor& x)
 {
     if (x.dim() < 1 || x.size(-1) < 1)
@@ -290,7 +298,7 @@ PyObject* norm_residual_bwd(PyObject* const* a)
     at::Tensor dx = fresh(r.sizes(), dt, r), dw = fresh(vec, at::kFloat, r), dy, ds;
     if (scaled) {
         dy = fresh(r.sizes(), dt, r);
-        if (PyObject_IsTrue(a[8]))
+        if (truth(a[8]))
             ds = fresh(vec, at::kFloat, r);
     }
     const Scratch ws(a[7], prism_norm_workspace_bytes(&d), r);

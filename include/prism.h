@@ -414,6 +414,10 @@ prism_status prism_bwd_ckpt(const prism_dims* d,
  * operator alone; these entry points are the steps that a layer made of it
  * needs next to it.  The conventions above hold (dense row-major device
  * pointers, 16-byte aligned, asynchronous, all checks before any launch).
+ * An output (and the workspace) shares no byte with an input, another output or the
+ * workspace, but for the whole buffers that an entry point names as usable for
+ * both; PRISM_EINVAL otherwise.  Calls that may run at the same time, captured
+ * graphs too, need a workspace each.
  * ------------------------------------------------------------------------ */
 
 typedef struct {
@@ -499,14 +503,20 @@ prism_status prism_norm_gate_bwd(const prism_norm_dims* d, const void* o, const 
                                  void* d_o, void* dz, float* dw,
                                  void* workspace, size_t workspace_bytes, void* stream);
 
+/* Tokens of a sequence that prism_decode_draft takes, at most. */
+#define PRISM_MAX_DRAFT 1024
+
 /*
  * The operator over the drafted tokens of every sequence, from a carried state
  * that stays as it is: what prism_fwd_resume computes from S and k_hist, but
  * neither is moved, since it is not known yet how many of the tokens stay, and a
  * recurrent state cannot be rolled back.  Sequence n brings the packed tokens
  * cu_seqlens[n] .. cu_seqlens[n + 1] - 1 (in serving: the last token it has, then
- * the drafted ones; none is fine).  Meant for a few tokens a sequence; any
- * number is served, 16 at a time.
+ * the drafted ones; none is fine).  Meant for a few tokens a sequence: they are taken 8
+ * at a time, and every 8 read those before them again, so the time grows with the
+ * square of the number.  A sequence of more than PRISM_MAX_DRAFT tokens is not served:
+ * its o, kw and p are NaN (total_tokens > n_seqs * PRISM_MAX_DRAFT, where there must be
+ * one: PRISM_EUNSUPPORTED); prism_fwd_resume is the call for such.
  *
  *   q .. conv_w, cu_seqlens, L, residual   as in prism_fwd_resume
  *   S           fp32 [n_seqs, H, dk, dv]   state before the first token, read only
@@ -516,8 +526,9 @@ prism_status prism_norm_gate_bwd(const prism_norm_dims* d, const void* o, const 
  *   p           out fp32 [T, H, dv]        S_{t-1}^T k_t: what prism_decode_commit needs
  *                                          to move the state by any number of the tokens
  * The write key is kept in fp32 (as in prism_decode_step).  dk, dv in {64, 128} and
- * H * max(dk (L - 1), dv) <= 48,000,000, else PRISM_EUNSUPPORTED.  A token's outputs depend on the tokens up to it only,
- * also where later ones hold infinities or NaN.  No workspace.
+ * H * max(dk (L - 1), dv) <= 48,000,000, else PRISM_EUNSUPPORTED.  A token's outputs
+ * depend on the tokens up to it only, also where later ones hold infinities or NaN.
+ * No workspace.
  */
 prism_status prism_decode_draft(const prism_dims* d,
                                 const void* q, const void* k, const void* v,

@@ -199,6 +199,31 @@ def test_later_tokens_do_not_reach_earlier_ones(what, dtype):
     del clean
 
 
+def test_long_drafts():
+    """The longest sequence that is served (gates about 0.95: what a token leaves fades within
+    a few passes, so the bound is that of short ones), and one token more, whose outputs and
+    records are NaN while its neighbours' are not."""
+    import torch
+    lens = [3, 1024, 1025, 9]
+    d, cu, cu_t, S, hist = make(lens, H=1, dk=64, dv=128, L=3, seed=13)
+    o, kw, p = run(d, cu_t, 3, S, hist)
+    for x in (o, kw, p):
+        assert torch.isnan(x[cu[2]:cu[3]]).all()
+    keep = [n for n in range(len(lens)) if n != 2]
+    for n in keep:
+        at = slice(cu[n], cu[n + 1])
+        ref = R.draft({k: f64(v) if k == "conv_w" or v is None else f64(v[at]) for k, v in d.items()}, [0, lens[n]], 3,
+                      f64(S[n:n + 1]), f64(hist[n:n + 1]), "linear")
+        for name, got, want in zip(("o", "kw", "p"), (o, kw, p), ref):
+            near(f"{name} of {lens[n]} tokens", got[at], want)
+    S_out, h_out = commit(d, cu_t, [3, 1024, 0, 9], kw, p, S, hist, S_out=torch.empty_like(S),
+                          k_hist_out=torch.empty_like(hist))
+    assert torch.equal(S_out[2], S[2]) and torch.equal(h_out[2], hist[2])
+    rS, _ = R.commit(f64(d["k"]), f64(d["v"]), f64(d["g"]), f64(d["b"]), cu, [3, 1024, 0, 9], f64(kw).nan_to_num(),
+                     f64(p).nan_to_num(), f64(S), f64(hist))
+    near("S", S_out, rS, 8e-6)               # 17 roundings a pass of the state, that fade within 3 or 4 passes
+
+
 def test_rows_behind_the_last_token_stay():
     """Buffers longer than the packed tokens: the rows behind are not written."""
     import torch

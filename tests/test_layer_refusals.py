@@ -155,6 +155,83 @@ def test_verify_refuses(B):
     assert B.verify_workspace_bytes(B.VerifyDims(64, 99, 128000, 1)) == 64 * 32 * 16
 
 
+def far(count):
+    """Addresses that no two arrays of these sizes reach from one to the other."""
+    return [FAKE + (i + 1 << 32) for i in range(count)]
+
+
+def test_outputs_that_overlap_are_refused(B):
+    """An output on an input, another output or the workspace: refused wherever it begins, but for
+    whole buffers that may be both.  Every call here is refused (a call with nothing wrong would
+    launch)."""
+    L = B.lib()
+    row, t = 64 * 2, 8 * 64 * 2                              # bytes of a row and of a tensor
+
+    names = ["x", "y", "scale", "w", "r", "n"]
+    at = dict(zip(names, far(6)))
+
+    def norm(**over):
+        a = {**at, **over}
+        return L.prism_norm_residual(nd(B), a["x"], a["y"], a["scale"], a["w"], 1e-6, a["r"], a["n"], None)
+
+    for over in (dict(r=at["n"]), dict(r=at["x"] + row), dict(n=at["y"] + t - 16), dict(n=at["x"] - t + 16),
+                 dict(r=at["w"]), dict(n=at["scale"] - 16), dict(r=at["n"] + t - row)):
+        assert norm(**over) == B.PRISM_EINVAL, over
+
+    names = ["r", "y", "scale", "w", "dn", "dr", "dx", "dy", "dw", "ds", "ws"]
+    at = dict(zip(names, far(11)))
+    for over in (dict(dx=at["dy"]), dict(dx=at["dn"] + row), dict(dy=at["w"]), dict(dw=at["ds"]), dict(dw=at["w"]),
+                 dict(ds=at["r"]), dict(ws=at["dn"]), dict(ws=at["dx"] + row), dict(dw=at["ws"] + 256)):
+        a = {**at, **over}
+        assert L.prism_norm_residual_bwd(nd(B), a["r"], a["y"], a["scale"], a["w"], 1e-6, a["dn"], a["dr"], a["dx"],
+                                         a["dy"], a["dw"], a["ds"], a["ws"], 1 << 30, None) == B.PRISM_EINVAL, over
+
+    names = ["o", "z", "w", "dy", "do", "dz", "dw", "ws"]
+    at = dict(zip(names, far(8)))
+    for over in (dict(do=at["dz"]), dict(do=at["o"] + row), dict(dz=at["w"]), dict(dw=at["dy"]), dict(ws=at["do"])):
+        a = {**at, **over}
+        assert L.prism_norm_gate_bwd(nd(B, heads=2), a["o"], a["z"], a["w"], 1e-6, 0, a["dy"], a["do"], a["dz"], a["dw"],
+                                     a["ws"], 1 << 30, None) == B.PRISM_EINVAL, over
+    for over in (at["o"] + row, at["z"] - 16, at["w"]):
+        assert L.prism_norm_gate(nd(B), at["o"], at["z"], at["w"], 1e-6, 0, over, None) == B.PRISM_EINVAL
+
+    dims = ctypes.byref(B.make_dims(4, 12, 2, 64, 64, 0))
+    names = ["q", "k", "v", "u", "g", "b", "a", "h", "conv_w", "cu"]
+    outs = ["S", "hist", "o", "kw", "p"]
+    at = dict(zip(names + outs, far(15)))
+    for out in ("o", "kw", "p"):
+        for other in names + outs:
+            if other != out:
+                a = {**at, out: at[other]}
+                assert L.prism_decode_draft(dims, *(a[n] for n in names), 3, 0, *(a[n] for n in outs),
+                                            None) == B.PRISM_EINVAL, (out, other)
+
+    names = ["k", "v", "g", "b", "cu", "n_accept", "kw", "p", "S", "hist", "S_out", "hist_out"]
+    at = dict(zip(names, far(12)))
+    for out in ("S_out", "hist_out"):
+        for other in names:
+            if other != out:
+                same = other == out[:-4]                     # the whole buffer may be both, a part of it not
+                a = {**at, out: at[other] + (16 if same else 0)}
+                assert L.prism_decode_commit(dims, *(a[n] for n in names), None) == B.PRISM_EINVAL, (out, other)
+
+    names = ["p", "q", "tokens", "cu", "u_accept", "u_sample", "n_accept", "next", "ws"]
+    at = dict(zip(names, far(9)))
+    for out in ("n_accept", "next", "ws"):
+        for other in names:
+            if other != out:
+                a = {**at, out: at[other]}
+                assert L.prism_verify_draft(ctypes.byref(B.VerifyDims(4, 12, 100000, 0)), *(a[n] for n in names),
+                                            1 << 30, None) == B.PRISM_EINVAL, (out, other)
+
+
+def test_drafts_longer_than_served_are_refused(B):
+    f = B.lib().prism_decode_draft
+    at = far(15)
+    assert f(ctypes.byref(B.make_dims(3, 3 * 1024 + 1, 2, 64, 64, 1)), *at[:10], 3, 0, *at[10:],
+             None) == B.PRISM_EUNSUPPORTED
+
+
 def test_binding_refuses_before_calling(B):
     """What the binding refuses by itself: host tensors, and the arguments it looks at
     before any address."""
