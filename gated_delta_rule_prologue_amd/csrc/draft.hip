@@ -27,27 +27,45 @@
 // and 消除 Step 间串行; gist.science summary of arXiv 2602.10796, section 2.1
 // (S_t = S_{t-1} A_t + B_t: moving by any prefix is exact).
 //
-// Bound by HBM: the fp32 state is read once (and written once by the commit);
-// the products cost 4 M dk dv flops a chain, which run on the fp32 matrix
-// instructions (16x16x4) under the loads of other workgroups.
+// Bounds.  The least traffic is the fp32 state, read once (and written once by the
+// commit), and the tokens' rows; the products cost 4 M dk dv flops a chain and run on the
+// fp32 matrix instructions (16x16x4) under the loads of other workgroups.  The commit
+// keeps to that: 256 sequences x 6 heads, dk = dv = 128, 5 of 8 tokens kept at the mean,
+// 210 MB in 41 us, 5.1 TB/s.  The draft is bound by the instructions a wavefront issues
+// for the small matrices (about 1000 vector and 400 scalar ones a pass, whatever the
+// number of tokens) and, where there are few chains, by one pass's latency: the same
+// batch, 1 to 8 tokens, 131 MB in 32 us, 4.1 TB/s; 512 x 8 heads of 64 x 64 with
+// L = 8, 39 us for 8 tokens (4.9 TB/s) and 73 us for 9, whose second pass costs
+// as much as the first; 8 x 6 heads of 5 tokens, 8.5 us (a launch alone: 3.8).
+// Long sequences are walked all the same, with the square of the passes: 32 x 8
+// heads (64 x 64) take 7.4, 100, 1520 and 25,000 us for 8, 64, 256 and 1024 tokens.
 //
-// Layout.  One workgroup per chain, one wavefront per 32 value columns, the
-// state in registers: lane (kq, j) = (lane / 16, lane % 16) holds rows
-// 16 R + 4 kq + r and the columns 2 j, 2 j + 1 of its wavefront, so a row of
-// the tile is read in 128-byte pieces.  That is the accumulator layout of a
-// 16x16 tile and, register r taken as one 16x16x4 step whose contraction index
-// kq names row 4 kq + r, the second operand's too: S enters [K; Q] S and receives
-// [K; KW]^T [X; Y] with no exchange between lanes.  The first operand of step r
-// then wants channel 4 kq + r, so one 16-byte LDS read serves four steps.  The
-// same holds for [P; O], which comes out of one product and enters the next.
+// Layout.  One workgroup per chain, one wavefront per 32 value columns; of the
+// state, lane (kq, j) = (lane / 16, lane % 16) takes rows 16 R + 4 kq + r and the
+// columns 2 j, 2 j + 1 of its wavefront, so a row of the tile is read in 128-byte
+// pieces.  That is the accumulator layout of a 16x16 tile and, register r taken as one
+// 16x16x4 step whose contraction index kq names row 4 kq + r, the second operand's
+// too: S enters [K; Q] S and receives [K; KW]^T [X; Y] with no exchange between lanes.
+// The first operand of step r then wants channel 4 kq + r, so one 16-byte LDS read
+// serves four steps.  The same holds for [P; O], which comes out of one product and
+// enters the next.
+// The commit holds the state in registers (64 a lane at 128 x 128).  The draft streams
+// it through the products instead, four tiles in flight, and reads it again in each
+// pass, where the tokens of earlier passes enter by 16x16 products of the rows: with the
+// state kept in registers 256 x 6 heads took 44 us instead of 35 (fewer workgroups at
+// a time).
 // Eight tokens fill a 16-row tile with K over Q, and one 16x16 product of
-// [K; Q] with [K; KW] gives the dot products of all four triangular matrices.
+// [K; Q] with [K; KW] gives the dot products of all four triangular matrices (16 tokens a
+// pass, with a tile each for K and Q and barriers between the small matrices: 512 x 8
+// heads 77 us instead of 45).
 // Token t sits in row 4 (t % 2) + t / 2 of its half: step r of a contraction over
 // tokens covers tokens 2 r and 2 r + 1, so steps beyond the last token are left out.
 // The write keys are formed by the whole workgroup (one thread per token and
 // four channels, every load of it issued before the state's and before the first
 // wait); after one barrier each wavefront forms the small matrices for itself
 // (16 to 32 matrix instructions) instead of waiting for another one's.
+// kw and p stay in fp32, as in the single-token step, so that the commit loses nothing;
+// o is rounded once, from fp32.
 #include "common.h"
 #include "kernels.h"
 #include "prism.h"
@@ -755,14 +773,25 @@ static hipError_t launch_draft_t(const DraftArgs& p, hipStream_t stream)
     return gelu ? launch_draft_lev<T, DK, DV, 3, true>(p, stream) : launch_draft_lev<T, DK, DV, 3, false>(p, stream);
 }
 
-template <typename T, int DK, int DV>
-static hipError_t launch_commit_t(const DraftArgs& p, hipStream_t stream)
+template <typename T, int DK, int DV, int ROWS>
+static hipError_t launch_commit_rows(const DraftArgs& p, hipStream_t stream)
 {
-    hipLaunchKernelGGL((commit_kernel<T, DK, DV, DK>), dim3((unsigned)((int64_t)p.n_seqs * p.heads)),
+    hipLaunchKernelGGL((commit_kernel<T, DK, DV, ROWS>), dim3((unsigned)((int64_t)p.n_seqs * p.heads), DK / ROWS),
                        dim3(2 * DV), 0, stream, (const T*)p.k, (const T*)p.v, (const T*)p.g, (const T*)p.b,
                        p.cu_seqlens, p.n_accept, p.heads, p.kw, p.p, p.S, (const T*)p.k_hist, p.S_out,
                        (T*)p.k_hist_out);
     return hipGetLastError();
+}
+
+// A chain's rows are apart in the commit, so few chains are cut into bands of 32 rows that
+// run side by side: 48 chains of 128 x 128 take 4.6 instead of 7.0 us, 192 take 7.0
+// instead of 7.7; with 384 the two are equal (11.3 us), and 1536 take 44.5 instead of
+// 43.5, the tokens' rows of p and v being read by every band.
+template <typename T, int DK, int DV>
+static hipError_t launch_commit_t(const DraftArgs& p, hipStream_t stream)
+{
+    return (int64_t)p.n_seqs * p.heads <= 256 ? launch_commit_rows<T, DK, DV, 32>(p, stream)
+                                               : launch_commit_rows<T, DK, DV, DK>(p, stream);
 }
 
 template <typename T> static hipError_t launch_T(const DraftArgs& p, bool commit, hipStream_t s)

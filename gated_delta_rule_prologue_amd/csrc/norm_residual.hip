@@ -9,7 +9,10 @@
 // mean(e rh) = rstd mean(e r), so both row sums (r^2 and e r) are taken in one
 // pass over the row.
 //
-// Bound by HBM: every element is read and written once, at 6 to 14 operations.
+// Bound by HBM: every element is read and written once, at 6 to 14 operations.  Backward
+// of 16,384 rows of 768 in bf16 with scale: 151 MB in 32 us, 4.7 TB/s, of which the
+// second launch takes 4; 4,099 rows of 1,001 in fp32, forward, 11.5 us; a decode
+// step's 8 rows, 5.8 us, a launch and one read after another.
 // A row stays in registers between the sum and the scaling; w and s stay in
 // registers over all rows of a workgroup, and so do the column sums of the
 // backward, which leave one fp32 partial row per workgroup (no atomics: the

@@ -27,7 +27,8 @@
 // the chunk in which the sum passes the threshold and walks that one alone.  A small
 // row takes one workgroup and one launch.  The sums over lanes stay in registers (DPP
 // moves of both halves: through LDS exchanges one sequence of 32,000 entries took 12.2
-// instead of 8.0 us).
+// instead of 9.0 us).  64 sequences of 128,000 entries in fp32, p and q: 65.5 MB in 15 us,
+// 4.3 TB/s, of which the second launch takes 5.
 #include "common.h"
 #include "kernels.h"
 
