@@ -31,12 +31,13 @@
 // commit), and the tokens' rows; the products cost 4 M dk dv flops a chain and run on the
 // fp32 matrix instructions (16x16x4) under the loads of other workgroups.  The commit
 // keeps to that: 256 sequences x 6 heads, dk = dv = 128, 5 of 8 tokens kept at the mean,
-// 210 MB in 41 us, 5.1 TB/s.  The draft is bound by the instructions a wavefront issues
-// for the small matrices (about 1000 vector and 400 scalar ones a pass, whatever the
-// number of tokens) and, where there are few chains, by one pass's latency: the same
-// batch, 1 to 8 tokens, 131 MB in 32 us, 4.1 TB/s; 512 x 8 heads of 64 x 64 with
-// L = 8, 39 us for 8 tokens (4.9 TB/s) and 73 us for 9, whose second pass costs
-// as much as the first; 8 x 6 heads of 5 tokens, 8.5 us (a launch alone: 3.8).
+// 210 MB in 41 us, 5.1 TB/s.  The draft of one pass is two or three
+// dependent reads, a barrier, the small matrices and the products, and a batch of 1500 to 4000 chains is
+// only two rounds of the workgroups that the registers let run at a time (120 a lane,
+// four wavefronts a SIMD), so that loads and products of one round overlap in part: the same
+// batch, 1 to 8 tokens, 131 MB in 31.4 us, 4.2 TB/s; 512 x 8 heads of 64 x 64 with
+// L = 8, 38 us for 8 tokens (5.0 TB/s) and 69 us for 9, whose second pass reads the
+// state again; 8 x 6 heads of 5 tokens, 8.2 us (a launch alone: 3.8).
 // Long sequences are walked all the same, with the square of the passes: 32 x 8
 // heads (64 x 64) take 7.4, 100, 1520 and 25,000 us for 8, 64, 256 and 1024 tokens.
 //
@@ -62,8 +63,10 @@
 // tokens covers tokens 2 r and 2 r + 1, so steps beyond the last token are left out.
 // The write keys are formed by the whole workgroup (one thread per token and
 // four channels, every load of it issued before the state's and before the first
-// wait); after one barrier each wavefront forms the small matrices for itself
-// (16 to 32 matrix instructions) instead of waiting for another one's.
+// wait).  After a barrier one wavefront forms the small matrices, while the others
+// go on to the state's product; after a second one all take them from LDS (each
+// wavefront for itself: 512 x 8 heads 40.8 instead of 38.8 us, 256 x 6 heads 32.6
+// instead of 31.4; the work given to another wavefront from chain to chain: 38.4 and 32.4).
 // kw and p stay in fp32, as in the single-token step, so that the commit loses nothing;
 // o is rounded once, from fp32.
 #include "common.h"
@@ -345,7 +348,9 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
     constexpr int ITEMS = (kBlock * CG + NTH - 1) / NTH;         // pieces of the tile rows a thread stages
     // rows 0..7 Q, 8..15 K, 16..23 KW: rows 8.. are [K; KW], row (i + 8) % 16 of [K; Q] is i
     __shared__ __align__(16) float sRows[24 * LD];
-    __shared__ __align__(16) float sM[W][2][16][20];     // a wavefront's [A B; C E], then W
+    __shared__ __align__(16) float sM[2][16][20];        // [A B; C E], then W
+    __shared__ __align__(16) float sGam[16];             // the gates before a row of K, up to a row of Q
+    __shared__ __align__(16) float sD[W][16][20];        // a wavefront's dot products with earlier tokens
     __shared__ int sWild[W];
 
     const Segment<T> in = (Segment<T>)__builtin_amdgcn_kernarg_segment_ptr();
@@ -410,9 +415,12 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
 #pragma unroll
         for (int x = 0; x < ITEMS; ++x) {
             const int i = tid + x * NTH, t = i / CG, ch = (i % CG) * 4;
-            f32x4_t kt, wt;
+            f32x4_t kt = {}, wt = {};
             const typename X::raw4 qr = X::load4(ps.q, (t * ps.krow + ch) * ES);
-            if (!staged) {
+            if (LEV > 0 && t >= m) {
+                // no token: zero rows without the chain (4 of 8 tokens, L = 8: 31.8 instead of 32.9
+                // us; at L = 1, where there is none, the branch costs more: 25.5 instead of 24.6)
+            } else if (!staged) {
                 WriteKey<T, DK, DV, LEV, GELU> key(ps, ap->k, ap->u, ap->a, ap->h, ap->conv_w, ap->k_hist, chain, c0,
                                                      base, m, H, e, L);
                 key.fetch(t, ch);
@@ -437,7 +445,7 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
                 WriteKey<T, DK, DV, LEV, GELU> key(later, al->k, al->u, al->a, al->h, al->conv_w, al->k_hist, chain, c0,
                                                    at, mt, H, e, L);
 #pragma unroll 1
-                for (int i = opaque(tid); i < kBlock * CG; i += NTH) {
+                for (int i = opaque(tid); i < mt * CG; i += NTH) {
                     f32x4_t kt;
                     key.fetch(i / CG, (i % CG) * 4);
                     key.form(i / CG, (i % CG) * 4, kt);
@@ -472,88 +480,92 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
             m = 0;                                       // the same tokens again
             continue;
         }
-        float gg[kBlock], bb[kBlock];
-#pragma unroll
-        for (int t = 0; t < kBlock; ++t) {
-            gg[t] = lane_value(gl, t);
-            bb[t] = lane_value(bl, t);
-        }
-        // [K; Q] [K; KW]^T
-        f32x4_t d0 = {}, d1 = {};
         const float* pa = sRows + ((j + 8) & 15) * LD + 4 * kq;      // row j of [K; Q]
-        const float* pb = sRows + (j + 8) * LD + 4 * kq;             // row j of [K; KW]
+        float(*M0)[20] = sM[0], (*M1)[20] = sM[1];
+        if (wave == 0) {                                 // the small matrices, while the others go on to the state
+            float gg[kBlock], bb[kBlock];
 #pragma unroll
-        for (int R = 0; R < RT; ++R) {
-            const f32x4_t fa = *reinterpret_cast<const f32x4_t*>(pa + 16 * R);
-            const f32x4_t fb = *reinterpret_cast<const f32x4_t*>(pb + 16 * R);
-            d0 = mfma4(fa[0], fb[0], d0);
-            d1 = mfma4(fa[1], fb[1], d1);
-            d0 = mfma4(fa[2], fb[2], d0);
-            d1 = mfma4(fa[3], fb[3], d1);
-            if (R % 4 == 3)
-                __builtin_amdgcn_sched_barrier(0);       // not all the LDS reads at once: registers
-        }
-        d0 += d1;
-        // element (i, j): token ti of row i against token tj of column j, times the gates
-        // between them: for a row of K those before ti, for a row of Q those up to ti
-        const int tj = token_of(j & 7);
-        float rho[4] = {}, gam[4], run = 0.f, all = 1.f, own = 0.f;
+            for (int t = 0; t < kBlock; ++t) {
+                gg[t] = lane_value(gl, t);
+                bb[t] = lane_value(bl, t);
+            }
+            // [K; Q] [K; KW]^T
+            f32x4_t d0 = {}, d1 = {};
+            const float* pb = sRows + (j + 8) * LD + 4 * kq;             // row j of [K; KW]
 #pragma unroll
-        for (int t = 0; t < kBlock; ++t) {
-            const float before = all, upto = run;        // products of the gates before t; from tj + 1 before t
-            all *= gg[t];
-            run = t == tj ? 1.f : run * gg[t];           // 0 before tj, rho(t, tj) from there on
-            own = t == tj ? gg[t] * bb[t] : own;
+            for (int R = 0; R < RT; ++R) {
+                const f32x4_t fa = *reinterpret_cast<const f32x4_t*>(pa + 16 * R);
+                const f32x4_t fb = *reinterpret_cast<const f32x4_t*>(pb + 16 * R);
+                d0 = mfma4(fa[0], fb[0], d0);
+                d1 = mfma4(fa[1], fb[1], d1);
+                d0 = mfma4(fa[2], fb[2], d0);
+                d1 = mfma4(fa[3], fb[3], d1);
+                if (R % 4 == 3)
+                    __builtin_amdgcn_sched_barrier(0);       // not all the LDS reads at once: registers
+            }
+            d0 += d1;
+            // element (i, j): token ti of row i against token tj of column j, times the gates
+            // between them: for a row of K those before ti, for a row of Q those up to ti
+            const int tj = token_of(j & 7);
+            float rho[4] = {}, gam[4] = {}, run = 0.f, all = 1.f, own = 0.f;
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (t == 2 * r + (kq & 1)) {
-                    rho[r] = kq < 2 ? upto : run;
-                    gam[r] = kq < 2 ? before : all;
+            for (int t = 0; t < kBlock; ++t) {
+                const float before = all, upto = run;        // products of the gates before t; from tj + 1 before t
+                all *= gg[t];
+                run = t == tj ? 1.f : run * gg[t];           // 0 before tj, rho(t, tj) from there on
+                own = t == tj ? gg[t] * bb[t] : own;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (t == 2 * r + (kq & 1)) {
+                        rho[r] = kq < 2 ? upto : run;
+                        gam[r] = kq < 2 ? before : all;
+                    }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if (j == 0)
+                *reinterpret_cast<f32x4_t*>(sGam + 4 * kq) = f32x4_t{gam[0], gam[1], gam[2], gam[3]};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int ti = 2 * r + (kq & 1);
+                float x = 0.f;                               // selected, not scaled: see above
+                if (ti < m && (kq < 2 ? tj < ti : tj <= ti))
+                    x = rho[r] * (j < 8 ? own : 1.f) * d0[r];
+                M0[4 * kq + r][j] = x;
+            }
+            wave_fence();
+            // T by substitution, column tj' = slot lane % 8 on every group of 8 lanes; row lane / 8 of
+            // T and of -C T is kept
+            {
+                const int c = lane & 7, gr = lane >> 3;
+                float tc[kBlock];                            // T's column, by token
+#pragma unroll
+                for (int i = 0; i < kBlock; ++i) {
+                    float x = token_of(c) == i ? 1.f : 0.f;
+                    const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(&M0[slot_of(i)][0]);
+                    const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(&M0[slot_of(i)][4]);
+#pragma unroll
+                    for (int l = 0; l < i; ++l)
+                        x -= ((l & 1) ? hi[l >> 1] : lo[l >> 1]) * tc[l];
+                    tc[i] = x;
+                    if (i % 4 == 3)
+                        __builtin_amdgcn_sched_barrier(0);
                 }
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        float(*M0)[20] = sM[wave][0], (*M1)[20] = sM[wave][1];
+                const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(&M0[8 + gr][0]);
+                const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(&M0[8 + gr][4]);
+                float ct = 0.f, tt = 0.f;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int ti = 2 * r + (kq & 1);
-            float x = 0.f;                               // selected, not scaled: see above
-            if (ti < m && (kq < 2 ? tj < ti : tj <= ti))
-                x = rho[r] * (j < 8 ? own : 1.f) * d0[r];
-            M0[4 * kq + r][j] = x;
-        }
-        wave_fence();
-        // T by substitution, column tj' = slot lane % 8 on every group of 8 lanes; row lane / 8 of
-        // T and of -C T is kept
-        {
-            const int c = lane & 7, gr = lane >> 3;
-            float tc[kBlock];                            // T's column, by token
-#pragma unroll
-            for (int i = 0; i < kBlock; ++i) {
-                float x = token_of(c) == i ? 1.f : 0.f;
-                const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(&M0[slot_of(i)][0]);
-                const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(&M0[slot_of(i)][4]);
-#pragma unroll
-                for (int l = 0; l < i; ++l)
-                    x -= ((l & 1) ? hi[l >> 1] : lo[l >> 1]) * tc[l];
-                tc[i] = x;
-                if (i % 4 == 3)
-                    __builtin_amdgcn_sched_barrier(0);
+                for (int l = 0; l < kBlock; ++l) {
+                    ct -= ((l & 1) ? hi[l >> 1] : lo[l >> 1]) * tc[l];
+                    tt = slot_of(l) == gr ? tc[l] : tt;
+                }
+                M1[gr][c] = tt;
+                M1[gr][8 + c] = 0.f;
+                M1[8 + gr][c] = ct;
+                M1[8 + gr][8 + c] = gr == c ? 1.f : 0.f;
             }
-            const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(&M0[8 + gr][0]);
-            const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(&M0[8 + gr][4]);
-            float ct = 0.f, tt = 0.f;
-#pragma unroll
-            for (int l = 0; l < kBlock; ++l) {
-                ct -= ((l & 1) ? hi[l >> 1] : lo[l >> 1]) * tc[l];
-                tt = slot_of(l) == gr ? tc[l] : tt;
-            }
-            M1[gr][c] = tt;
-            M1[gr][8 + c] = 0.f;
-            M1[8 + gr][c] = ct;
-            M1[8 + gr][8 + c] = gr == c ? 1.f : 0.f;
+            wave_fence();
+            __builtin_amdgcn_sched_barrier(0);
         }
-        wave_fence();
-        __builtin_amdgcn_sched_barrier(0);
         // [K; Q] S
         f32x4_t x[2] = {};
 #pragma unroll
@@ -569,9 +581,11 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
             if (R % 4 == 3)
                 __builtin_amdgcn_sched_barrier(0);
         }
+        lds_barrier();
         // columns 8.. of the first matrix ([B; E]; the second half of vv repeats the first), and W
         const f32x4_t fv = *reinterpret_cast<const f32x4_t*>(&M0[j][8 + 4 * (kq & 1)]);
         const f32x4_t fw = *reinterpret_cast<const f32x4_t*>(&M1[j][4 * kq]);
+        const f32x4_t gam = *reinterpret_cast<const f32x4_t*>(sGam + 4 * kq);
         if (base > 0) {
             // the tokens of earlier passes, 8 at a time from the latest: their part of the state
             // is [K'; KW']^T [X'; Y'], so that they add ([K; Q] [K'; KW']^T) [X'; Y'] of 16x16
@@ -611,10 +625,10 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
                 for (int r = 0; r < 4; ++r) {
                     xy[0][r] *= f[r];
                     xy[1][r] *= f[r];
-                    M0[4 * kq + r][j] = d[r];
+                    sD[wave][4 * kq + r][j] = d[r];
                 }
                 wave_fence();
-                const f32x4_t fd = *reinterpret_cast<const f32x4_t*>(&M0[j][4 * kq]);
+                const f32x4_t fd = *reinterpret_cast<const f32x4_t*>(&sD[wave][j][4 * kq]);
                 wave_fence();
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
