@@ -176,6 +176,7 @@ struct NormResidualArgs {
     float* ws;                      // norm_residual_bwd_blocks() partial rows of dw (and dscale)
 };
 constexpr int kNormMaxWidth = 8192, kNormGateMaxWidth = 1024;
+constexpr int kNormGateMaxHeads = 65535;         // as many columns as the launch that adds the partials holds
 constexpr int kNormBwdBlocks = 512;              // workgroups of a backward, at most
 int norm_residual_bwd_blocks(int64_t rows, int width);
 hipError_t launch_norm_residual(const NormResidualArgs& p, hipStream_t stream);

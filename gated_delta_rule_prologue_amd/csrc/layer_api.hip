@@ -60,8 +60,8 @@ bool apart(std::initializer_list<Region> outs, std::initializer_list<Region> ins
 
 int64_t size_of(int dtype) { return dtype == PRISM_BF16 ? 2 : 4; }
 
-// one grid dimension holds the workgroups
-bool grid_ok(int64_t blocks) { return blocks <= INT32_MAX; }
+// A launch holds less than 2^32 threads in a dimension of its grid.
+bool grid_ok(int64_t blocks, int64_t threads) { return blocks <= UINT32_MAX / threads; }
 
 // The kernels of drafted tokens reach 8 tokens and the three rows before them from one
 // base with 32-bit offsets.
@@ -69,7 +69,7 @@ bool draft_shape_ok(const prism_dims* d, int64_t levels)
 {
     const int64_t row = d->dk * levels > d->dv ? d->dk * levels : d->dv;
     return prism::decode_supported(d->dk, d->dv) && (int64_t)d->heads * row * 11 * 4 <= INT32_MAX &&
-           grid_ok((int64_t)d->n_seqs * d->heads);
+           grid_ok((int64_t)d->n_seqs * d->heads, 2 * d->dv);
 }
 
 }  // namespace
@@ -155,7 +155,7 @@ prism_status prism_norm_gate(const prism_norm_dims* d, const void* o, const void
         return PRISM_EINVAL;
     if (!row_ok(d, o) || !row_ok(d, z) || !ptr_ok(w) || !row_ok(d, y))
         return PRISM_EINVAL;
-    if (d->width > prism::kNormGateMaxWidth)
+    if (d->width > prism::kNormGateMaxWidth || d->heads > prism::kNormGateMaxHeads)
         return PRISM_EUNSUPPORTED;
     const int64_t es = size_of(d->dtype), all = d->rows * d->width * es;
     if (!apart({{y, all, true}}, {{o, all, true}, {z, all, true}, {w, (int64_t)d->heads * d->width * es}}))
@@ -181,7 +181,7 @@ prism_status prism_norm_gate_bwd(const prism_norm_dims* d, const void* o, const 
     if (!row_ok(d, o) || !row_ok(d, z) || !ptr_ok(w) || !row_ok(d, dy) || !row_ok(d, d_o) || !row_ok(d, dz) ||
         !ptr_ok(dw) || !ptr_ok(workspace))
         return PRISM_EINVAL;
-    if (d->width > prism::kNormGateMaxWidth)
+    if (d->width > prism::kNormGateMaxWidth || d->heads > prism::kNormGateMaxHeads)
         return PRISM_EUNSUPPORTED;
     const int64_t need = prism_norm_workspace_bytes(d);
     if (workspace_bytes < (size_t)need)
@@ -308,7 +308,7 @@ prism_status prism_verify_draft(const prism_verify_dims* d, const void* p, const
     const size_t need = prism_verify_workspace_bytes(d);
     if (need > 0 ? !ptr_ok(workspace) || workspace_bytes < need : !opt_ok(workspace))
         return PRISM_EINVAL;
-    if (d->vocab > (1 << 28) || !grid_ok((int64_t)d->n_seqs * prism::verify_chunks(d->vocab)))
+    if (d->vocab > (1 << 28) || !grid_ok((int64_t)d->n_seqs * prism::verify_chunks(d->vocab), 1024))
         return PRISM_EUNSUPPORTED;
     const int64_t rows = (int64_t)d->total_tokens * d->vocab * size_of(d->dtype), each = (int64_t)d->n_seqs * 4;
     if (!apart({{n_accept, each}, {next_token, each}, {workspace, (int64_t)need}},

@@ -487,7 +487,7 @@ prism_status prism_norm_residual_bwd(const prism_norm_dims* d, const void* r, co
  *   w         [heads, width]  heads = H: a weight a head; 1: one for all
  *   gate      prism_gate
  *   y         out [rows, width]; may be the buffer of o or z
- * width <= 1024, else PRISM_EUNSUPPORTED.
+ * width <= 1024 and heads <= 65535, else PRISM_EUNSUPPORTED.
  */
 prism_status prism_norm_gate(const prism_norm_dims* d, const void* o, const void* z, const void* w,
                              float eps, int gate, void* y, void* stream);
@@ -526,7 +526,8 @@ prism_status prism_norm_gate_bwd(const prism_norm_dims* d, const void* o, const 
  *   p           out fp32 [T, H, dv]        S_{t-1}^T k_t: what prism_decode_commit needs
  *                                          to move the state by any number of the tokens
  * The write key is kept in fp32 (as in prism_decode_step).  dk, dv in {64, 128} and
- * H * max(dk (L - 1), dv) <= 48,000,000, else PRISM_EUNSUPPORTED.  A token's outputs
+ * H * max(dk (L - 1), dv) <= 48,000,000 and 2 dv n_seqs H < 2^32, else
+ * PRISM_EUNSUPPORTED.  A token's outputs
  * depend on the tokens up to it only, also where later ones hold infinities or NaN.
  * No workspace.
  */
@@ -594,7 +595,7 @@ size_t prism_verify_workspace_bytes(const prism_verify_dims* d);
  * p and q need not be normalised.  Weights that are not positive and finite (NaN
  * too) count as none; a row of max(p - q, 0) without weight falls back to p, and a
  * row of p without weight gives -1.  Products and sums are formed in 64 bits.
- * vocab <= 2^28, else PRISM_EUNSUPPORTED.
+ * vocab <= 2^28 and n_seqs * ceil((vocab + 7) / 4096) < 2^22, else PRISM_EUNSUPPORTED.
  */
 prism_status prism_verify_draft(const prism_verify_dims* d, const void* p, const void* q,
                                 const int32_t* tokens, const int32_t* cu_seqlens,

@@ -2,7 +2,7 @@
 recurrence in 64 bits.
 
 Tolerances.  The records and fp32 outputs come from fp32 sums of dk <= 128 products and
-a triangular system over at most 16 tokens whose couplings b k.k are at most 1 in
+a triangular system over at most 16 tokens (8 a pass) whose couplings b k.k are at most 1 in
 size: 128 + 2 x 16 terms' roundings (160 x 2^-24 = 1e-5) times the solve's growth
 (below 10 for unit keys and b <= 1) stays under 1e-4 of the largest element, the bound
 this operator's fp32 results are held to everywhere.  A bf16 output adds its own

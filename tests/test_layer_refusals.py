@@ -225,6 +225,22 @@ def test_outputs_that_overlap_are_refused(B):
                                             1 << 30, None) == B.PRISM_EINVAL, (out, other)
 
 
+def test_grids_beyond_a_launch_are_refused(B):
+    """Chains, sequences and heads that one launch cannot hold (2^32 threads)."""
+    at = far(15)
+    L = B.lib()
+    for n, H, dv in ((1 << 20, 16, 128), (1 << 20, 32, 64)):
+        d = ctypes.byref(B.make_dims(n, 12, H, 64, dv, 1))
+        assert L.prism_decode_draft(d, *at[:10], 3, 0, *at[10:], None) == B.PRISM_EUNSUPPORTED
+        assert L.prism_decode_commit(d, *at[:12], None) == B.PRISM_EUNSUPPORTED
+    for n, vocab in ((1 << 22, 1000), (1 << 19, 40000)):
+        assert L.prism_verify_draft(ctypes.byref(B.VerifyDims(n, 12, vocab, 0)), *at[:9], 1 << 40,
+                                    None) == B.PRISM_EUNSUPPORTED
+    d = nd(B, rows=65536, heads=65536, width=8)
+    assert L.prism_norm_gate(d, *at[:3], 1e-6, 0, at[3], None) == B.PRISM_EUNSUPPORTED
+    assert L.prism_norm_gate_bwd(d, *at[:3], 1e-6, 0, *at[3:8], 1 << 40, None) == B.PRISM_EUNSUPPORTED
+
+
 def test_drafts_longer_than_served_are_refused(B):
     f = B.lib().prism_decode_draft
     at = far(15)
