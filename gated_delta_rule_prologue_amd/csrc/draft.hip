@@ -16,8 +16,10 @@
 //   O         = diag(gamma_i) Q S - C P + E V
 //   A_ij = rho(i-1, j) g_j b_j <k_j, k_i>, B_ij = rho(i-1, j) <kw_j, k_i>   (j < i)
 //   C_ij = rho(i, j) g_j b_j <k_j, q_i>,   E_ij = rho(i, j) <kw_j, q_i>     (j <= i)
-// In one product, with T = (I + A)^-1 and the rows of K and Q stacked:
-//   [P; O] = W ([gamma K S; gamma Q S] + [B; E] V),   W = [[T, 0], [-C T, I]].
+// With T = (I + A)^-1 and the rows of K and Q stacked,
+//   [XP; XO] = [gamma K S; gamma Q S] + [B; E] V,   [P; O] = [0; XO] + W XP,   W = [T; -C T]:
+// a row of Q is added to its own output and enters no product with the others', whose zeros
+// would make a query that is not finite a NaN of every token.
 // The products of gates are formed directly (never a quotient), so a gate of
 // exactly zero is served.  kw and p are left as records, in fp32, from which
 // the commit moves the state by m kept tokens without solving anything:
@@ -48,7 +50,7 @@
 // 16x16x4 step whose contraction index kq names row 4 kq + r, the second operand's
 // too: S enters [K; Q] S and receives [K; KW]^T [X; Y] with no exchange between lanes.
 // The first operand of step r then wants channel 4 kq + r, so one 16-byte LDS read
-// serves four steps.  The same holds for [P; O], which comes out of one product and
+// serves four steps.  The same holds for XP, which comes out of one product and
 // enters the next.
 // The commit holds the state in registers (64 a lane at 128 x 128).  The draft streams
 // it through the products instead, four tiles in flight, and reads it again in each
@@ -559,9 +561,8 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
                     tt = slot_of(l) == gr ? tc[l] : tt;
                 }
                 M1[gr][c] = tt;
-                M1[gr][8 + c] = 0.f;
                 M1[8 + gr][c] = ct;
-                M1[8 + gr][8 + c] = gr == c ? 1.f : 0.f;
+                M1[gr][8 + c] = M1[8 + gr][8 + c] = 0.f;     // what the lanes of Q's rows read
             }
             wave_fence();
             __builtin_amdgcn_sched_barrier(0);
@@ -582,7 +583,8 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
                 __builtin_amdgcn_sched_barrier(0);
         }
         lds_barrier();
-        // columns 8.. of the first matrix ([B; E]; the second half of vv repeats the first), and W
+        // columns 8.. of the first matrix ([B; E]; the second half of vv repeats the first), and W,
+        // zeros for the rows of Q
         const f32x4_t fv = *reinterpret_cast<const f32x4_t*>(&M0[j][8 + 4 * (kq & 1)]);
         const f32x4_t fw = *reinterpret_cast<const f32x4_t*>(&M1[j][4 * kq]);
         const f32x4_t gam = *reinterpret_cast<const f32x4_t*>(sGam + 4 * kq);
@@ -650,6 +652,11 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
             for (int r = 0; r < 4; ++r)
                 if (r < steps)
                     x[c] = mfma4(kq < 2 ? fv[r] : 0.f, vv[c][r], x[c]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {                // Q's rows: to their outputs alone
+                y[c][r] = kq < 2 ? 0.f : x[c][r];
+                x[c][r] = kq < 2 ? x[c][r] : 0.f;
+            }
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 if (r < steps)

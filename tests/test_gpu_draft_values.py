@@ -1,0 +1,60 @@
+"""Drafted tokens with values that are not finite or whose products overflow: every output and
+record against the token-by-token recurrence in 64 bits wherever a value does not reach
+it.  Tolerances as in test_gpu_draft.py (the same sums), per row where rows differ in scale."""
+import pytest
+
+from tests.layer_refs import f64
+from tests import layer_refs as R
+from tests.test_gpu_draft import commit, make, near, run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from gated_delta_rule_prologue_amd import binding
+    binding.lib()
+
+
+def reference(d, cu, L, S, hist, residual="linear"):
+    return R.draft({k: f64(v) for k, v in d.items()}, cu, L, f64(S), f64(hist), residual)
+
+
+def commit_near(d, cu, cu_t, kept, kw, p, S, hist):
+    """The state moved by `kept` tokens, from the records, is finite and the reference's."""
+    import torch
+    S_out, _ = commit(d, cu_t, kept, kw, p, S, hist, S_out=torch.empty_like(S), k_hist_out=torch.empty_like(hist))
+    want, _ = R.commit(f64(d["k"]), f64(d["v"]), f64(d["g"]), f64(d["b"]), cu, kept, f64(kw), f64(p), f64(S), f64(hist))
+    for n in range(len(kept)):
+        near(f"S of {n}", S_out[n], want[n], 8e-6)
+
+
+@pytest.mark.parametrize("value", ["nan", "inf"])
+@pytest.mark.parametrize("single", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_query_stays_in_its_row(value, single, dtype):
+    """A q that is not finite shows in its own row of o: the records (its own token's too) and every
+    other output stay, in blocks of 8 and where a later value (`single`) makes a sequence's
+    tokens go one at a time; the commit may keep that token."""
+    import torch
+    d, cu, cu_t, S, hist = make([9, 9, 18], dk=128, dv=64, dtype=dtype, seed=7)
+    rows = (5, 18 + 5, 18 + 10)
+    for row in rows:
+        d["q"][row, 0, 3] = float(value)
+    last = cu[-1]
+    if single:
+        d["v"][18 + 12, 0, 7] = 1e30                     # beyond what a block takes
+        last = 18 + 12
+    o, kw, p = run(d, cu_t, 4, S, hist)
+    ro, rkw, rp, _ = reference(d, cu, 4, S, hist)
+    for row in rows:
+        assert not torch.isfinite(o[row, 0]).any() and not torch.isfinite(ro[row, 0]).any()
+    clean = [t for t in range(last) if t not in rows]
+    near("o", o[clean], ro[clean])
+    near("o of the other head", o[:, 1], ro[:, 1])
+    near("kw", kw[:last], rkw[:last])
+    near("p", p[:last], rp[:last])
+    commit_near(d, cu, cu_t, [6, 9, 12], kw, p, S, hist)
