@@ -71,6 +71,8 @@
 // instead of 31.4; the work given to another wavefront from chain to chain: 38.4 and 32.4).
 // kw and p stay in fp32, as in the single-token step, so that the commit loses nothing;
 // o is rounded once, from fp32.
+#include <float.h>
+
 #include "common.h"
 #include "kernels.h"
 #include "prism.h"
@@ -190,6 +192,37 @@ __device__ __forceinline__ float scale_tokens(float gl, float bl, int kq, float 
         f[t >> 1] = (t & 1) == 1 || (kq & 1) == 0 ? (kq < 2 ? x : y) : f[t >> 1];
     }
     return after;
+}
+
+__device__ __forceinline__ bool finite4(f32x4_t x)
+{
+    return fabsf(x[0]) <= FLT_MAX && fabsf(x[1]) <= FLT_MAX && fabsf(x[2]) <= FLT_MAX && fabsf(x[3]) <= FLT_MAX;
+}
+
+// y += M x for a matrix M (16 rows, columns `at` .. at + 7, rows and columns in slots) that is
+// triangular in the tokens, and the tokens' values x (token 2 r + kq in register r of lanes
+// kq < 2): as the matrix product, but M's zeros are left out instead of multiplied, which an
+// x that is not finite would turn into NaN of earlier tokens.  A row takes the tokens up to its
+// own (a row of K, if `before`, those before it); rows past the m tokens stay.
+__device__ __forceinline__ void add_triangular(f32x4_t (&y)[2], const float (*M)[20], int at, bool before,
+                                               const f32x4_t (&x)[2], int m, int kq, int j)
+{
+#pragma unroll
+    for (int t = 0; t < kBlock; ++t) {
+        float xt[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            xt[c] = __shfl(x[c][t >> 1], (t & 1) * 16 + j);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int own = 2 * r + (kq & 1);
+            const bool in = own < m && (t < own || (t == own && !(before && kq < 2)));
+            const float w = M[4 * kq + r][at + slot_of(t)];
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                y[c][r] = in ? y[c][r] + w * xt[c] : y[c][r];
+        }
+    }
 }
 
 // S <- gam S + [K; KW]^T [X; Y] for the rows of [K; KW] in LDS (fp32, 16 rows of
@@ -642,16 +675,24 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
             for (int c = 0; c < 2; ++c)
                 x[c] = between * x[c] + z[c];
         }
-        f32x4_t y[2] = {};
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int r = 0; r < 4; ++r)                  // rows past the tokens stay out of the next product
                 x[c][r] = 2 * r + (kq & 1) < m ? gam[r] * x[c][r] : 0.f;
+        if (__ballot(!(finite4(vv[0]) && finite4(vv[1])))) {
+            add_triangular(x, M0, 8, true, vv, m, kq, j);
+        } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (r < steps)
-                    x[c] = mfma4(kq < 2 ? fv[r] : 0.f, vv[c][r], x[c]);
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (r < steps)
+                        x[c] = mfma4(kq < 2 ? fv[r] : 0.f, vv[c][r], x[c]);
+        }
+        f32x4_t y[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {                // Q's rows: to their outputs alone
                 y[c][r] = kq < 2 ? 0.f : x[c][r];

@@ -58,3 +58,21 @@ def test_a_query_stays_in_its_row(value, single, dtype):
     near("kw", kw[:last], rkw[:last])
     near("p", p[:last], rp[:last])
     commit_near(d, cu, cu_t, [6, 9, 12], kw, p, S, hist)
+
+
+@pytest.mark.parametrize("value", ["nan", "inf"])
+@pytest.mark.parametrize("name", ["v", "u"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_write_stays_out_of_its_own_record(name, value, dtype):
+    """p of a token is formed from the state before it: its own v and write key, finite or not, are no
+    part of it."""
+    d, cu, cu_t, S, hist = make([9, 18], dk=64, dv=128, dtype=dtype, seed=17)
+    rows = (4, 9 + 12)
+    for row in rows:
+        d[name][(row, 0, 3) if name == "v" else (row, 0, 1, 3)] = float(value)
+    o, kw, p = run(d, cu_t, 4, S, hist)
+    ro, rkw, rp, _ = reference(d, cu, 4, S, hist)
+    upto = list(range(5)) + list(range(9, 9 + 13))
+    near("p", p[upto], rp[upto])
+    before = [t for t in upto if t not in rows]
+    near("o", o[before], ro[before])
