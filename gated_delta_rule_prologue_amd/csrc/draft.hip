@@ -21,7 +21,10 @@
 // a row of Q is added to its own output and enters no product with the others', whose zeros
 // would make a query that is not finite a NaN of every token.
 // The products of gates are formed directly (never a quotient), so a gate of
-// exactly zero is served.  kw and p are left as records, in fp32, from which
+// exactly zero is served.  A token's p and o depend on the tokens up to it alone, also where later
+// ones hold infinities or NaN, or overflow: what a later token makes of a matrix is in its own
+// row, and where a triangular matrix meets rows that are not finite (XP, V), its zeros are
+// left out by selection instead of multiplied.  kw and p are left as records, in fp32, from which
 // the commit moves the state by m kept tokens without solving anything:
 //   S' = gamma_{m-1} S + sum_{j<m} k_j x_j^T + kw_j y_j^T,
 //   x_j = -rho(m-1, j) g_j b_j p_j,  y_j = rho(m-1, j) v_j.
@@ -71,8 +74,6 @@
 // instead of 31.4; the work given to another wavefront from chain to chain: 38.4 and 32.4).
 // kw and p stay in fp32, as in the single-token step, so that the commit loses nothing;
 // o is rounded once, from fp32.
-#include <float.h>
-
 #include "common.h"
 #include "kernels.h"
 #include "prism.h"
@@ -82,7 +83,6 @@ namespace prism {
 namespace {
 
 constexpr int kBlock = 8;                        // tokens per pass, at most
-constexpr float kLarge = 1073741824.f;           // 2^30
 
 __device__ __forceinline__ f32x4_t mfma4(float a, float b, f32x4_t c)
 {
@@ -164,11 +164,6 @@ typedef Elems<float> E32;
 constexpr int kOnce = 2;                         // nontemporal: read once per call
 constexpr uint32_t kOutside = 0xffffff00u;       // an offset past any span
 
-__device__ __forceinline__ bool tame4(f32x4_t x)
-{
-    return fabsf(x[0]) <= kLarge && fabsf(x[1]) <= kLarge && fabsf(x[2]) <= kLarge && fabsf(x[3]) <= kLarge;
-}
-
 // LDS that only this wavefront uses: what its lanes have stored is there for its loads
 // (no instruction: the LDS serves a wavefront in order).
 __device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local"); }
@@ -194,30 +189,38 @@ __device__ __forceinline__ float scale_tokens(float gl, float bl, int kq, float 
     return after;
 }
 
-__device__ __forceinline__ bool finite4(f32x4_t x)
+// Whether every lane's values are finite: 0 x is zero for them, and NaN for an infinity or a NaN.
+__device__ __forceinline__ bool all_finite(const f32x4_t (&x)[2])
 {
-    return fabsf(x[0]) <= FLT_MAX && fabsf(x[1]) <= FLT_MAX && fabsf(x[2]) <= FLT_MAX && fabsf(x[3]) <= FLT_MAX;
+    float z[2] = {0.f, 0.f};
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            z[c] = __builtin_fmaf(x[c][r], 0.f, z[c]);
+    return __ballot(z[0] + z[1] != 0.f) == 0;
 }
 
 // y += M x for a matrix M (16 rows, columns `at` .. at + 7, rows and columns in slots) that is
 // triangular in the tokens, and the tokens' values x (token 2 r + kq in register r of lanes
 // kq < 2): as the matrix product, but M's zeros are left out instead of multiplied, which an
 // x that is not finite would turn into NaN of earlier tokens.  A row takes the tokens up to its
-// own (a row of K, if `before`, those before it); rows past the m tokens stay.
-__device__ __forceinline__ void add_triangular(f32x4_t (&y)[2], const float (*M)[20], int at, bool before,
-                                               const f32x4_t (&x)[2], int m, int kq, int j)
+// own; with STRICT a row of K (kq < 2) takes those before it.
+template <bool STRICT>
+__device__ __forceinline__ void add_triangular(f32x4_t (&y)[2], const float (*M)[20], int at, const f32x4_t (&x)[2],
+                                               int kq, int j)
 {
+    const bool own_even = !STRICT || kq != 0, own_odd = STRICT ? kq == 3 : (kq & 1) == 1;
 #pragma unroll
     for (int t = 0; t < kBlock; ++t) {
         float xt[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-            xt[c] = __shfl(x[c][t >> 1], (t & 1) * 16 + j);
+            xt[c] = __int_as_float(__builtin_amdgcn_ds_bpermute(4 * ((t & 1) * 16 + j), __float_as_int(x[c][t >> 1])));
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int own = 2 * r + (kq & 1);
-            const bool in = own < m && (t < own || (t == own && !(before && kq < 2)));
+        for (int r = t >> 1; r < 4; ++r) {               // row 4 kq + r: token 2 r + kq % 2
             const float w = M[4 * kq + r][at + slot_of(t)];
+            const bool in = t < 2 * r || (t == 2 * r ? own_even : own_odd);
 #pragma unroll
             for (int c = 0; c < 2; ++c)
                 y[c][r] = in ? y[c][r] + w * xt[c] : y[c][r];
@@ -368,7 +371,8 @@ template <typename T> struct DraftPointers {
 };
 template <typename T> using Segment = const __attribute__((address_space(4))) DraftPointers<T>*;
 
-// The same address, whose loads are not moved to where it came from.
+// The same scalar value, not known to the compiler: loads from an address, and what derives
+// from a number, are not moved to where it came from.
 template <typename P> __device__ __forceinline__ P again(P p)
 {
     asm volatile("" : "+s"(p));
@@ -386,13 +390,12 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
     __shared__ __align__(16) float sM[2][16][20];        // [A B; C E], then W
     __shared__ __align__(16) float sGam[16];             // the gates before a row of K, up to a row of Q
     __shared__ __align__(16) float sD[W][16][20];        // a wavefront's dot products with earlier tokens
-    __shared__ int sWild[W];
 
     const Segment<T> in = (Segment<T>)__builtin_amdgcn_kernarg_segment_ptr();
-    const int H = in->H, L = in->L;
+    const int heads = in->H, levels = in->L;
     const int64_t chain = blockIdx.x;
-    const int e = (int)(chain % H);
-    const int64_t n = chain / H;
+    const int e = (int)(chain % heads);
+    const int64_t n = chain / heads;
 
     // the state is streamed: tiles R .. R + PRE - 1 in flight, rows 16 R + 4 kq + r, two
     // columns a lane; the first EARLY are on their way before the sequence is looked up
@@ -416,28 +419,26 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
         return;
     if (len > PRISM_MAX_DRAFT) {                         // not served
         for (int64_t i = threadIdx.x; i < (int64_t)len * DK; i += NTH)
-            in->kw[((c0 + i / DK) * H + e) * DK + i % DK] = __builtin_nanf("");
+            in->kw[((c0 + i / DK) * heads + e) * DK + i % DK] = __builtin_nanf("");
         for (int64_t i = threadIdx.x; i < (int64_t)len * DV; i += NTH) {
-            in->p[((c0 + i / DV) * H + e) * DV + i % DV] = __builtin_nanf("");
-            X::store1(in->o + ((c0 + i / DV) * H + e) * DV + i % DV, __builtin_nanf(""));
+            in->p[((c0 + i / DV) * heads + e) * DV + i % DV] = __builtin_nanf("");
+            X::store1(in->o + ((c0 + i / DV) * heads + e) * DV + i % DV, __builtin_nanf(""));
         }
         return;
     }
 
-    // A token's zeros in the triangular matrices would turn an infinity or a NaN
-    // of a later token into a NaN of its own, so a sequence with a value beyond
-    // kLarge (whose products may overflow too) takes its tokens one at a time.
-    int cap = kBlock, m = 0;
-    bool staged = false;                                 // whether the write keys are formed
-    for (int base = 0; base < len; base += m) {
+    for (int base = 0, m; base < len; base += m) {
+        // what derives from the sizes is formed in each pass: kept over them it is spilled
+        const int H = again(heads), L = again(levels);
         const int tid = opaque(threadIdx.x), lane = tid & 63, kq = lane >> 4, j = lane & 15;
         const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = 32 * wave + 2 * j;
-        m = len - base < cap ? len - base : cap;
+        m = len - base < kBlock ? len - base : kBlock;
         const int steps = (m + 1) >> 1;
         const Segment<T> ap = again(in);
         const Pass<T, DK, DV> ps(ap->k, ap->q, ap->v, ap->g, ap->b, ap->kw, ap->p, c0 + base, m, H, e);
+        const bool staged = again(base) > 0;             // whether the write keys are formed
         if (staged)
-            __syncthreads();                             // the pass before is done with the LDS; kw_out is written
+            __syncthreads();                             // the pass before is done with the LDS; kw and p are written
         // gates (lane t holds token t's) and value rows: register r holds row 4 (kq % 2) + r, token
         // 2 r + kq % 2, in both halves
         const typename X::raw1 gr = X::load1(ps.g, (lane & 7) * ps.grow * ES),
@@ -446,7 +447,6 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             vr[r] = X::load2(ps.v, ((2 * r + (kq & 1)) * ps.vrow + col) * ES);
-        bool tame = true;
 #pragma unroll
         for (int x = 0; x < ITEMS; ++x) {
             const int i = tid + x * NTH, t = i / CG, ch = (i % CG) * 4;
@@ -469,7 +469,6 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
                 *reinterpret_cast<f32x4_t*>(to) = X::f32(qr);
                 *reinterpret_cast<f32x4_t*>(to + 8 * LD) = kt;
                 *reinterpret_cast<f32x4_t*>(to + 16 * LD) = wt;
-                tame = tame && tame4(kt) && tame4(wt);
             }
         }
         if (!staged) {
@@ -491,7 +490,6 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
         for (int R = 0; R < PRE; ++R)
             if (staged || R >= EARLY)
                 fetch_state(R, tid);
-        staged = true;
         const float gl = (lane & 7) < m ? X::f32(gr) : 1.f, bl = X::f32(br);
         f32x4_t vv[2];
 #pragma unroll
@@ -500,21 +498,7 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
             vv[0][r] = x[0];
             vv[1][r] = x[1];
         }
-        tame = tame && fabsf(gl) <= kLarge && fabsf(bl) <= kLarge && tame4(vv[0]) && tame4(vv[1]);
-        if (lane == 0)
-            sWild[wave] = 0;
-        if (__ballot(!tame) && lane == 0)
-            sWild[wave] = 1;
         lds_barrier();                                   // the state's loads stay in flight
-        int wild = 0;
-#pragma unroll
-        for (int x = 0; x < W; ++x)
-            wild |= sWild[x];
-        if (wild && cap > 1) {
-            cap = 1;
-            m = 0;                                       // the same tokens again
-            continue;
-        }
         const float* pa = sRows + ((j + 8) & 15) * LD + 4 * kq;      // row j of [K; Q]
         float(*M0)[20] = sM[0], (*M1)[20] = sM[1];
         if (wave == 0) {                                 // the small matrices, while the others go on to the state
@@ -587,10 +571,11 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
                 }
                 const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(&M0[8 + gr][0]);
                 const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(&M0[8 + gr][4]);
+                const int own = token_of(gr);
                 float ct = 0.f, tt = 0.f;
 #pragma unroll
-                for (int l = 0; l < kBlock; ++l) {
-                    ct -= ((l & 1) ? hi[l >> 1] : lo[l >> 1]) * tc[l];
+                for (int l = 0; l < kBlock; ++l) {           // C's zeros left out: later rows of T may not be finite
+                    ct = l <= own ? ct - ((l & 1) ? hi[l >> 1] : lo[l >> 1]) * tc[l] : ct;
                     tt = slot_of(l) == gr ? tc[l] : tt;
                 }
                 M1[gr][c] = tt;
@@ -626,13 +611,12 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
             // is [K'; KW']^T [X'; Y'], so that they add ([K; Q] [K'; KW']^T) [X'; Y'] of 16x16
             f32x4_t z[2] = {};
             float between = 1.f;                         // the product of the gates from here to this pass
-            for (int cb = (base - 1) / kBlock * kBlock; cb >= 0; cb -= kBlock) {
-                const int mc = base - cb < kBlock ? base - cb : kBlock;
+            for (int cb = base - kBlock; cb >= 0; cb -= kBlock) {
                 const int lane = opaque(threadIdx.x) & 63, kq = lane >> 4, j = lane & 15;
                 const float* pa = sRows + ((j + 8) & 15) * LD + 4 * kq;
                 const Segment<T> ac = again(in);
-                const Pass<T, DK, DV> pc(ac->k, ac->q, ac->v, ac->g, ac->b, ac->kw, ac->p, c0 + cb, mc, H, e);
-                const float gc = (lane & 7) < mc ? X::f32(X::load1(pc.g, (lane & 7) * pc.grow * ES)) : 1.f;
+                const Pass<T, DK, DV> pc(ac->k, ac->q, ac->v, ac->g, ac->b, ac->kw, ac->p, c0 + cb, again(kBlock), H, e);
+                const float gc = X::f32(X::load1(pc.g, (lane & 7) * pc.grow * ES));
                 const float bc = X::f32(X::load1(pc.b, (lane & 7) * pc.grow * ES));
                 f32x4_t xy[2], d = {};
 #pragma unroll
@@ -680,14 +664,14 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
 #pragma unroll
             for (int r = 0; r < 4; ++r)                  // rows past the tokens stay out of the next product
                 x[c][r] = 2 * r + (kq & 1) < m ? gam[r] * x[c][r] : 0.f;
-        if (__ballot(!(finite4(vv[0]) && finite4(vv[1])))) {
-            add_triangular(x, M0, 8, true, vv, m, kq, j);
+        if (!all_finite(vv)) {
+            add_triangular<true>(x, M0, 8, vv, kq, j);
         } else {
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+            for (int r = 0; r < 4; ++r)
+                if (r < steps)
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (r < steps)
+                    for (int c = 0; c < 2; ++c)
                         x[c] = mfma4(kq < 2 ? fv[r] : 0.f, vv[c][r], x[c]);
         }
         f32x4_t y[2];
@@ -698,10 +682,18 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
                 y[c][r] = kq < 2 ? 0.f : x[c][r];
                 x[c][r] = kq < 2 ? x[c][r] : 0.f;
             }
+        }
+        // an infinity or a NaN of a token's row of XP (its key's, or an overflow) is not its
+        // predecessors'
+        if (!all_finite(x)) {
+            add_triangular<false>(y, M1, 0, x, kq, j);
+        } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 if (r < steps)
-                    y[c] = mfma4(fw[r], x[c][r], y[c]);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        y[c] = mfma4(fw[r], x[c][r], y[c]);
         }
         const Span out(again(in)->o + ((c0 + base) * H + e) * DV, ps.bytes(m, H, DV, ES));
 #pragma unroll

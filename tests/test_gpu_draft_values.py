@@ -76,3 +76,56 @@ def test_a_write_stays_out_of_its_own_record(name, value, dtype):
     near("p", p[upto], rp[upto])
     before = [t for t in upto if t not in rows]
     near("o", o[before], ro[before])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_later_gates_that_overflow(dtype):
+    """Each gate is in range, their product over tokens 2..7 is 2^180: tokens before them stay."""
+    d, cu, cu_t, S, hist = make([9, 5, 18], dk=64, dv=64, dtype=dtype, seed=21)
+    d["g"][2:8, 0] = 2.0 ** 30
+    d["g"][14 + 10:14 + 16, 0] = 2.0 ** 30
+    o, kw, p = run(d, cu_t, 4, S, hist)
+    ro, rkw, rp, _ = reference(d, cu, 4, S, hist)
+    near("kw", kw, rkw)
+    for first, n in ((0, 2), (9, 5), (14, 10)):
+        near("o", o[first:first + n], ro[first:first + n])
+        near("p", p[first:first + n], rp[first:first + n])
+    near("o of the other head", o[:, 1], ro[:, 1])
+    near("p of the other head", p[:, 1], rp[:, 1])
+    commit_near(d, cu, cu_t, [2, 5, 10], kw, p, S, hist)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_later_keys_that_overflow_with_the_state(dtype):
+    """A state of 1e30 and a later key of 4e8, whose product is beyond fp32: tokens before it stay."""
+    d, cu, cu_t, S, hist = make([9, 5, 18], dk=64, dv=64, dtype=dtype, seed=22)
+    S *= 3e30
+    for row in (6, 14 + 12):
+        d["k"][row, 0, 3] = 4e8
+    o, kw, p = run(d, cu_t, 4, S, hist)
+    ro, rkw, rp, _ = reference(d, cu, 4, S, hist)
+    assert (rp[6].abs() > 3.5e38).any()
+    for first, n in ((0, 6), (9, 5), (14, 12)):
+        near("o", o[first:first + n], ro[first:first + n])
+        near("p", p[first:first + n], rp[first:first + n])
+    commit_near(d, cu, cu_t, [6, 5, 12], kw, p, S, hist)
+
+
+@pytest.mark.parametrize("name,value", [("k", 1e25), ("k", -1e38), ("b", float("inf")), ("b", float("nan")), ("b", 1e30),
+                                        ("g", float("inf")), ("g", 1e38), ("v", 3e38)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_later_values_beyond_products(name, value, dtype):
+    """A value of a later token that is not finite or overflows any product with it, twice in a
+    sequence: tokens before the first one stay, and so does the other head."""
+    d, cu, cu_t, S, hist = make([8, 9, 20], dk=128, dv=128, dtype=dtype, seed=23)
+    for row in (5, 6, 17 + 11, 17 + 14):
+        d[name][(row, 0, 3) if d[name].dim() == 3 else (row, 0)] = value
+    o, kw, p = run(d, cu_t, 4, S, hist)
+    ro, rkw, rp, _ = reference(d, cu, 4, S, hist)
+    for first, n in ((0, 5), (8, 9), (17, 11)):
+        near("o", o[first:first + n], ro[first:first + n])
+        near("p", p[first:first + n], rp[first:first + n])
+        near("kw", kw[first:first + n], rkw[first:first + n])
+    near("o of the other head", o[:, 1], ro[:, 1])
+    near("p of the other head", p[:, 1], rp[:, 1])
+    commit_near(d, cu, cu_t, [5, 9, 11], kw, p, S, hist)
