@@ -309,9 +309,8 @@ template <typename T, int DK, int DV, int LEV, bool GELU> struct WriteKey {
             hr[l] = X::template load4<kOnce>(h, l0 + l < L - 2 ? la : kOutside);
         }
     }
-    __device__ void fetch(uint32_t t, uint32_t ch)
+    __device__ void fetch_taps(uint32_t t, uint32_t ch)
     {
-        fetch_levels(t, ch, 0);
         kr = X::load4(ps.k, (t * ps.krow + ch) * ES);
 #pragma unroll
         for (int d = 1; d <= 3; ++d) {
@@ -324,10 +323,16 @@ template <typename T, int DK, int DV, int LEV, bool GELU> struct WriteKey {
             wr[x] = X::load4(w, (ch + x) * 4 * ES);
         br = X::load1(ps.b, t * ps.grow * ES);
     }
-    __device__ f32x4_t form(uint32_t t, uint32_t ch, f32x4_t& kt)
+    __device__ void fetch(uint32_t t, uint32_t ch)
+    {
+        fetch_levels(t, ch, 0);
+        fetch_taps(t, ch);
+    }
+    // the ShortConv anchor r and b k
+    __device__ void start(f32x4_t& kt, f32x4_t& r, f32x4_t& acc)
     {
         kt = X::f32(kr);
-        f32x4_t x[3], r, acc;
+        f32x4_t x[3];
 #pragma unroll
         for (int d = 0; d < 3; ++d)                      // one of the two is zero
             x[d] = X::f32(pr[d] | hi[d]);
@@ -338,6 +343,11 @@ template <typename T, int DK, int DV, int LEV, bool GELU> struct WriteKey {
             r[c] = wc[3] * kt[c] + wc[2] * x[0][c] + wc[1] * x[1][c] + wc[0] * x[2][c];
             acc[c] = bt * kt[c];
         }
+    }
+    __device__ f32x4_t form(uint32_t t, uint32_t ch, f32x4_t& kt)
+    {
+        f32x4_t r, acc;
+        start(kt, r, acc);
         for (int l0 = 0; LEV > 0 && l0 < L - 1; l0 += LV) {
             if (l0 > 0)
                 fetch_levels(t, ch, l0);
@@ -352,7 +362,29 @@ template <typename T, int DK, int DV, int LEV, bool GELU> struct WriteKey {
                 }
             }
         }
+        if (LEV > 0 && !(acc[0] * 0.f + acc[1] * 0.f + acc[2] * 0.f + acc[3] * 0.f == 0.f))
+            acc = form_by_level(t, ch);
         E32::store4(ps.kw, (t * ps.krow + ch) * 4, acc);
+        return acc;
+    }
+    // The same where it is not finite: level by level as the recurrence has it, so that an infinite r is
+    // neither met by the zeros past the last level nor taken from itself
+    __device__ f32x4_t form_by_level(uint32_t t, uint32_t ch)
+    {
+        f32x4_t kt, r, acc;
+        fetch_taps(t, ch);
+        start(kt, r, acc);
+#pragma unroll 1
+        for (int l = 0; l < L - 1; ++l) {
+            const uint32_t at = ((t * ps.krow * (L - 1) + ch) + l * DK) * ES;
+            const f32x4_t av = X::f32(X::load4(a, at)), uv = X::f32(X::load4(u, at)), hv = X::f32(X::load4(h, at));
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                acc[c] += av[c] * r[c] * uv[c];
+                if (l < L - 2)
+                    r[c] = GELU ? r[c] - av[c] * gelu_as(hv[c] * r[c]) : r[c] * (1.f - av[c] * hv[c]);
+            }
+        }
         return acc;
     }
 };
@@ -430,6 +462,7 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
     for (int base = 0, m; base < len; base += m) {
         // what derives from the sizes is formed in each pass: kept over them it is spilled
         const int H = again(heads), L = again(levels);
+        __builtin_assume(LEV == 0 || L > 1);             // as launched: no branch parts a token's loads
         const int tid = opaque(threadIdx.x), lane = tid & 63, kq = lane >> 4, j = lane & 15;
         const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = 32 * wave + 2 * j;
         m = len - base < kBlock ? len - base : kBlock;

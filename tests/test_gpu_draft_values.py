@@ -129,3 +129,25 @@ def test_later_values_beyond_products(name, value, dtype):
     near("o of the other head", o[:, 1], ro[:, 1])
     near("p of the other head", p[:, 1], rp[:, 1])
     commit_near(d, cu, cu_t, [5, 9, 11], kw, p, S, hist)
+
+
+@pytest.mark.parametrize("L,residual", [(2, "linear"), (3, "linear"), (4, "linear"), (6, "linear"), (8, "linear"),
+                                        (9, "linear"), (12, "linear"), (2, "gelu"), (3, "gelu"), (6, "gelu")])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_write_keys_of_infinite_keys(dtype, L, residual):
+    """An infinite k (positive levels and taps) gives the infinities and NaN that the recurrence
+    has, in its channel of four tokens: no level beyond the last one takes part.  12 tokens: the
+    second pass forms its write keys elsewhere."""
+    import torch
+    d, cu, cu_t, S, hist = make([12, 3], dk=64, dv=64, L=L, dtype=dtype, seed=31)
+    for name in ("u", "conv_w"):
+        d[name] = d[name].abs() + 2.0 ** -6
+    for row, value in ((2, "inf"), (8, "-inf")):
+        d["k"][row, 0, 5] = float(value)
+    kw = run(d, cu_t, L, S, hist, residual=residual)[1].cpu().double()
+    want = reference(d, cu, L, S, hist, residual)[1]
+    assert torch.equal(torch.isnan(kw), torch.isnan(want))
+    assert torch.equal(torch.isinf(kw) * torch.sign(kw).nan_to_num(), torch.isinf(want) * torch.sign(want).nan_to_num())
+    fine = torch.isfinite(want)
+    assert (~fine).sum() == 8
+    assert ((kw - want)[fine].abs().max() <= 1e-5 * want[fine].abs().max())
