@@ -28,6 +28,18 @@ from . import binding
 _INPUTS = ("q", "k", "v", "u", "g", "b", "a", "h", "conv_w")
 
 
+def _aligned(t):
+    """t as the kernels take it: contiguous, from an address that is a multiple of 16 (autograd
+    hands out slices, as for a concatenation, that begin at any element)."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
+def _upstream(grad, like):
+    """An upstream gradient as the kernels take it, or None."""
+    return None if grad is None else _aligned(grad.to(like.dtype))
+
+
 class PrismFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, u, g, b, a, h, conv_w, cu_seqlens, L, S_init, residual):
@@ -52,8 +64,8 @@ class PrismFunction(torch.autograd.Function):
         q, k, v, u, g, b, a, h, conv_w, cu_seqlens, S_init, ckpt = ctx.saved_tensors
         if not ctx.has_s_init:
             S_init = None
-        d_o = torch.zeros_like(v) if d_o is None else d_o.to(v.dtype).contiguous()
-        d_s = None if d_s is None else d_s.to(torch.float32).contiguous()
+        d_o = torch.zeros_like(v) if d_o is None else _upstream(d_o, v)
+        d_s = None if d_s is None else _aligned(d_s.to(torch.float32))
         want_s = ctx.has_s_init and ctx.needs_input_grad[11]
         args = (q, k, v, u, g, b, a, h, conv_w, cu_seqlens, ctx.L, d_o)
         kw = dict(dS_final=d_s, S_init=S_init, want_dS_init=want_s, residual=ctx.residual)
@@ -78,11 +90,6 @@ class PrismFunction(torch.autograd.Function):
 def prism(q, k, v, u, g, b, a, h, conv_w, cu_seqlens, L: int, S_init=None, residual="linear"):
     """Differentiable forward pass: returns (o, S_final)."""
     return PrismFunction.apply(q, k, v, u, g, b, a, h, conv_w, cu_seqlens, L, S_init, residual)
-
-
-def _upstream(grad, like):
-    """An upstream gradient as the kernels take it, or None."""
-    return None if grad is None else grad.to(like.dtype).contiguous()
 
 
 class NormResidualFunction(torch.autograd.Function):
