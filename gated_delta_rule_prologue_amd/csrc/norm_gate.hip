@@ -23,10 +23,25 @@ namespace prism {
 
 using rows::group_sum;
 
-// act(z), and with GRAD act'(z): s = 1 / (1 + e^-z); silu = z s, silu' = s (1 + z (1 - s))
-template <int GATE> __device__ __forceinline__ float gate_act(float z, float& slope)
+// e^-a for a >= 0 (a NaN stays one).  exp2 of the rounded product a log2 e is off by up to 64
+// half steps of fp32 at a = 80.  That is nothing beside bf16's own rounding (2^-18 of the value
+// against 2^-9); in fp32 it is 2^n 2^f with n + f = -a log2 e, |f| <= 1/2 and log2 e in two
+// parts, so that f is rounded once and the error does not grow with a.
+template <typename T> __device__ __forceinline__ float exp_minus(float a)
 {
-    const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
+    if constexpr (sizeof(T) == 2)
+        return __builtin_amdgcn_exp2f(a * -1.44269504088896341f);
+    const float n = fmaxf(rintf(a * -1.44269504088896341f), -200.f);     // beyond it f takes the rest, and e^-a is zero
+    const float f = __builtin_fmaf(a, -1.925962991e-8f, __builtin_fmaf(a, -1.44269502162933350f, -n));
+    return ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
+}
+
+// act(z) and act'(z): s = 1 / (1 + e^-z), formed from e^-|z| <= 1; silu = z s,
+// silu' = s (1 + z (1 - s))
+template <typename T, int GATE> __device__ __forceinline__ float gate_act(float z, float& slope)
+{
+    const float e = exp_minus<T>(fabsf(z)), d = __builtin_amdgcn_rcpf(1.f + e);
+    const float s = z < 0.f ? e * d : d;
     if (GATE == 0) {
         slope = s * (1.f + z * (1.f - s));
         return z * s;
@@ -66,7 +81,7 @@ __global__ __launch_bounds__(S::THREADS) void norm_gate_kernel(
 #pragma unroll
         for (int c = 0; c < S::E; ++c) {
             float slope;
-            ov[c] = ov[c] * rstd * wv[c] * gate_act<GATE>(zv[c], slope);
+            ov[c] = ov[c] * rstd * wv[c] * gate_act<typename S::elem, GATE>(zv[c], slope);
         }
         sh.store(y + at, ov);
     }
@@ -104,7 +119,7 @@ __global__ __launch_bounds__(S::THREADS) void norm_gate_bwd_kernel(
 #pragma unroll
         for (int c = 0; c < S::E; ++c) {
             float slope;
-            const float act = gate_act<GATE>(zv[c], slope);
+            const float act = gate_act<typename S::elem, GATE>(zv[c], slope);
             zv[c] = dv[c] * wv[c] * slope * ov[c];       // dz, but for rstd
             dv[c] *= act;                                // dy act(z)
             ss[0] += ov[c] * ov[c];
