@@ -36,17 +36,18 @@ template <typename T> __device__ __forceinline__ float exp_minus(float a)
     return ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
 }
 
-// act(z) and act'(z): s = 1 / (1 + e^-z), formed from e^-|z| <= 1; silu = z s,
-// silu' = s (1 + z (1 - s))
+// act(z) and act'(z): s = 1 / (1 + e^-z) and c = 1 - s = 1 / (1 + e^z), both formed from
+// e^-|z| <= 1 (a difference 1 - s would lose c of open gates: 6 % at z = 16, all of it from 18 on);
+// silu = z s, silu' = s (1 + z c)
 template <typename T, int GATE> __device__ __forceinline__ float gate_act(float z, float& slope)
 {
     const float e = exp_minus<T>(fabsf(z)), d = __builtin_amdgcn_rcpf(1.f + e);
-    const float s = z < 0.f ? e * d : d;
+    const float s = z < 0.f ? e * d : d, c = z < 0.f ? d : e * d;
     if (GATE == 0) {
-        slope = s * (1.f + z * (1.f - s));
+        slope = s * (1.f + z * c);
         return z * s;
     }
-    slope = s * (1.f - s);
+    slope = s * c;
     return s;
 }
 

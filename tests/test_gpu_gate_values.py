@@ -71,3 +71,18 @@ def test_activation_of_infinite_gates():
         y = B.norm_gate(o, z, w, eps=0.0)[0, :7].float().cpu()
         assert y[0] == float("inf") and torch.isnan(y[1:3]).all()
         assert y[3:].tolist() == [torch.finfo(dt).max, 0.0, 0.0, 0.0]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("gate", ["silu", "sigmoid"])
+def test_slope(gate, dtype):
+    """dz of gates that are nearly open or shut: s (1 - s), and s (1 + z (1 - s)), whose magnitude
+    is s (1 + |z| (1 - s)) where its terms cancel (near z = -1.28)."""
+    import torch
+    from gated_delta_rule_prologue_amd import binding as B
+    o, z, w = gates({"bf16": torch.bfloat16, "f32": torch.float32}[dtype])
+    g = B.norm_gate_bwd(o, z, w, torch.ones_like(o), eps=0.0, gate=gate)
+    z6, s, c = f64(z), torch.sigmoid(f64(z)), torch.sigmoid(-f64(z))
+    want = s * (1 + z6 * c) if gate == "silu" else s * c
+    mag = s * (1 + z6.abs() * c) if gate == "silu" else s * c
+    within(f"slope of {gate} {dtype}", g["z"], f64(o) * want, mag, z6)
