@@ -2,9 +2,9 @@
 
 Each source compiles to an object under ``_build/`` in parallel, then the
 objects link into ``gated_delta_rule_prologue_amd/libprism.so``.  The library
-exports only the C ABI of ``include/prism.h``.  The Python calls of the layer
-operators (``csrc/torch_calls.cpp``) build into ``_calls.so`` beside it, a CPython
-module linked to it and to torch.
+exports only the C ABI of ``include/prism.h`` and needs hipcc alone.  The Python calls
+of the layer operators (``csrc/torch_calls.cpp``) build into ``_calls.so`` beside it, a
+CPython module linked to it and to torch, where torch can be imported.
 """
 from __future__ import annotations
 
@@ -66,9 +66,17 @@ def _run(cmd, verbose):
         print(out, flush=True)
 
 
-def _calls_cmd(out: str, link: bool):
+def _torch():
+    """The torch module, or None where there is none."""
+    try:
+        import torch
+    except (ImportError, OSError):                 # OSError: a library that torch loads is missing
+        return None
+    return torch
+
+
+def _calls_cmd(torch, out: str, link: bool):
     """Compile (or link) torch_calls.cpp: host code only."""
-    import torch
     torch_dir = os.path.dirname(torch.__file__)
     obj = os.path.join(BUILD, "torch_calls.o")
     if not link:
@@ -91,13 +99,14 @@ def build(verbose: bool = False, extra_flags=()) -> str:
         obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
         objs.append(obj)
         cmds.append([hipcc, *HIPCC_FLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj])
-    cmds.append(_calls_cmd(CALLS, link=False))
     # device assembly of the MFMA kernels, for the machine-code check below
     asm = {src: os.path.join(BUILD, os.path.splitext(src)[0] + ".s") for src in CHECKED}
     for src, out in asm.items():
         cmds.append([hipcc, *HIPCC_FLAGS, *extra_flags, "-S", "--cuda-device-only",
                      os.path.join(CSRC, src), "-o", out])
-    with ThreadPoolExecutor(max_workers=len(cmds)) as ex:
+    torch = _torch()
+    with ThreadPoolExecutor(max_workers=len(cmds) + 1) as ex:
+        calls = ex.submit(lambda: _run(_calls_cmd(torch, CALLS, link=False), verbose)) if torch else None
         list(ex.map(lambda c: _run(c, verbose), cmds))
     for src, out in asm.items():
         text = open(out).read()
@@ -115,8 +124,15 @@ def build(verbose: bool = False, extra_flags=()) -> str:
     _run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-Wl,-soname,libprism.so", *objs,
           "-o", tmp], verbose)
     os.replace(tmp, LIB)
+    if os.path.exists(CALLS):                      # an earlier one may not fit the new library
+        os.remove(CALLS)
+    if calls is None:
+        print("torch cannot be imported: _calls.so (the Python calls of the layer operators) is not built",
+              flush=True)
+        return LIB
+    calls.result()
     tmp = CALLS + ".tmp%d" % os.getpid()
-    _run(_calls_cmd(tmp, link=True), verbose)
+    _run(_calls_cmd(torch, tmp, link=True), verbose)
     os.replace(tmp, CALLS)
     return LIB
 
