@@ -38,13 +38,15 @@
 // keeps to that: 256 sequences x 6 heads, dk = dv = 128, 5 of 8 tokens kept at the mean,
 // 210 MB in 41 us, 5.1 TB/s.  The draft of one pass is two or three
 // dependent reads, a barrier, the small matrices and the products, and a batch of 1500 to 4000 chains is
-// only two rounds of the workgroups that the registers let run at a time (120 a lane,
-// four wavefronts a SIMD), so that loads and products of one round overlap in part: the same
-// batch, 1 to 8 tokens, 131 MB in 31.4 us, 4.2 TB/s; 512 x 8 heads of 64 x 64 with
-// L = 8, 38 us for 8 tokens (5.0 TB/s) and 69 us for 9, whose second pass reads the
-// state again; 8 x 6 heads of 5 tokens, 8.2 us (a launch alone: 3.8).
+// only two rounds of the workgroups that the registers let run at a time (up to 128 a lane
+// and four wavefronts a SIMD in bf16 and at L = 1; 129 to 159 and three in fp32 with levels, and in bf16
+// with the GELU chain beyond L = 4), so that loads and products of one round overlap in part: the same
+// batch, 1 to 8 tokens, 131 MB in 29.4 us, 4.5 TB/s; 512 x 8 heads of 64 x 64 with
+// L = 8, 37 us for 8 tokens (5.1 TB/s) and 66 us for 9, whose second pass reads the
+// state again; 8 x 6 heads of 5 tokens, 7.1 us (a launch alone: 3.8).  In fp32 those two batches
+// take 32 us (156 MB, 4.9 TB/s) and 57 us (297 MB, 5.2 TB/s) for up to 8 tokens.
 // Long sequences are walked all the same, with the square of the passes: 32 x 8
-// heads (64 x 64) take 7.4, 100, 1520 and 25,000 us for 8, 64, 256 and 1024 tokens.
+// heads (64 x 64) take 8.5, 94, 1380 and 23,000 us for 8, 64, 256 and 1024 tokens.
 //
 // Layout.  One workgroup per chain, one wavefront per 32 value columns; of the
 // state, lane (kq, j) = (lane / 16, lane % 16) takes rows 16 R + 4 kq + r and the
@@ -391,7 +393,7 @@ template <typename T, int DK, int DV, int LEV, bool GELU> struct WriteKey {
 
 // The draft kernel's arguments, read from the kernel's argument segment where they are used:
 // held in scalar registers over the pass loop (30 of them beside the buffer resources)
-// they were spilled into vector lanes.
+// they were spilled into vector lanes, as 10 to 23 scalars of the instances with levels still are.
 template <typename T> struct DraftPointers {
     const T *q, *k, *v, *u, *a, *h, *g, *b, *conv_w;
     const int32_t* cu;
@@ -486,8 +488,8 @@ __global__ __launch_bounds__(2 * DV, 3) void draft_kernel(DraftPointers<T>)
             f32x4_t kt = {}, wt = {};
             const typename X::raw4 qr = X::load4(ps.q, (t * ps.krow + ch) * ES);
             if (LEV > 0 && t >= m) {
-                // no token: zero rows without the chain (4 of 8 tokens, L = 8: 31.8 instead of 32.9
-                // us; at L = 1, where there is none, the branch costs more: 25.5 instead of 24.6)
+                // no token: zero rows without the chain (4 of 8 tokens, L = 8: 3 % less time; at
+                // L = 1, where there is none, the branch costs 4 %)
             } else if (!staged) {
                 WriteKey<T, DK, DV, LEV, GELU> key(ps, ap->k, ap->u, ap->a, ap->h, ap->conv_w, ap->k_hist, chain, c0,
                                                      base, m, H, e, L);

@@ -6,15 +6,15 @@
 //   do = rstd (e - oh mean(e oh)),   dz = dy oh w act'(z),   dw = sum dy act(z) oh.
 // w is one row for all heads, or one a head; dw is summed accordingly.
 //
-// Bound by HBM (3 streams forward, 5 backward, up to 26 operations an
+// Bound by HBM (3 streams forward, 5 backward, up to some 40 operations an
 // element).  A head's row is a few hundred bytes, held by 8 to 64 lanes, so a
 // wavefront works on several rows at once and the row sums stay within it.
 // With a weight a head a workgroup keeps to one head (w and the column sums
 // stay in its registers); its rows are then H rows apart, each of them at least
 // a whole 64-byte segment at the operator's widths.  Forward of 65,536 tokens x 16 heads
-// x 128 in bf16: 805 MB in 160 us, 5.0 TB/s (a copy of a gigabyte: 5.2); backward of
-// 65,536 tokens x 4 heads x 64: 168 MB in 35 us, 4.8 TB/s, of which the second
-// launch takes 4.  Outputs may be the inputs' own buffers.
+// x 128 in bf16: 805 MB in 161 us, 5.0 TB/s (a copy of a gigabyte: 5.2); backward of
+// 65,536 tokens x 4 heads x 64: 168 MB in 36 us, 4.7 TB/s, of which the second
+// launch takes 4.  In fp32 65,536 x 4 x 128 takes 80 us forward and 124 us backward.  Outputs may be the inputs' own buffers.
 #include "common.h"
 #include "kernels.h"
 #include "norm_rows.h"

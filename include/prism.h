@@ -528,7 +528,8 @@ prism_status prism_norm_gate_bwd(const prism_norm_dims* d, const void* o, const 
  * The write key is kept in fp32 (as in prism_decode_step).  dk, dv in {64, 128} and
  * H * max(dk (L - 1), dv) <= 48,000,000 and 2 dv n_seqs H < 2^32, else
  * PRISM_EUNSUPPORTED.  A token's outputs
- * depend on the tokens up to it only, also where later ones hold infinities or NaN.
+ * depend on the tokens up to it only, also where later ones hold infinities or NaN, or
+ * overflow; its q reaches its o alone, its v and write key no p but those of later tokens.
  * No workspace.
  */
 prism_status prism_decode_draft(const prism_dims* d,
