@@ -25,7 +25,7 @@ using rows::group_sum;
 
 // e^-a for a >= 0 (a NaN stays one).  exp2 of the rounded product a log2 e is off by up to 64
 // half steps of fp32 at a = 80.  That is nothing beside bf16's own rounding (2^-18 of the value
-// against 2^-9); in fp32 it is 2^n 2^f with n + f = -a log2 e, |f| <= 1/2 and log2 e in two
+// against 2^-8); in fp32 it is 2^n 2^f with n + f = -a log2 e, |f| <= 1/2 and log2 e in two
 // parts, so that f is rounded once and the error does not grow with a.
 template <typename T> __device__ __forceinline__ float exp_minus(float a)
 {
