@@ -17,6 +17,11 @@ The norms around the operator, differentiable in every tensor they take:
 
     n, r = norm_residual(x, w, y=None, scale=None, eps=1e-6)
     y = norm_gate(o, z, w, eps=1e-6, gate="silu")
+
+The steps in front of it, differentiable in x, w, bias and hist, and in q, k, wq and wk:
+
+    y = short_conv(x, w, cu_seqlens, bias=None, activation="silu", hist=None)
+    q, k = qk_norm(q, k, wq=None, wk=None, norm="l2", ...)
 """
 from __future__ import annotations
 
@@ -148,3 +153,59 @@ class NormGateFunction(torch.autograd.Function):
 def norm_gate(o, z, w, eps: float = 1e-6, gate: str = "silu"):
     """Differentiable binding.norm_gate: returns y."""
     return NormGateFunction.apply(o, z, w, eps, gate)
+
+
+class ShortConvFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, bias, hist, cu_seqlens, activation):
+        y, _ = binding.short_conv(x, w, cu_seqlens, bias=bias, activation=activation, hist=hist)
+        ctx.save_for_backward(x, w, bias, hist, cu_seqlens)
+        ctx.activation = activation
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, w, bias, hist, cu_seqlens = ctx.saved_tensors
+        want = ctx.needs_input_grad
+        grads = binding.short_conv_bwd(x, w, cu_seqlens, _upstream(dy, x), bias=bias, activation=ctx.activation,
+                                       hist=hist, want_dhist=want[3])
+        return (grads["x"] if want[0] else None, grads["w"].to(w.dtype) if want[1] else None,
+                grads["bias"].to(bias.dtype) if want[2] else None, grads["hist"] if want[3] else None, None, None)
+
+
+def short_conv(x, w, cu_seqlens, bias=None, activation="silu", hist=None):
+    """Differentiable binding.short_conv: returns y.  No gradient reaches ``hist`` from a history
+    carried out: sequences cut into pieces are trained piece by piece."""
+    return ShortConvFunction.apply(x, w, bias, hist, cu_seqlens, activation)
+
+
+class QkNormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, wq, wk, positions, freqs, how):
+        q_out, k_out = binding.qk_norm(q, k, wq, wk, positions=positions, freqs=freqs, **how)
+        ctx.save_for_backward(q, k, wq, wk, positions, freqs)
+        ctx.how = how
+        return q_out if k is None else (q_out, k_out)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq, dk=None):
+        q, k, wq, wk, positions, freqs = ctx.saved_tensors
+        grads = binding.qk_norm_bwd(q, _upstream(dq, q), k, None if k is None else _upstream(dk, k), wq, wk,
+                                    positions=positions, freqs=freqs, **ctx.how)
+        want = ctx.needs_input_grad
+        return (grads["q"] if want[0] else None, grads["k"] if want[1] else None,
+                grads["wq"].to(wq.dtype) if want[2] else None, grads["wk"].to(wk.dtype) if want[3] else None,
+                None, None, None)
+
+
+def qk_norm(q, k=None, wq=None, wk=None, norm="l2", eps: float = 1e-6, positions=None, freqs=None, layout="half",
+            rot_scale: float = 1.0):
+    """Differentiable binding.qk_norm: returns (q, k).  Frequencies take no gradient."""
+    if freqs is not None and freqs.requires_grad:
+        raise ValueError("no gradient is formed for freqs")
+    how = dict(norm=norm, eps=eps, layout=layout, rot_scale=rot_scale)
+    if k is None:
+        return QkNormFunction.apply(q, None, wq, wk, positions, freqs, how), None
+    return QkNormFunction.apply(q, k, wq, wk, positions, freqs, how)

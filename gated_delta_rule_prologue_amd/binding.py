@@ -15,7 +15,9 @@ with a residual choice), ``scan_wait_giveups`` -> prism_scan_wait_giveups.
 The layer around the operator: ``norm_residual`` / ``norm_residual_bwd`` ->
 prism_norm_residual(_bwd), ``norm_gate`` / ``norm_gate_bwd`` -> prism_norm_gate(_bwd),
 ``decode_draft`` -> prism_decode_draft, ``decode_commit`` -> prism_decode_commit,
-``verify_draft`` -> prism_verify_draft.  These calls are checked and marshalled in C++
+``verify_draft`` -> prism_verify_draft.  In front of it and behind the model's last product:
+``short_conv`` / ``short_conv_step`` / ``short_conv_bwd`` -> prism_short_conv(_step, _bwd), ``qk_norm`` /
+``qk_norm_bwd`` -> prism_qk_norm(_bwd), ``sample`` -> prism_sample.  These calls are checked and marshalled in C++
 (csrc/torch_calls.cpp) and run on the device of their tensors whichever is
 current, on ``stream`` or that device's current stream; what they allocate
 belongs to the stream they run on.
@@ -23,6 +25,7 @@ belongs to the stream they run on.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -37,6 +40,9 @@ PRISM_F32, PRISM_BF16 = 0, 1
 RESIDUAL = {"linear": 0, "gelu": 1}          # prism_residual
 MAX_LEVELS = 16
 GATE = {"silu": 0, "sigmoid": 1}             # prism_gate
+ACTIVATION = {None: 0, "silu": 1}            # prism_activation
+QK_NORM = {"none": 0, "rms": 1, "l2": 2}     # prism_qk_kind
+ROT_LAYOUT = {"half": 0, "interleaved": 1}   # prism_rot_layout
 
 
 class PrismError(RuntimeError):
@@ -54,6 +60,23 @@ class Dims(ctypes.Structure):
 class NormDims(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("heads", ctypes.c_int32), ("width", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
+
+
+class ConvDims(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("total_tokens", ctypes.c_int32), ("channels", ctypes.c_int32),
+                ("taps", ctypes.c_int32), ("dtype", ctypes.c_int32), ("x_stride", ctypes.c_int64)]
+
+
+class QkDims(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("heads_q", ctypes.c_int32), ("heads_k", ctypes.c_int32),
+                ("width", ctypes.c_int32), ("rot", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64)]
+
+
+class SampleDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("vocab", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("stride", ctypes.c_int64)]
 
 
 class VerifyDims(ctypes.Structure):
@@ -130,6 +153,25 @@ def lib():
         L.prism_verify_workspace_bytes.restype = S
         L.prism_verify_draft.argtypes = [V] + [P] * 9 + [S, P]
         L.prism_verify_draft.restype = I
+        C, Q, M = ctypes.POINTER(ConvDims), ctypes.POINTER(QkDims), ctypes.POINTER(SampleDims)
+        L.prism_conv_workspace_bytes.argtypes = [C]
+        L.prism_conv_workspace_bytes.restype = S
+        L.prism_short_conv.argtypes = [C, P, P, P, P, P, I, P, P, P]
+        L.prism_short_conv.restype = I
+        L.prism_short_conv_step.argtypes = [C, P, P, P, P, I, P, P, P]
+        L.prism_short_conv_step.restype = I
+        L.prism_short_conv_bwd.argtypes = [C, P, P, P, P, P, I] + [P] * 6 + [S, P]
+        L.prism_short_conv_bwd.restype = I
+        L.prism_qk_workspace_bytes.argtypes = [Q]
+        L.prism_qk_workspace_bytes.restype = S
+        L.prism_qk_norm.argtypes = [Q, P, P, P, P, I, F, P, P, I, F, P, P, P]
+        L.prism_qk_norm.restype = I
+        L.prism_qk_norm_bwd.argtypes = [Q, P, P, P, P, I, F, P, P, I, F] + [P] * 7 + [S, P]
+        L.prism_qk_norm_bwd.restype = I
+        L.prism_sample_workspace_bytes.argtypes = [M]
+        L.prism_sample_workspace_bytes.restype = S
+        L.prism_sample.argtypes = [M] + [P] * 9 + [S, P]
+        L.prism_sample.restype = I
         L.prism_abi_version.argtypes = []
         L.prism_abi_version.restype = I
         _lib = L
@@ -534,7 +576,7 @@ def verify_workspace_bytes(dims: VerifyDims) -> int:
 
 def _choice(name: str, table: dict, value) -> int:
     if value not in table:
-        raise ValueError(f"{name} must be one of {sorted(table)}")
+        raise ValueError(f"{name} must be one of {sorted(table, key=str)}")
     return table[value]
 
 
@@ -621,6 +663,124 @@ def verify_draft(p, tokens, cu_seqlens, u_accept, u_sample, q=None, n_accept=Non
                                 workspace)
     return _layer().verify_draft(p, tokens, cu_seqlens, u_accept, u_sample, q, n_accept, next_token,
                                  workspace)
+
+
+# ---------------------------------------------------------------- in front of the operator, behind the last product
+
+
+def conv_workspace_bytes(dims: ConvDims) -> int:
+    return int(lib().prism_conv_workspace_bytes(ctypes.byref(dims)))
+
+
+def qk_workspace_bytes(dims: QkDims) -> int:
+    return int(lib().prism_qk_workspace_bytes(ctypes.byref(dims)))
+
+
+def sample_workspace_bytes(dims: SampleDims) -> int:
+    return int(lib().prism_sample_workspace_bytes(ctypes.byref(dims)))
+
+
+def short_conv(x, w, cu_seqlens, bias=None, activation: Optional[str] = "silu", hist=None, hist_out=None, y=None,
+               stream=None):
+    """Causal depthwise convolution of packed sequences, act(bias + sum_m w[c, m] x[t - K + 1 + m])
+    (prism_short_conv): ``x`` [T, C] (any row stride: the columns of a wider tensor), ``w`` [C, K], K <= 8, tap
+    K - 1 on the token itself, ``bias`` [C], ``activation`` "silu" or None, ``hist`` [N, K - 1, C] the rows in
+    front of every sequence (None: zero).  ``hist_out`` (may be ``hist``) receives the history to
+    carry on.  Rows of ``y`` behind the last sequence are not written.  Returns (y, hist_out)."""
+    if stream is not None:
+        with _on(x, stream):
+            return short_conv(x, w, cu_seqlens, bias, activation, hist, hist_out, y)
+    act = _choice("activation", ACTIVATION, activation)
+    return _layer().short_conv(x, w, cu_seqlens, bias, act, hist, hist_out, y), hist_out
+
+
+def short_conv_step(x, w, hist, bias=None, activation: Optional[str] = "silu", hist_out=None, y=None, stream=None):
+    """short_conv for one new token a sequence (prism_short_conv_step): ``x`` [N, C] with the history
+    ``hist`` [N, K - 1, C], which is moved on in place unless ``hist_out`` is given.
+    Returns (y, hist_out)."""
+    if stream is not None:
+        with _on(x, stream):
+            return short_conv_step(x, w, hist, bias, activation, hist_out, y)
+    act = _choice("activation", ACTIVATION, activation)
+    return (_layer().short_conv_step(x, w, hist, bias, act, hist_out, y), hist if hist_out is None else hist_out)
+
+
+def short_conv_bwd(x, w, cu_seqlens, dy, bias=None, activation: Optional[str] = "silu", hist=None, workspace=None,
+                   want_dhist: bool = True, stream=None) -> dict:
+    """Gradients of short_conv for the gradient ``dy`` [T, C] of y (prism_short_conv_bwd): a dict of x
+    (input dtype, zero behind the last sequence), w [C, K] and bias [C] (fp32; bias None without
+    one) and hist (input dtype; None without one or with ``want_dhist`` false)."""
+    if stream is not None:
+        with _on(x, stream):
+            return short_conv_bwd(x, w, cu_seqlens, dy, bias, activation, hist, workspace, want_dhist)
+    dx, dw, db, dh = _layer().short_conv_bwd(x, w, cu_seqlens, dy, bias, _choice("activation", ACTIVATION, activation),
+                                             hist, workspace, want_dhist)
+    return {"x": dx, "w": dw, "bias": db, "hist": dh}
+
+
+def qk_norm(q, k=None, wq=None, wk=None, norm: str = "l2", eps: float = 1e-6, positions=None, freqs=None,
+            layout: str = "half", rot_scale: float = 1.0, q_out=None, k_out=None, stream=None):
+    """Every head's query and key normalised, weighted and rotated by its position
+    (prism_qk_norm): ``q`` [T, Hq, d], ``k`` [T, Hk, d] or None, with any strides of tokens and heads;
+    ``norm`` "l2", "rms" or "none"; ``wq``, ``wk`` [d] (both or neither); ``positions`` int32 [T] and ``freqs`` fp32
+    [rot / 2] (rotary_freqs) turn the first rot elements, pairs (i, i + rot / 2) with ``layout``
+    "half", (2 i, 2 i + 1) with "interleaved", and multiply them by ``rot_scale``.  ``q_out``,
+    ``k_out`` may be given, also as dense q and k.  Returns (q_out, k_out)."""
+    if stream is not None:
+        with _on(q, stream):
+            return qk_norm(q, k, wq, wk, norm, eps, positions, freqs, layout, rot_scale, q_out, k_out)
+    return _layer().qk_norm(q, k, wq, wk, _choice("norm", QK_NORM, norm), eps, positions, freqs,
+                            _choice("layout", ROT_LAYOUT, layout), rot_scale, q_out, k_out)
+
+
+def qk_norm_bwd(q, dq_out, k=None, dk_out=None, wq=None, wk=None, norm: str = "l2", eps: float = 1e-6, positions=None,
+                freqs=None, layout: str = "half", rot_scale: float = 1.0, workspace=None, stream=None) -> dict:
+    """Gradients of qk_norm for the gradients ``dq_out``, ``dk_out`` (contiguous) of its outputs
+    (prism_qk_norm_bwd): a dict of q and k (input dtype, contiguous) and wq and wk (fp32; None
+    without weights)."""
+    if stream is not None:
+        with _on(q, stream):
+            return qk_norm_bwd(q, dq_out, k, dk_out, wq, wk, norm, eps, positions, freqs, layout, rot_scale, workspace)
+    dq, dk, dwq, dwk = _layer().qk_norm_bwd(q, dq_out, k, dk_out, wq, wk, _choice("norm", QK_NORM, norm), eps,
+                                            positions, freqs, _choice("layout", ROT_LAYOUT, layout), rot_scale,
+                                            workspace)
+    return {"q": dq, "k": dk, "wq": dwq, "wk": dwk}
+
+
+def rotary_freqs(rot: int, base: float = 10000.0, factor: float = 1.0, trained: Optional[int] = None,
+                 low: float = 1.0, high: float = 32.0, device="cuda") -> torch.Tensor:
+    """Frequencies for qk_norm, fp32 [rot / 2]: base^(-2 i / rot), for contexts ``factor`` times as long
+    as trained on.  ``trained`` None: every frequency is divided by ``factor`` (positions
+    interpolated).  With the ``trained`` context length it is done by parts: frequencies that turn more than
+    ``high`` times within it stay, those that turn less than ``low`` times are divided, and those between are
+    blended linearly in the number of turns.  Formed in 64 bits, rounded once."""
+    if rot < 0 or rot % 2:
+        raise ValueError("rot must be even")
+    if not (base > 0 and factor > 0 and 0 <= low < high):
+        raise ValueError("base and factor must be positive, low less than high")
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    f = base ** (-2 * i / max(rot, 1))
+    if trained is None:
+        f = f / factor
+    else:
+        turns = trained * f / (2 * math.pi)
+        keep = ((turns - low) / (high - low)).clamp(0, 1)
+        f = f * keep + f / factor * (1 - keep)
+    return f.float().to(device)
+
+
+def sample(logits, u=None, temperature=None, top_k=None, top_p=None, min_p=None, want_probs: bool = False, tokens=None,
+           probs=None, workspace=None, stream=None):
+    """The token that ``u`` (fp32 [N], in [0, 1)) draws from every row of ``logits`` [N, vocab] (any row
+    stride), and with ``want_probs`` (or ``probs`` given) the fp32 distribution it is drawn from, as
+    verify_draft takes it (prism_sample).  ``temperature`` fp32 [N] (0: the largest logit), ``top_k`` int32 [N]
+    (0: off), ``top_p`` fp32 [N] (1: off), ``min_p`` fp32 [N] (0: off), each None: off for all; the filters
+    apply in this order, each to what the one before left.  The draw goes by falling logits.
+    Returns (tokens, probs): int32 [N] or None without ``u``, [N, vocab] or None."""
+    if stream is not None:
+        with _on(logits, stream):
+            return sample(logits, u, temperature, top_k, top_p, min_p, want_probs, tokens, probs, workspace)
+    return _layer().sample(logits, u, temperature, top_k, top_p, min_p, want_probs, tokens, probs, workspace)
 
 
 def to_device(inp, device="cuda") -> dict:

@@ -31,7 +31,7 @@ SOURCES = ["prism_api.hip", "prologue.hip", "prologue_bf16.hip", "prologue_f32.h
            "chunk_scan_bf16.hip", "decode.hip", "long_seq.hip", "backward.hip",
            "scan_f32_recurrent.hip", "chunk_gram.hip", "chunk_scan_state.hip",
            "backward_chunk.hip", "layer_api.hip", "norm_residual.hip", "norm_gate.hip",
-           "draft.hip", "verify.hip"]
+           "draft.hip", "verify.hip", "stack_api.hip", "short_conv.hip", "qk_norm.hip", "sample.hip"]
 CHECKED = ["chunk_scan_bf16.hip", "chunk_scan.hip", "backward.hip", "chunk_gram.hip",
            "chunk_scan_state.hip", "backward_chunk.hip", "draft.hip"]   # MFMA chains, DPP
 ARCH = "gfx950"

@@ -241,4 +241,79 @@ int verify_chunks(int vocab);
 size_t verify_workspace_bytes(int n_seqs, int vocab);
 hipError_t launch_verify(const VerifyArgs& p, hipStream_t stream);
 
+// Causal depthwise convolution over packed sequences (short_conv.hip).
+constexpr int kConvMaxTaps = 8;
+constexpr int kConvBwdBlocks = 1024;             // workgroups of a backward, at most
+
+struct ShortConvArgs {
+    bool bf16;
+    bool silu;
+    int n_seqs, total_tokens, channels, taps;
+    int64_t x_stride;               // elements from a row of x to the next
+    const void *x, *w, *bias;       // bias may be null
+    const void* hist;               // [n_seqs, taps - 1, channels] or null (zero)
+    const int32_t* cu_seqlens;
+    void *y, *hist_out;             // forward, step
+    const void* dy;                 // backward
+    void *dx, *dhist;
+    float *dw, *dbias;
+    float* ws;                      // partial sums [blocks][channels * (taps + 1)]
+};
+
+// Workgroups of the largest launch of a forward pass or step.
+int64_t short_conv_blocks(int total_tokens, int n_seqs, int channels, bool bf16, int taps);
+int short_conv_bwd_blocks(int total_tokens, int channels, bool bf16, int taps);
+hipError_t launch_short_conv(const ShortConvArgs& p, hipStream_t stream);
+hipError_t launch_short_conv_step(const ShortConvArgs& p, hipStream_t stream);
+hipError_t launch_short_conv_bwd(const ShortConvArgs& p, hipStream_t stream);
+
+// Queries and keys of every head normalised, weighted and rotated (qk_norm.hip).
+constexpr int kQkMaxWidth = 512;
+constexpr int kQkBwdBlocks = 1024;               // workgroups of a backward, at most
+
+struct QkNormArgs {
+    bool bf16;
+    int norm;                       // prism_qk_norm_kind
+    bool interleaved;
+    int64_t tokens;
+    int heads[2];                   // of q and of k (0: no k)
+    int width, rot;
+    float eps, rot_scale;
+    int64_t stride[2], head_stride[2];
+    const void *x[2], *w[2];        // w may be null
+    const int32_t* positions;
+    const float* freqs;
+    void* y[2];                     // forward
+    const void* dy[2];              // backward
+    void* dx[2];
+    float* dw[2];
+    float* ws;                      // partial sums [blocks][2 * width]
+};
+
+int qk_norm_bwd_blocks(int64_t tokens);
+hipError_t launch_qk_norm(const QkNormArgs& p, hipStream_t stream);
+hipError_t launch_qk_norm_bwd(const QkNormArgs& p, hipStream_t stream);
+
+// Temperature, top-k, top-p and min-p over rows of logits (sample.hip).
+constexpr int kSampleMaxVocab = 1 << 20;
+
+struct SampleArgs {
+    bool bf16;
+    int64_t rows;
+    int vocab;
+    int64_t stride;                 // elements from a row of logits to the next
+    const void* logits;
+    const float* temperature;       // [rows] or null, as the three below
+    const int32_t* top_k;
+    const float *top_p, *min_p;
+    const float* u;                 // [rows], with tokens
+    int32_t* tokens;                // or null
+    float* probs;                   // [rows, vocab] or null
+    void* ws;
+};
+
+bool sample_fits(int64_t rows, int vocab);
+size_t sample_workspace_bytes(int64_t rows, int vocab);
+hipError_t launch_sample(const SampleArgs& p, hipStream_t stream);
+
 }  // namespace prism

@@ -2,10 +2,6 @@
 // operator (declared in include/prism.h): the norms before and after it, the
 // decoding of drafted tokens, its commit and the verification.  Argument
 // checks and launches on the caller's stream.
-#include <math.h>
-
-#include <initializer_list>
-
 #include "api_checks.h"
 #include "kernels.h"
 #include "prism.h"
@@ -22,8 +18,6 @@ bool norm_dims_ok(const prism_norm_dims* d)
 // Row arrays may be null when there are no rows.
 bool row_ok(const prism_norm_dims* d, const void* p) { return d->rows == 0 ? aligned16(p) : ptr_ok(p); }
 
-bool eps_ok(float eps) { return eps >= 0.f && isfinite(eps); }
-
 bool gate_ok(int gate) { return gate == PRISM_GATE_SILU || gate == PRISM_GATE_SIGMOID; }
 
 bool verify_dims_ok(const prism_verify_dims* d)
@@ -31,37 +25,6 @@ bool verify_dims_ok(const prism_verify_dims* d)
     return d && d->n_seqs >= 1 && d->total_tokens >= 0 && d->vocab >= 1 &&
            (d->dtype == PRISM_F32 || d->dtype == PRISM_BF16);
 }
-
-// The bytes of an array that a call reads or writes; `either`: its whole buffer may be
-// input and output at once.
-struct Region {
-    const void* p;
-    int64_t bytes;
-    bool either = false;
-};
-
-// No output shares a byte with an input or another output, but for buffers that may be both.
-bool apart(std::initializer_list<Region> outs, std::initializer_list<Region> ins)
-{
-    auto meet = [](const Region& x, const Region& y) {
-        return x.p && y.p && x.bytes > 0 && y.bytes > 0 && (uintptr_t)x.p < (uintptr_t)y.p + y.bytes &&
-               (uintptr_t)y.p < (uintptr_t)x.p + x.bytes;
-    };
-    for (const Region* o = outs.begin(); o != outs.end(); ++o) {
-        for (const Region* x = o + 1; x != outs.end(); ++x)
-            if (meet(*o, *x))
-                return false;
-        for (const Region& x : ins)
-            if (meet(*o, x) && !(o->either && x.either && o->p == x.p && o->bytes == x.bytes))
-                return false;
-    }
-    return true;
-}
-
-int64_t size_of(int dtype) { return dtype == PRISM_BF16 ? 2 : 4; }
-
-// A launch holds less than 2^32 threads in a dimension of its grid.
-bool grid_ok(int64_t blocks, int64_t threads) { return blocks <= UINT32_MAX / threads; }
 
 // The kernels of drafted tokens reach 8 tokens and the three rows before them from one
 // base with 32-bit offsets.

@@ -177,7 +177,7 @@ __global__ __launch_bounds__(kPartCols* kPartSlices) void sum_partials_kernel(co
     if (slice == 0 && c < cols) {
         if (c < split)
             out0[c] = s[0][ci];
-        else
+        else if (out1)
             out1[c - split] = s[0][ci];
     }
 }

@@ -426,6 +426,249 @@ PyObject* verify_draft(PyObject* const* a)
     return wrap_all(na.t, nt.t);
 }
 
+// Address of a device tensor of this dtype on like's device whose last axis is dense; its
+// other strides are the caller's to read.
+void* strided(const char* name, const at::Tensor& t, at::ScalarType dtype, const at::Tensor& like)
+{
+    if (t.scalar_type() != dtype)
+        fail(PyExc_TypeError, std::string(name) + ": expected " + text(dtype) + ", got " + text(t.scalar_type()));
+    if (t.device() != like.device())
+        fail(PyExc_ValueError, std::string(name) + " is on " + t.device().str() + ", not on " + like.device().str());
+    if (t.size(-1) > 1 && t.stride(-1) != 1)
+        fail(PyExc_ValueError, std::string(name) + ": the last axis must be contiguous");
+    return t.data_ptr();
+}
+
+int32_t size32(const char* what, int64_t n)
+{
+    if (n > INT32_MAX)
+        fail(PyExc_ValueError, std::string(what) + " exceeds 2^31 - 1");
+    return (int32_t)n;
+}
+
+// x [T, C] with any row stride, w [C, K]; n_seqs sequences.
+prism_conv_dims conv_dims(const at::Tensor& x, PyObject* w_obj, int64_t n_seqs)
+{
+    const at::Tensor& w = tensor("w", w_obj);
+    if (x.dim() != 2 || x.size(1) < 1)
+        fail(PyExc_ValueError, "x must be [T, channels]");
+    if (w.dim() != 2 || w.size(0) != x.size(1) || w.size(1) < 1)
+        fail(PyExc_ValueError, "w must be [channels, taps], got " + text(w.sizes()));
+    prism_conv_dims d;
+    d.n_seqs = size32("the number of sequences", n_seqs);
+    d.total_tokens = size32("the number of tokens", x.size(0));
+    d.channels = size32("channels", x.size(1));
+    d.taps = size32("taps", w.size(1));
+    d.dtype = dtype_code(x);
+    d.x_stride = x.stride(0);
+    return d;
+}
+
+int64_t sequences(PyObject* o)
+{
+    const at::Tensor& cu = tensor("cu_seqlens", o);
+    if (cu.scalar_type() != at::kInt || cu.dim() != 1 || cu.numel() < 2)
+        fail(PyExc_ValueError, "cu_seqlens must be int32 [n_seqs + 1] with n_seqs >= 1");
+    return cu.numel() - 1;
+}
+
+// x, w, cu_seqlens, bias, activation, hist, hist_out, y
+PyObject* short_conv(PyObject* const* a)
+{
+    const at::Tensor& x = leading("x", a[0]);
+    const prism_conv_dims d = conv_dims(x, a[1], sequences(a[2]));
+    const int64_t C = d.channels, n1[1] = {(int64_t)d.n_seqs + 1}, vec[1] = {C}, w[2] = {C, d.taps};
+    const int64_t hist[3] = {d.n_seqs, d.taps - 1, C};
+    const auto dt = x.scalar_type();
+    on_device(x);
+    const c10::DeviceGuard guard(x.device());
+    void *xp = strided("x", x, dt, x), *wp = arg("w", a[1], w, dt, x), *cup = arg("cu_seqlens", a[2], n1, at::kInt, x);
+    void *bp = opt("bias", a[3], vec, dt, x), *hp = opt("hist", a[5], hist, dt, x);
+    void* ho = opt("hist_out", a[6], hist, dt, x);
+    Out y("y", a[7], x.sizes(), dt, x);
+    done("prism_short_conv",
+         prism_short_conv(&d, xp, wp, bp, hp, (const int32_t*)cup, (int)whole(a[4]), y.p, ho, stream_of(x)));
+    return wrap(y.t);
+}
+
+// x, w, hist, bias, activation, hist_out, y
+PyObject* short_conv_step(PyObject* const* a)
+{
+    const at::Tensor& x = leading("x", a[0]);
+    if (x.dim() != 2 || x.size(0) < 1)
+        fail(PyExc_ValueError, "x must be [n_seqs, channels] with n_seqs >= 1");
+    const prism_conv_dims d = conv_dims(x, a[1], x.size(0));
+    const int64_t C = d.channels, vec[1] = {C}, w[2] = {C, d.taps}, hist[3] = {d.n_seqs, d.taps - 1, C};
+    const auto dt = x.scalar_type();
+    on_device(x);
+    const c10::DeviceGuard guard(x.device());
+    void *xp = strided("x", x, dt, x), *wp = arg("w", a[1], w, dt, x), *hp = arg("hist", a[2], hist, dt, x);
+    void* bp = opt("bias", a[3], vec, dt, x);
+    void* ho = a[5] == Py_None ? hp : arg("hist_out", a[5], hist, dt, x);        // in place unless another is given
+    Out y("y", a[6], x.sizes(), dt, x);
+    done("prism_short_conv_step", prism_short_conv_step(&d, xp, wp, bp, hp, (int)whole(a[4]), y.p, ho, stream_of(x)));
+    return wrap(y.t);
+}
+
+// x, w, cu_seqlens, dy, bias, activation, hist, workspace, want_dhist
+PyObject* short_conv_bwd(PyObject* const* a)
+{
+    const at::Tensor& x = leading("x", a[0]);
+    const prism_conv_dims d = conv_dims(x, a[1], sequences(a[2]));
+    const int64_t C = d.channels, n1[1] = {(int64_t)d.n_seqs + 1}, vec[1] = {C}, w[2] = {C, d.taps};
+    const int64_t hist[3] = {d.n_seqs, d.taps - 1, C};
+    const auto dt = x.scalar_type();
+    on_device(x);
+    const c10::DeviceGuard guard(x.device());
+    void *xp = strided("x", x, dt, x), *wp = arg("w", a[1], w, dt, x), *cup = arg("cu_seqlens", a[2], n1, at::kInt, x);
+    void *dyp = arg("dy", a[3], x.sizes(), dt, x), *bp = opt("bias", a[4], vec, dt, x);
+    void* hp = opt("hist", a[6], hist, dt, x);
+    at::Tensor dx = fresh(x.sizes(), dt, x), dw = fresh(w, at::kFloat, x), db, dh;
+    if (bp)
+        db = fresh(vec, at::kFloat, x);
+    if (a[6] != Py_None && truth(a[8]))
+        dh = fresh(hist, dt, x);
+    const Scratch ws(a[7], prism_conv_workspace_bytes(&d), x);
+    done("prism_short_conv_bwd",
+         prism_short_conv_bwd(&d, xp, wp, bp, hp, (const int32_t*)cup, (int)whole(a[5]), dyp, dx.data_ptr(),
+                              dw.data_ptr<float>(), db.defined() ? db.data_ptr<float>() : nullptr,
+                              dh.defined() ? dh.data_ptr() : nullptr, ws.p, ws.bytes, stream_of(x)));
+    return wrap_all(dx, dw, db, dh);
+}
+
+// What both passes of qk_norm read: q, k, wq, wk, positions, freqs.
+struct QkInputs {
+    prism_qk_dims d;
+    const at::Tensor& q;
+    const at::Tensor* k = nullptr;
+    void *qp, *kp = nullptr, *wq, *wk = nullptr, *pos = nullptr, *freqs = nullptr;
+
+    QkInputs(PyObject* qo, PyObject* ko, PyObject* wqo, PyObject* wko, PyObject* po, PyObject* fo) : q(leading("q", qo))
+    {
+        if (q.dim() != 3 || q.size(1) < 1 || q.size(2) < 1)
+            fail(PyExc_ValueError, "q must be [T, heads, width]");
+        const auto dt = q.scalar_type();
+        on_device(q);
+        d = {};
+        d.tokens = q.size(0);
+        d.heads_q = size32("heads", q.size(1));
+        d.width = size32("width", q.size(2));
+        d.dtype = dtype_code(q);
+        d.q_stride = q.stride(0);
+        d.q_head_stride = q.stride(1);
+        qp = strided("q", q, dt, q);
+        const int64_t vec[1] = {d.width}, t[1] = {d.tokens};
+        wq = opt("wq", wqo, vec, dt, q);
+        if (ko != Py_None) {
+            k = &tensor("k", ko);
+            if (k->dim() != 3 || k->size(0) != q.size(0) || k->size(1) < 1 || k->size(2) != q.size(2))
+                fail(PyExc_ValueError, "k must be [T, heads, width] with q's T and width, got " + text(k->sizes()));
+            d.heads_k = size32("heads", k->size(1));
+            d.k_stride = k->stride(0);
+            d.k_head_stride = k->stride(1);
+            kp = strided("k", *k, dt, q);
+            wk = opt("wk", wko, vec, dt, q);
+            if (!wq != !wk)
+                fail(PyExc_ValueError, "wq and wk come together");
+        } else if (wko != Py_None) {
+            fail(PyExc_ValueError, "wk without k");
+        }
+        if ((po == Py_None) != (fo == Py_None))
+            fail(PyExc_ValueError, "positions and freqs come together");
+        if (po != Py_None) {
+            const at::Tensor& f = tensor("freqs", fo);
+            if (f.dim() != 1 || 2 * f.numel() > d.width)
+                fail(PyExc_ValueError, "freqs must be [rot / 2] with rot <= width, got " + text(f.sizes()));
+            d.rot = (int32_t)(2 * f.numel());
+            pos = arg("positions", po, t, at::kInt, q);
+            freqs = arg("freqs", fo, f.sizes(), at::kFloat, q);
+        }
+    }
+};
+
+// q, k, wq, wk, norm, eps, positions, freqs, layout, rot_scale, q_out, k_out
+PyObject* qk_norm(PyObject* const* a)
+{
+    const at::Tensor& q = leading("q", a[0]);
+    on_device(q);
+    const c10::DeviceGuard guard(q.device());
+    const QkInputs in(a[0], a[1], a[2], a[3], a[6], a[7]);
+    Out qo("q_out", a[10], q.sizes(), q.scalar_type(), q), ko;
+    if (in.k)
+        ko = Out("k_out", a[11], in.k->sizes(), q.scalar_type(), q);
+    else if (a[11] != Py_None)
+        fail(PyExc_ValueError, "k_out without k");
+    done("prism_qk_norm",
+         prism_qk_norm(&in.d, in.qp, in.kp, in.wq, in.wk, (int)whole(a[4]), (float)number(a[5]), (const int32_t*)in.pos,
+                       (const float*)in.freqs, (int)whole(a[8]), (float)number(a[9]), qo.p, ko.p, stream_of(q)));
+    return wrap_all(qo.t, ko.t);
+}
+
+// q, dq_out, k, dk_out, wq, wk, norm, eps, positions, freqs, layout, rot_scale, workspace
+PyObject* qk_norm_bwd(PyObject* const* a)
+{
+    const at::Tensor& q = leading("q", a[0]);
+    on_device(q);
+    const c10::DeviceGuard guard(q.device());
+    const QkInputs in(a[0], a[2], a[4], a[5], a[8], a[9]);
+    const auto dt = q.scalar_type();
+    const int64_t vec[1] = {in.d.width};
+    void *dqo = arg("dq_out", a[1], q.sizes(), dt, q), *dko = nullptr;
+    at::Tensor dq = fresh(q.sizes(), dt, q), dk, dwq, dwk;
+    if (in.k) {
+        dko = arg("dk_out", a[3], in.k->sizes(), dt, q);
+        dk = fresh(in.k->sizes(), dt, q);
+    } else if (a[3] != Py_None) {
+        fail(PyExc_ValueError, "dk_out without k");
+    }
+    if (in.wq)
+        dwq = fresh(vec, at::kFloat, q);
+    if (in.wk)
+        dwk = fresh(vec, at::kFloat, q);
+    const Scratch ws(a[12], in.wq ? prism_qk_workspace_bytes(&in.d) : 0, q);
+    done("prism_qk_norm_bwd",
+         prism_qk_norm_bwd(&in.d, in.qp, in.kp, in.wq, in.wk, (int)whole(a[6]), (float)number(a[7]),
+                           (const int32_t*)in.pos, (const float*)in.freqs, (int)whole(a[10]), (float)number(a[11]), dqo,
+                           dko, dq.data_ptr(), dk.defined() ? dk.data_ptr() : nullptr,
+                           dwq.defined() ? dwq.data_ptr<float>() : nullptr,
+                           dwk.defined() ? dwk.data_ptr<float>() : nullptr, ws.p, ws.bytes, stream_of(q)));
+    return wrap_all(dq, dk, dwq, dwk);
+}
+
+// logits, u, temperature, top_k, top_p, min_p, want_probs, tokens, probs, workspace
+PyObject* sample(PyObject* const* a)
+{
+    const at::Tensor& l = leading("logits", a[0]);
+    if (l.dim() != 2 || l.size(1) < 1)
+        fail(PyExc_ValueError, "logits must be [rows, vocab]");
+    on_device(l);
+    const c10::DeviceGuard guard(l.device());
+    const int64_t rows[1] = {l.size(0)};
+    prism_sample_dims d;
+    d.rows = l.size(0);
+    d.vocab = size32("vocab", l.size(1));
+    d.dtype = dtype_code(l);
+    d.stride = l.stride(0);
+    void *lp = strided("logits", l, l.scalar_type(), l), *up = opt("u", a[1], rows, at::kFloat, l);
+    void *tp = opt("temperature", a[2], rows, at::kFloat, l), *kp = opt("top_k", a[3], rows, at::kInt, l);
+    void *pp = opt("top_p", a[4], rows, at::kFloat, l), *mp = opt("min_p", a[5], rows, at::kFloat, l);
+    const bool want_probs = a[8] != Py_None || truth(a[6]);
+    if (a[1] == Py_None && a[7] != Py_None)
+        fail(PyExc_ValueError, "tokens without u");
+    if (a[1] == Py_None && !want_probs)
+        fail(PyExc_ValueError, "u (for tokens) or want_probs is required");
+    Out tokens, probs;
+    if (a[1] != Py_None)
+        tokens = Out("tokens", a[7], rows, at::kInt, l);
+    if (want_probs)
+        probs = Out("probs", a[8], l.sizes(), at::kFloat, l);
+    const Scratch ws(a[9], prism_sample_workspace_bytes(&d), l);
+    done("prism_sample",
+         prism_sample(&d, lp, (const float*)tp, (const int32_t*)kp, (const float*)pp, (const float*)mp,
+                      (const float*)up, (int32_t*)tokens.p, (float*)probs.p, ws.p, ws.bytes, stream_of(l)));
+    return wrap_all(tokens.t, probs.t);
+}
+
 // No C++ exception leaves the module: torch's become their Python exceptions.
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t count)
@@ -454,7 +697,9 @@ PyObject* set_error(PyObject*, PyObject* cls)
 PyMethodDef methods[] = {
     PRISM_CALL(norm_residual, 7),  PRISM_CALL(norm_residual_bwd, 9), PRISM_CALL(norm_gate, 6),
     PRISM_CALL(norm_gate_bwd, 7),  PRISM_CALL(decode_draft, 17),     PRISM_CALL(decode_commit, 12),
-    PRISM_CALL(verify_draft, 9),   {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr},
+    PRISM_CALL(verify_draft, 9),   PRISM_CALL(short_conv, 8),        PRISM_CALL(short_conv_step, 7),
+    PRISM_CALL(short_conv_bwd, 9), PRISM_CALL(qk_norm, 12),          PRISM_CALL(qk_norm_bwd, 13),
+    PRISM_CALL(sample, 10),        {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr},
 };
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -604,6 +604,164 @@ prism_status prism_verify_draft(const prism_verify_dims* d, const void* p, const
                                 int32_t* n_accept, int32_t* next_token,
                                 void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * In front of the operator and behind the model's last product: the short
+ * convolution of the projections, the norm and rotation of queries and keys, and
+ * the choice of a token from logits.  The conventions of the section above hold
+ * (overlaps, workspaces), except that an input with a stride may begin at any
+ * element's address.
+ * ------------------------------------------------------------------------ */
+
+/* Activation of prism_short_conv: none, or s / (1 + e^-s). */
+typedef enum { PRISM_ACT_NONE = 0, PRISM_ACT_SILU = 1 } prism_activation;
+
+#define PRISM_MAX_TAPS 8
+
+typedef struct {
+    int32_t n_seqs;        /* packed sequences, >= 1 */
+    int32_t total_tokens;  /* rows of x, >= cu_seqlens[n_seqs] */
+    int32_t channels;      /* C, 1..2^22 */
+    int32_t taps;          /* K, 1..PRISM_MAX_TAPS */
+    int32_t dtype;         /* prism_dtype of every float tensor but the fp32 gradients */
+    int64_t x_stride;      /* elements from a row of x to the next, >= 0 */
+} prism_conv_dims;
+
+/* Bytes of device workspace prism_short_conv_bwd needs (fp32 partial sums of the weights'
+ * gradients, one set per workgroup).  0 for invalid dims. */
+size_t prism_conv_workspace_bytes(const prism_conv_dims* d);
+
+/*
+ * Causal depthwise convolution over packed sequences, as the projections of q, k and v pass
+ * through it in front of the operator:
+ *   s_t = bias + sum_{m=0..K-1} w[c][m] x[t - K + 1 + m],   y_t = act(s_t)   (per channel c).
+ * Rows in front of a sequence are its history's (slot K - 2 the one just before it), or zero.
+ *
+ *   x           [T, C] with rows x_stride elements apart (columns of a wider tensor)
+ *   w           [C, K]              tap K - 1 multiplies the token itself
+ *   bias        [C] or NULL (zero)
+ *   hist        [n_seqs, K - 1, C] or NULL (zero)
+ *   activation  prism_activation
+ *   y           out [T, C]
+ *   hist_out    out [n_seqs, K - 1, C] or NULL (not written): the history to carry on; may be
+ *               the buffer of hist
+ * hist and hist_out are not looked at when K == 1.  Rows behind the last sequence
+ * (cu_seqlens[n_seqs] and on) are neither read nor written.
+ */
+prism_status prism_short_conv(const prism_conv_dims* d, const void* x, const void* w, const void* bias,
+                              const void* hist, const int32_t* cu_seqlens, int activation,
+                              void* y, void* hist_out, void* stream);
+
+/* One new token a sequence (total_tokens must equal n_seqs; no cu_seqlens): y [n_seqs, C] from
+ * x [n_seqs, C] and the history, and the history moved on by it.  hist is required when K > 1;
+ * hist_out may be its buffer.  Other arguments as in prism_short_conv. */
+prism_status prism_short_conv_step(const prism_conv_dims* d, const void* x, const void* w, const void* bias,
+                                   const void* hist, int activation, void* y, void* hist_out, void* stream);
+
+/*
+ * Gradients of prism_short_conv for the gradient dy [T, C] of y (a history that is carried
+ * out takes none):
+ *   dx          out [T, C]; zero in rows behind the last sequence
+ *   dw          out fp32 [C, K]        dbias  out fp32 [C] or NULL (not formed)
+ *   dhist       out [n_seqs, K - 1, C] or NULL (not formed)
+ *   workspace   prism_conv_workspace_bytes(d) bytes
+ * dx may not be the buffer of dy.  The same call gives the same bits.
+ */
+prism_status prism_short_conv_bwd(const prism_conv_dims* d, const void* x, const void* w, const void* bias,
+                                  const void* hist, const int32_t* cu_seqlens, int activation, const void* dy,
+                                  void* dx, float* dw, float* dbias, void* dhist,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Norm of prism_qk_norm: none, 1 / sqrt(mean(x^2) + eps), or 1 / sqrt(sum(x^2) + eps). */
+typedef enum { PRISM_QK_NONE = 0, PRISM_QK_RMS = 1, PRISM_QK_L2 = 2 } prism_qk_kind;
+/* Pairs that turn together among the first `rot` elements: (i, i + rot / 2), or (2 i, 2 i + 1). */
+typedef enum { PRISM_ROT_HALF = 0, PRISM_ROT_INTERLEAVED = 1 } prism_rot_layout;
+
+typedef struct {
+    int64_t tokens;                        /* T >= 0 */
+    int32_t heads_q, heads_k;              /* >= 1; heads_k 0: no k */
+    int32_t width;                         /* elements per head, 1..512 */
+    int32_t rot;                           /* elements that turn, even, 0..width */
+    int32_t dtype;                         /* prism_dtype of every float tensor but freqs and the fp32 gradients */
+    int64_t q_stride, q_head_stride;       /* elements from a token (a head) of q to the next, >= 0 */
+    int64_t k_stride, k_head_stride;
+} prism_qk_dims;
+
+/* Bytes of device workspace prism_qk_norm_bwd needs.  0 for invalid dims. */
+size_t prism_qk_workspace_bytes(const prism_qk_dims* d);
+
+/*
+ * The queries and keys of every head normalised, weighted and rotated by their token's
+ * position in one pass (the operator takes normalised keys):
+ *   y = R(position * freqs) (x rstd w)        (per head row; w one)
+ * with R (a, b) = rot_scale (a cos - b sin, b cos + a sin) for each pair.  Angles are formed
+ * in 64 bits.
+ *
+ *   q, k        [T, heads, width] with the strides of d; k NULL iff heads_k == 0
+ *   wq, wk      [width], or NULL (one); both or neither where there is a k
+ *   norm, layout  prism_qk_kind, prism_rot_layout
+ *   eps         >= 0, finite
+ *   positions   int32 [T]             freqs  fp32 [rot / 2]      (NULL allowed iff rot == 0)
+ *   q_out, k_out  out [T, heads, width], dense; may be the buffers of dense q and k
+ * Per-token arrays may be NULL when tokens == 0.
+ */
+prism_status prism_qk_norm(const prism_qk_dims* d, const void* q, const void* k, const void* wq, const void* wk,
+                           int norm, float eps, const int32_t* positions, const float* freqs, int layout,
+                           float rot_scale, void* q_out, void* k_out, void* stream);
+
+/*
+ * Gradients of prism_qk_norm for the gradients dq_out, dk_out (dense) of its outputs: dq, dk
+ * (dense, input dtype; may be the buffers of dq_out, dk_out), dwq, dwk fp32 [width] (with wq,
+ * wk alone).  The same call gives the same bits.
+ *   workspace   prism_qk_workspace_bytes(d) bytes
+ */
+prism_status prism_qk_norm_bwd(const prism_qk_dims* d, const void* q, const void* k, const void* wq, const void* wk,
+                               int norm, float eps, const int32_t* positions, const float* freqs, int layout,
+                               float rot_scale, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                               float* dwq, float* dwk, void* workspace, size_t workspace_bytes, void* stream);
+
+#define PRISM_MAX_SAMPLE_VOCAB (1 << 20)
+
+typedef struct {
+    int64_t rows;          /* >= 0 */
+    int32_t vocab;         /* 1..PRISM_MAX_SAMPLE_VOCAB */
+    int32_t dtype;         /* prism_dtype of the logits */
+    int64_t stride;        /* elements from a row of logits to the next, >= 0 */
+} prism_sample_dims;
+
+/* Bytes of device workspace prism_sample needs (0: the workspace may be NULL); 0 for invalid dims. */
+size_t prism_sample_workspace_bytes(const prism_sample_dims* d);
+
+/*
+ * The token that a given random number draws from a row of logits, and the distribution it is
+ * drawn from (what prism_verify_draft takes as p and q).  The entries of a row are taken in
+ * the order of falling logits, equal ones by rising index, with the weights
+ * exp((l - max) / temperature).  Of that order are kept, one after the other,
+ *   top_k   the first k entries;
+ *   top_p   of these the entries before which less than p of their weight has passed;
+ *   min_p   of these the entries with a weight of at least p (the largest entry's is one);
+ * the first entry always.  The token is the first of them at which the running weight exceeds
+ * u times the kept weight.
+ *
+ *   logits       [rows, vocab] with rows `stride` elements apart
+ *   temperature  fp32 [rows] or NULL (one); not greater than zero, or NaN: the largest entry is
+ *                taken, the first of equal ones
+ *   top_k        int32 [rows] or NULL; 0 and less: off
+ *   top_p        fp32 [rows] or NULL; 1 and more, or NaN: off
+ *   min_p        fp32 [rows] or NULL; 0 and less, or NaN: off; more than 1 counts as 1
+ *   u            fp32 [rows] in [0, 1) (values outside count as the nearest inside, NaN as 0);
+ *                NULL allowed iff tokens is NULL
+ *   tokens       out int32 [rows], or NULL (not chosen)
+ *   probs        out fp32 [rows, vocab], or NULL (not formed); tokens or probs is required
+ *   workspace    prism_sample_workspace_bytes(d) bytes
+ * Entries of -infinity and NaN are never kept; a row without any other gives the token -1 and
+ * probabilities of zero.  Beside entries of +infinity no others are kept.  Weights are formed
+ * in 64 bits and added exactly in steps of 2^-43 of the largest: the same call gives the same
+ * token, whatever else runs.
+ */
+prism_status prism_sample(const prism_sample_dims* d, const void* logits, const float* temperature,
+                          const int32_t* top_k, const float* top_p, const float* min_p, const float* u,
+                          int32_t* tokens, float* probs, void* workspace, size_t workspace_bytes, void* stream);
+
 /*
  * Diagnostic: the number of bounded in-kernel waits that gave up since the
  * last reset, on the current device.  The eight-wavefront bf16 scan has one
