@@ -243,7 +243,7 @@ hipError_t launch_verify(const VerifyArgs& p, hipStream_t stream);
 
 // Causal depthwise convolution over packed sequences (short_conv.hip).
 constexpr int kConvMaxTaps = 8;
-constexpr int kConvBwdBlocks = 1024;             // workgroups of a backward, at most
+constexpr int kConvBwdBlocks = 512;              // workgroups of a backward, at most (or one per chunk of channels)
 
 struct ShortConvArgs {
     bool bf16;

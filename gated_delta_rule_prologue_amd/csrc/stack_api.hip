@@ -29,7 +29,7 @@ bool act_ok(int a) { return a == PRISM_ACT_NONE || a == PRISM_ACT_SILU; }
 
 bool conv_fits(const prism_conv_dims* d)
 {
-    return d->channels <= 1 << 22 &&
+    return d->channels <= 1 << 22 && d->total_tokens <= 1 << 30 &&
            grid_ok(prism::short_conv_blocks(d->total_tokens, d->n_seqs, d->channels, d->dtype == PRISM_BF16, d->taps), 256);
 }
 

@@ -619,7 +619,7 @@ typedef enum { PRISM_ACT_NONE = 0, PRISM_ACT_SILU = 1 } prism_activation;
 
 typedef struct {
     int32_t n_seqs;        /* packed sequences, >= 1 */
-    int32_t total_tokens;  /* rows of x, >= cu_seqlens[n_seqs] */
+    int32_t total_tokens;  /* rows of x, >= cu_seqlens[n_seqs], at most 2^30 */
     int32_t channels;      /* C, 1..2^22 */
     int32_t taps;          /* K, 1..PRISM_MAX_TAPS */
     int32_t dtype;         /* prism_dtype of every float tensor but the fp32 gradients */

@@ -68,6 +68,9 @@ def test_conv_refuses(B):
     L = B.lib()
     assert L.prism_short_conv(None, *far(5), 1, *far(2), None) == B.PRISM_EINVAL
     assert all(B.conv_workspace_bytes(d) == 0 for d in bad)
+    for call in (conv, grad):
+        many = dict(zip(CONV if call is conv else GRAD, [FAKE + (i << 48) for i in range(11)]))
+        assert call(B, B.ConvDims(4, (1 << 30) + 1, 1, 4, 1, 1), **many) == B.PRISM_EUNSUPPORTED
     # a launch holds 2^32 threads: a billion tokens of 2^15 channels are more
     assert conv(B, B.ConvDims(4, 1 << 30, 1 << 15, 4, 1, 1 << 15), **dict(zip(CONV, [FAKE + (i << 48) for i in range(7)]))) \
         == B.PRISM_EUNSUPPORTED
