@@ -74,7 +74,9 @@ bool qk_dims_ok(const prism_qk_dims* d)
 
 bool qk_fits(const prism_qk_dims* d)
 {
-    return d->width <= prism::kQkMaxWidth && d->heads_q <= 65535 && d->heads_k <= 65535 && grid_ok(d->tokens, 256);
+    const auto near = [](int64_t stride) { return stride <= UINT32_MAX; };
+    return d->width <= prism::kQkMaxWidth && d->heads_q <= 65535 && d->heads_k <= 65535 && near(d->q_stride) &&
+           near(d->q_head_stride) && near(d->k_stride) && near(d->k_head_stride) && grid_ok(2 * d->tokens, 256);
 }
 
 struct QkSizes {

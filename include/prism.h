@@ -682,7 +682,7 @@ typedef struct {
     int32_t width;                         /* elements per head, 1..512 */
     int32_t rot;                           /* elements that turn, even, 0..width */
     int32_t dtype;                         /* prism_dtype of every float tensor but freqs and the fp32 gradients */
-    int64_t q_stride, q_head_stride;       /* elements from a token (a head) of q to the next, >= 0 */
+    int64_t q_stride, q_head_stride;       /* elements from a token (a head) of q to the next, 0 .. 2^32 - 1 */
     int64_t k_stride, k_head_stride;
 } prism_qk_dims;
 
