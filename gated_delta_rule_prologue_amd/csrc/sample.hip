@@ -5,16 +5,19 @@
 // the weights w = exp((l - max) / temperature).  Every filter keeps a prefix of that order: the
 // first k; those before which less than p of the weight (of the first k) has passed; those with
 // w >= min_p.  The token is the first at which the running weight exceeds u times the weight
-// that is kept, so the draw too is a place in that order.  No sort is needed for it:
-// a histogram of the distance from the maximum (kBuckets steps over at most 32 nats) gives the
-// bucket of each place, and only that bucket's entries are ordered, by counting.
-// A bucket of more entries than kList (ties) is cut further by digits of (logit, index).
+// that is kept, so the draw too is a place in that order.  No sort of the row is needed for it:
+// a histogram of the distance from the maximum (768 buckets over at most 16 nats, 256 over what is behind) bounds the weight before each place, and so the few buckets in which each can lie; only their entries
+// are collected and sorted, and the places are looked up one after the other.  More entries in those buckets than
+// kList (ties, places in the last bucket) are cut further by digits of (logit, index).
 //
 // Weights are formed in 64 bits and added as whole numbers in steps of 2^-43 of the largest: sums
 // of 2^20 of them fit 63 bits, no order of additions changes them, and the choice agrees with
-// one made in 64-bit floating point but at a border nearer than some 10^-12.
+// one made in 64-bit floating point but at a border nearer than some 10^-11.
 //
-// One workgroup takes a row and reads it once for the maximum and once for each place looked for.
+// Bound by a chain of passes where there are few rows, by the arithmetic of the weights (some 25
+// instructions an entry) where there are many.  A row of up to 32,768 entries stays in the registers of one
+// workgroup for all passes.  Longer rows, and shorter ones where they are few, are cut into chunks, one workgroup
+// each, with a launch for the maximum, the histogram, the collection and the choice.
 #include "common.h"
 #include "kernels.h"
 #include "norm_rows.h"
@@ -23,38 +26,69 @@ namespace prism {
 
 namespace {
 
-constexpr int kThreads = 1024, kWaves = kThreads / 64;
-constexpr int kBuckets = 2048, kList = 1024, kIndexBits = 20, kDigitBits = 11;
+constexpr int kBuckets = 1024, kLast = kBuckets - 1, kList = 1024, kIndexBits = 20, kDigitBits = 10;
 static_assert(kSampleMaxVocab == 1 << kIndexBits, "an index fills the order's low bits");
-static_assert(kBuckets == 2 * kThreads && kBuckets == 1 << kDigitBits, "two buckets a thread; a digit fills them");
+static_assert(kBuckets == 1 << kDigitBits, "a digit fills the buckets");
 constexpr double kOne = 8796093022208.;                      // 2^43, the weight of the maximum
+constexpr float kNats = 16.f;                                // that the first kNear buckets cover
+constexpr int kNear = 768;
+constexpr uint64_t kNowhere = ~0ull;
 
-// Counts and weights of 2048 buckets; after scan() the sums up to and with each.
+__device__ __forceinline__ float infinity() { return __builtin_inff(); }
+
+// Counts and weights of the buckets; after scan() the sums up to and with each.
 struct Hist {
     uint64_t mass[kBuckets];
     uint32_t count[kBuckets];
+    __device__ __forceinline__ uint64_t mass_before(int b) const { return b ? mass[b - 1] : 0; }
+    __device__ __forceinline__ uint32_t count_before(int b) const { return b ? count[b - 1] : 0; }
 };
-struct List {
-    uint64_t order[kList], weight[kList];
+
+// What a row is measured by.
+struct Scale {
+    float max, min, floor;                                   // floor: a weight of 2^-45
+    float step, far_step, far_from;                          // buckets per unit of l, near and far, where they meet
+    double c, top;                                           // 32 log2 e / temperature; max
+};
+
+// What is asked of a row.
+struct Wish {
+    float t, p, m;                                           // m: 0 is off
+    double at;                                               // u as the nearest below 1
+    int k;                                                   // 0 is off
+    bool draw;
+};
+
+// What a row's histogram says of it: which filters cut it (min_p's place, or kNowhere), and the ranges of buckets in
+// which the places lie, as bounds on (max - l) * step.
+struct Plan {
+    uint64_t m_order;
+    int k, p, m;                                             // k, p: whether they are in force; m: its bucket, or -1
+    int ranges;
+    float from[4], to[4];
+};
+
+struct Choice {
+    uint64_t cut, total;                                     // the last place that is kept, the weight up to it
+    int token;
 };
 
 struct Shared {
     Hist h;
     union {
         Hist digits;
-        List list;
+        struct {
+            uint64_t order[kList], mass[kList];
+        } list;
     } x;
     double table[32];                                        // 2^(i / 32)
-    uint64_t wave_mass[kWaves], found_order, found_mass, base_mass;
-    uint32_t wave_count[kWaves], base_count, number;
-    float wave_max[kWaves], wave_min[kWaves];
-    int wave_arg[kWaves], at;
-};
-
-// What a row is measured by.
-struct Row {
-    float max, step;                                         // step: buckets per unit of l
-    double c;                                                // 32 log2 e / temperature
+    uint64_t wave_mass[16], found_order, found_mass, base_mass;
+    Plan plan;
+    Choice choice;
+    uint32_t wave_count[16], base_count, number;
+    uint32_t first[kBuckets];                                // where a bucket begins in the sorted list
+    float wave_max[16], wave_min[16];
+    int at;
 };
 
 // l as a whole number that rises with it (+0 and -0 the same).
@@ -72,99 +106,411 @@ __device__ __forceinline__ uint64_t order_of(float l, int index)
 }
 __device__ __forceinline__ float logit_of(uint64_t order) { return of_key(~(uint32_t)(order >> kIndexBits)); }
 
-__device__ __forceinline__ int bucket_of(const Row& r, float l)
+// A bucket and a fraction, rising as l falls: near the maximum d * step, from where the far buckets begin on the
+// smaller of both lines.
+__device__ __forceinline__ float height_of(const Scale& r, float l)
 {
-    return (int)fminf((r.max - l) * r.step, (float)(kBuckets - 1));
+    const float d = r.max - l;
+    return fminf(fminf(d * r.step, __builtin_fmaf(d, r.far_step, r.far_from)), (float)kLast);
 }
+__device__ __forceinline__ int bucket_of(const Scale& r, float l) { return (int)height_of(r, l); }
 
 // exp((l - max) / temperature): 2^(n / 32) from the table, and the rest of the exponent, at most
-// ln 2 / 64, by its series to the fifth power (2 10^-15).
-__device__ __forceinline__ double weight_of(const Row& r, const double* table, float l)
+// ln 2 / 64, by its series to the fourth power (10^-12).  Adding 1.5 * 2^52 leaves n in the sum's low word.
+__device__ __forceinline__ double series_of(const Scale& r, float l, int& n)
 {
-    const double y = fmax(((double)l - (double)r.max) * r.c, -32. * 1100.), n = rint(y);
-    const double t = (y - n) * 0.021660849392498290;         // ln 2 / 32
-    double s = __builtin_fma(t, 1. / 120, 1. / 24);
-    s = __builtin_fma(s, t, 1. / 6);
-    s = __builtin_fma(s, t, 0.5);
-    s = __builtin_fma(s, t, 1.);
-    s = __builtin_fma(s, t, 1.);
-    const int i = (int)n;
-    return ldexp(table[i & 31] * s, i >> 5);
+    const double d = (double)l - r.top, m = __builtin_fma(d, r.c, 6755399441055744.);
+    const double t = __builtin_fma(d, r.c, -(m - 6755399441055744.));
+    double s = __builtin_fma(t, 9.17256270182464302e-09, 1.69385097243718210e-06);               // powers of ln 2 / 32 over 4!, 3!, 2!
+    s = __builtin_fma(s, t, 2.34596198202246799e-04);
+    s = __builtin_fma(s, t, 2.16608493924982902e-02);
+    n = (int)__double_as_longlong(m);
+    return __builtin_fma(s, t, 1.);
 }
-__device__ __forceinline__ uint64_t steps_of(double w)
+// In steps of 2^-43; entries below `floor` have less than half a step.
+__device__ __forceinline__ uint64_t steps_of(const Scale& r, const double* table, float l)
 {
-    return (uint64_t)__double_as_longlong(__builtin_fma(w, kOne, 4503599627370496.)) & 0xfffffffffffffull;   // + 2^52
+    int n;
+    const double s = series_of(r, fmaxf(l, r.floor), n), t = table[n & 31];
+    const double e = __hiloint2double(__double2hiint(t) + (((n >> 5) + 43) << 20), __double2loint(t));
+    const double w = __builtin_fma(e, s, 4503599627370496.); // + 2^52: the steps are the mantissa
+    const bool some = l >= r.floor;
+    return (uint64_t)(uint32_t)(some ? __double2hiint(w) & 0xfffff : 0) << 32 | (uint32_t)(some ? __double2loint(w) : 0);
+}
+__device__ __forceinline__ double weight_of(const Scale& r, const double* table, float l)
+{
+    if (((double)l - r.top) * r.c < -32. * 1100.)
+        return 0.;
+    int n;
+    const double s = series_of(r, l, n);
+    return ldexp(table[n & 31] * s, n >> 5);
 }
 
+// Whether an entry counts, by its bits: the compiler takes a float comparison of what entry() has selected back to the
+// value before the selection, and lets NaN through.
+__device__ __forceinline__ bool live_entry(float l) { return __float_as_uint(l) != 0xff800000u; }
+
 // Entries of a row as they are weighed: NaN counts as -infinity; beside +infinity nothing else counts.
-__device__ __forceinline__ float entry(float l) { return l > -__builtin_inff() ? l : -__builtin_inff(); }
+__device__ __forceinline__ float entry(float l) { return l > -infinity() ? l : -infinity(); }
 __device__ __forceinline__ float entry(float l, bool infinite)
 {
     l = entry(l);
-    return !infinite ? l : l == __builtin_inff() ? 0.f : -__builtin_inff();
+    return !infinite ? l : l == infinity() ? 0.f : -infinity();
 }
 
-// f(l, index) for every element of a row, which may begin at any element's address.
-template <typename T, typename F> __device__ __forceinline__ void each(const T* row, int vocab, F f)
-{
-    constexpr int VE = Vec16<T>::N;
-    const int whole = vocab / VE * VE;
-    for (int at = threadIdx.x * VE; at < whole; at += kThreads * VE) {
-        const rows::AtElement a = *reinterpret_cast<const rows::AtElement*>(row + at);
+// The elements from `first` to `end` of a row that are read again each time they are gone over.  A row may begin at
+// any element's address.
+template <typename T, int THREADS_> struct Streamed {
+    static constexpr int THREADS = THREADS_;
+    const T* row;
+    int first, end;
+    bool infinite;                                           // entries of +infinity are all that counts
+    __device__ __forceinline__ void load() { infinite = false; }
+    __device__ __forceinline__ void only_infinite() { infinite = true; }
+    // f(entry, index) for every element, spread over the workgroup
+    template <typename F> __device__ __forceinline__ void each(F f) const
+    {
+        constexpr int VE = Vec16<T>::N;
+        const int whole = first + (end - first) / VE * VE;
+        for (int at = first + threadIdx.x * VE; at < whole; at += THREADS * VE) {
+            const rows::AtElement a = *reinterpret_cast<const rows::AtElement*>(row + at);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (sizeof(T) == 2) {
-                f(__uint_as_float(a[i] << 16), at + 2 * i);
-                f(__uint_as_float(a[i] & 0xffff0000u), at + 2 * i + 1);
-            } else {
-                f(__uint_as_float(a[i]), at + i);
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (sizeof(T) == 2) {
+                    f(entry(__uint_as_float(a[i] << 16), infinite), at + 2 * i);
+                    f(entry(__uint_as_float(a[i] & 0xffff0000u), infinite), at + 2 * i + 1);
+                } else {
+                    f(entry(__uint_as_float(a[i]), infinite), at + i);
+                }
+            }
+        }
+        if (whole + (int)threadIdx.x < end)
+            f(entry(to_f32(row[whole + threadIdx.x]), infinite), whole + threadIdx.x);
+    }
+    // f(entries, index of the first) for every four, -infinity behind the last
+    template <typename F> __device__ __forceinline__ void each4(F f) const
+    {
+        constexpr int VE = Vec16<T>::N;
+        const int whole = first + (end - first) / VE * VE;
+        for (int at = first + threadIdx.x * VE; at < whole; at += THREADS * VE) {
+            const rows::AtElement a = *reinterpret_cast<const rows::AtElement*>(row + at);
+#pragma unroll
+            for (int j = 0; j < VE / 4; ++j) {
+                float l[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (sizeof(T) == 2)
+                        l[i] = entry(__uint_as_float(i % 2 ? a[2 * j + i / 2] & 0xffff0000u : a[2 * j + i / 2] << 16), infinite);
+                    else
+                        l[i] = entry(__uint_as_float(a[i]), infinite);
+                }
+                f(l, at + 4 * j);
+            }
+        }
+        if (whole + (int)threadIdx.x < end) {
+            const float l[4] = {entry(to_f32(row[whole + threadIdx.x]), infinite), -infinity(), -infinity(), -infinity()};
+            f(l, whole + threadIdx.x);
+        }
+    }
+};
+
+// Those that stay in the workgroup's registers, PER elements a thread; what is behind them reads as -infinity.
+template <typename T, int THREADS_, int PER_> struct Held {
+    static constexpr int THREADS = THREADS_, PER = PER_, VE = Vec16<T>::N, W = PER * (int)sizeof(T) / 4;
+    const T* row;
+    int first, end;
+    uint32_t x[W];
+    __device__ __forceinline__ int index(int vec) const { return first + (vec * THREADS + (int)threadIdx.x) * VE; }
+    __device__ __forceinline__ void load()
+    {
+        constexpr uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+#pragma unroll
+        for (int v = 0; v < W / 4; ++v) {
+            rows::AtElement a = {none, none, none, none};
+            if (index(v) + VE <= end)
+                a = *reinterpret_cast<const rows::AtElement*>(row + index(v));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[4 * v + i] = a[i];
+        }
+        if ((end - first) % VE) {                            // the last vector, element by element
+#pragma unroll
+            for (int v = 0; v < W / 4; ++v)
+                if (index(v) < end && index(v) + VE > end) {
+#pragma unroll
+                    for (int i = 0; i < VE; ++i)
+                        if (index(v) + i < end) {
+                            if constexpr (sizeof(T) == 2) {
+                                const uint32_t half = row[index(v) + i];
+                                x[4 * v + i / 2] = i % 2 ? (x[4 * v + i / 2] & 0xffffu) | half << 16
+                                                         : (x[4 * v + i / 2] & 0xffff0000u) | half;
+                            } else {
+                                x[4 * v + i] = __float_as_uint(row[index(v) + i]);
+                            }
+                        }
+                }
+        }
+        change([](float l) { return entry(l); });
+    }
+    template <typename F> __device__ __forceinline__ void each(F f) const
+    {
+#pragma unroll
+        for (int v = 0; v < W / 4; ++v) {
+            const int at = index(v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t a = x[4 * v + i];
+                if constexpr (sizeof(T) == 2) {
+                    asm volatile("" : "+v"(a));              // the halves are not kept beside the words
+                    f(__uint_as_float(a << 16), at + 2 * i);
+                    f(__uint_as_float(a & 0xffff0000u), at + 2 * i + 1);
+                } else {
+                    f(__uint_as_float(a), at + i);
+                }
             }
         }
     }
-    if (whole + (int)threadIdx.x < vocab)
-        f(to_f32(row[whole + threadIdx.x]), whole + threadIdx.x);
-}
+    // f(entries, index of the first) for every four
+    template <typename F> __device__ __forceinline__ void each4(F f) const
+    {
+#pragma unroll
+        for (int v = 0; v < W / 4; ++v) {
+            const int at = index(v);
+#pragma unroll
+            for (int j = 0; j < VE / 4; ++j) {
+                float l[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (sizeof(T) == 2) {
+                        uint32_t a = x[4 * v + 2 * j + i / 2];
+                        asm volatile("" : "+v"(a));
+                        l[i] = __uint_as_float(i % 2 ? a & 0xffff0000u : a << 16);
+                    } else {
+                        l[i] = __uint_as_float(x[4 * v + i]);
+                    }
+                }
+                f(l, at + 4 * j);
+            }
+        }
+    }
+    template <typename F> __device__ __forceinline__ void change(F f)
+    {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            if constexpr (sizeof(T) == 2)
+                x[i] = __float_as_uint(f(__uint_as_float(x[i] << 16))) >> 16 |
+                       __float_as_uint(f(__uint_as_float(x[i] & 0xffff0000u)));
+            else
+                x[i] = __float_as_uint(f(__uint_as_float(x[i])));
+        }
+    }
+    __device__ __forceinline__ void only_infinite()
+    {
+        change([](float l) { return entry(l, true); });
+    }
+};
 
-__device__ __forceinline__ void clear(Hist& h)
+template <int THREADS> __device__ __forceinline__ void clear(Hist& h)
 {
-    for (int i = threadIdx.x; i < kBuckets; i += kThreads) {
+    for (int i = threadIdx.x; i < kBuckets; i += THREADS) {
         h.mass[i] = 0;
         h.count[i] = 0;
     }
 }
 
-// Sums up to and with each bucket.
-__device__ void scan(Hist& h, Shared& s)
+// Sums over the lanes up to and with each, in registers: shifts by 1, 2, 4, 8 within rows of 16 lanes, then the
+// rows' last lanes to the rows behind them.
+template <int CTRL, int ROWS> __device__ __forceinline__ uint32_t moved(uint32_t x)
 {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS> __device__ __forceinline__ uint64_t moved(uint64_t x)
+{
+    return (uint64_t)moved<CTRL, ROWS>((uint32_t)(x >> 32)) << 32 | moved<CTRL, ROWS>((uint32_t)x);
+}
+template <typename N> __device__ __forceinline__ N lane_scan(N x)
+{
+    x += moved<0x111, 0xF>(x);
+    x += moved<0x112, 0xF>(x);
+    x += moved<0x114, 0xF>(x);
+    x += moved<0x118, 0xF>(x);
+    x += moved<0x142, 0xA>(x);
+    return x + moved<0x143, 0xC>(x);
+}
+__device__ __forceinline__ uint32_t at_lane(uint32_t x, int lane) { return __builtin_amdgcn_readlane(x, lane); }
+__device__ __forceinline__ uint64_t at_lane(uint64_t x, int lane)
+{
+    return (uint64_t)at_lane((uint32_t)(x >> 32), lane) << 32 | at_lane((uint32_t)x, lane);
+}
+
+// Sums up to and with each bucket.
+template <int THREADS> __device__ __forceinline__ void scan(Hist& h, Shared& s)
+{
+    constexpr int PER = kBuckets / THREADS, WAVES = THREADS / 64;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     __syncthreads();
-    uint64_t m0 = h.mass[2 * tid], m = m0 + h.mass[2 * tid + 1];
-    uint32_t c0 = h.count[2 * tid], c = c0 + h.count[2 * tid + 1];
-    const uint64_t m_own = m;
-    const uint32_t c_own = c;
+    uint64_t m[PER], mt = 0;
+    uint32_t c[PER], ct = 0;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint64_t mu = __shfl_up(m, d);
-        const uint32_t cu = __shfl_up(c, d);
-        if (lane >= d) {
-            m += mu;
-            c += cu;
-        }
+    for (int i = 0; i < PER; ++i) {
+        m[i] = mt += h.mass[PER * tid + i];
+        c[i] = ct += h.count[PER * tid + i];
     }
+    const uint64_t m_own = mt;
+    const uint32_t c_own = ct;
+    mt = lane_scan(mt);
+    ct = lane_scan(ct);
     if (lane == 63) {
-        s.wave_mass[wave] = m;
-        s.wave_count[wave] = c;
+        s.wave_mass[wave] = mt;
+        s.wave_count[wave] = ct;
     }
     __syncthreads();
-    for (int w = 0; w < wave; ++w) {
-        m += s.wave_mass[w];
-        c += s.wave_count[w];
+    mt -= m_own;
+    ct -= c_own;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+        mt += w < wave ? s.wave_mass[w] : 0;
+        ct += w < wave ? s.wave_count[w] : 0;
     }
-    h.mass[2 * tid] = m - m_own + m0;
-    h.mass[2 * tid + 1] = m;
-    h.count[2 * tid] = c - c_own + c0;
-    h.count[2 * tid + 1] = c;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        h.mass[PER * tid + i] = mt + m[i];
+        h.count[PER * tid + i] = ct + c[i];
+    }
     __syncthreads();
+}
+
+// The largest value of the lanes, in registers.
+template <int CTRL, int ROWS> __device__ __forceinline__ float max_moved(float x)
+{
+    return fmaxf(x, __uint_as_float(__builtin_amdgcn_update_dpp(__float_as_uint(x), __float_as_uint(x), CTRL, ROWS, 0xF, false)));
+}
+__device__ __forceinline__ float lane_max(float x)
+{
+    x = max_moved<0x111, 0xF>(x);
+    x = max_moved<0x112, 0xF>(x);
+    x = max_moved<0x114, 0xF>(x);
+    x = max_moved<0x118, 0xF>(x);
+    x = max_moved<0x142, 0xA>(x);
+    x = max_moved<0x143, 0xC>(x);
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), 63));
+}
+
+// The largest and smallest entry, and the number of them (the wavefront's comes in), over the workgroup.
+template <int THREADS> __device__ __forceinline__ void reduce(float& hi, float& lo, uint32_t& live, Shared& s)
+{
+    constexpr int WAVES = THREADS / 64;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    hi = lane_max(hi);
+    lo = -lane_max(-lo);
+    if (lane == 0) {
+        s.wave_max[wave] = hi;
+        s.wave_min[wave] = lo;
+        s.wave_count[wave] = live;
+    }
+    __syncthreads();
+    live = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+        hi = fmaxf(hi, s.wave_max[w]);
+        lo = fminf(lo, s.wave_min[w]);
+        live += s.wave_count[w];
+    }
+    __syncthreads();
+}
+
+template <typename Source> __device__ __forceinline__ void extremes(const Source& row, float& hi, float& lo, uint32_t& live)
+{
+    hi = -infinity();
+    lo = infinity();
+    live = 0;
+    row.each([&](float l, int) {
+        const bool there = live_entry(l);
+        hi = fmaxf(hi, l);
+        lo = fminf(lo, there ? l : infinity());
+        live += (uint32_t)__popcll(__ballot(there));         // of the wavefront
+    });
+}
+
+// The lowest index of an entry that equals hi.
+template <typename Source> __device__ __forceinline__ int index_of(const Source& row, float hi, Shared& s)
+{
+    if (threadIdx.x == 0)
+        s.at = INT32_MAX;
+    __syncthreads();
+    int arg = INT32_MAX;
+    row.each([&](float l, int i) { arg = l == hi && i < arg ? i : arg; });
+    if (arg != INT32_MAX)
+        atomicMin(&s.at, arg);
+    __syncthreads();
+    return s.at;
+}
+
+__device__ __forceinline__ Scale scale_of(float hi, float lo, float t)
+{
+    Scale r;
+    const bool infinite = hi == infinity();
+    r.max = infinite ? 0.f : hi;
+    r.min = infinite ? 0.f : lo;
+    const float range = r.max - r.min, near = kNats * t;
+    if (range * ((float)kNear / kLast) > near) {             // the far buckets are the wider ones
+        r.step = fminf(kNear / near, 3e38f);
+        r.far_step = (kLast - kNear) / (range - near);
+        r.far_from = kNear - near * r.far_step;
+    } else {
+        r.step = range > 0.f ? fminf(kLast / range, 3e38f) : 0.f;
+        r.far_step = 0.f;
+        r.far_from = (float)kLast;
+    }
+    r.c = 46.166241308446828384 / (double)t;                 // 32 log2 e
+    r.top = r.max;
+    r.floor = fmaxf((float)(r.top - 31.191623125197541 * (double)t), -3.4028234663852886e38f);      // 45 ln 2
+    return r;
+}
+
+struct Settings {
+    int64_t stride;
+    int vocab, chunk, chunks;
+    const float* temperature;
+    const int32_t* top_k;
+    const float *top_p, *min_p, *u;
+    int32_t* tokens;
+    float* probs;
+};
+
+__device__ __forceinline__ Wish wish_of(const Settings& a, int64_t n)
+{
+    Wish w;
+    w.t = a.temperature ? a.temperature[n] : 1.f;
+    w.p = a.top_p ? a.top_p[n] : 1.f;
+    w.m = a.min_p && a.min_p[n] > 0.f ? fminf(a.min_p[n], 1.f) : 0.f;     // NaN: off
+    const int k = a.top_k ? a.top_k[n] : 0;
+    w.k = k > 0 && k < a.vocab ? k : 0;
+    w.draw = a.tokens != nullptr;
+    const float u = w.draw ? a.u[n] : 0.f;
+    w.at = u >= 1.f ? 1. - 5.9604644775390625e-8 : u > 0.f ? (double)u : 0.;         // below 1 by an fp32 half step
+    return w;
+}
+
+// The entries into a cleared histogram.
+template <typename Source>
+__device__ __forceinline__ void fill(const Source& row, const Scale& r, bool counted, Shared& s)
+{
+    row.each([&](float l, int) {
+        const int b = bucket_of(r, l);
+        const uint64_t w = steps_of(r, s.table, l);
+        if (w || (counted && live_entry(l))) {
+            if (counted)
+                atomicAdd(&s.h.count[b], 1u);
+            atomicAdd((unsigned long long*)&s.h.mass[b], (unsigned long long)w);
+        }
+    });
+}
+
+__device__ __forceinline__ void start_table(Shared& s)
+{
+    if (threadIdx.x < 32)
+        s.table[threadIdx.x] = exp2(threadIdx.x / 32.);
 }
 
 // The places that are looked for in the order.
@@ -176,97 +522,400 @@ enum Place {
 };
 
 // Whether a step from (count, mass) before it by (dc, dm) takes in the place.
-template <Place P>
-__device__ __forceinline__ bool takes(uint64_t goal, uint64_t mass, uint64_t dm, uint32_t count, uint32_t dc)
+__device__ __forceinline__ bool takes(Place place, uint64_t goal, uint64_t mass, uint64_t dm, uint32_t count, uint32_t dc)
 {
-    if (P == kCount)
+    if (place == kCount)
         return count < goal && goal <= (uint64_t)count + dc;
-    if (P == kReach)
+    if (place == kReach)
         return mass < goal && goal <= mass + dm;
     return mass <= goal && goal < mass + dm;
 }
 
-// The bucket of a scanned histogram that takes in the place, and what is before it.  For kUpTo
-// it is the bucket `given`.
-template <Place P> __device__ __forceinline__ void find_bucket(const Hist& h, Shared& s, uint64_t goal, int given, uint64_t mass0, uint32_t count0)
+// The goals of top-p and of the draw for a weight that is left.
+__device__ __forceinline__ uint64_t reach_goal(float p, uint64_t total)
 {
-    for (int b = threadIdx.x; b < kBuckets; b += kThreads) {
-        const uint64_t before = b ? h.mass[b - 1] : 0;
-        const uint32_t cb = b ? h.count[b - 1] : 0;
-        const bool hit = P == kUpTo ? b == given
-                                    : takes<P>(goal, mass0 + before, h.mass[b] - before, count0 + cb, h.count[b] - cb);
-        if (hit) {
-            s.at = b;
-            s.base_mass = mass0 + before;
-            s.base_count = count0 + cb;
-            s.number = h.count[b] - cb;
+    return (uint64_t)fmax(ceil((double)p * (double)total), 1.);
+}
+__device__ __forceinline__ uint64_t pass_goal(double at, uint64_t total) { return (uint64_t)(at * (double)total); }
+
+// min_p's place: behind the smallest logit whose weight is at least m.  False where that keeps every entry.
+__device__ __forceinline__ bool least_place(const Scale& r, const Wish& w, uint64_t& order, int& bucket)
+{
+    const double least = log((double)w.m), back = 1. / (double)w.t;
+    float l = (float)((double)r.max + least * (double)w.t);
+    auto heavy = [&](float v) { return ((double)v - (double)r.max) * back >= least; };
+    for (int i = 0; i < 4 && !heavy(l); ++i)
+        l = of_key(key_of(l) + 1);
+    for (int i = 0; i < 4 && heavy(of_key(key_of(l) - 1)); ++i)
+        l = of_key(key_of(l) - 1);
+    order = order_of(l, kSampleMaxVocab - 1);
+    bucket = bucket_of(r, l);
+    return l > r.min;
+}
+
+// The first bucket whose sum takes in the goal, by one wavefront: of every sixteenth, then of the sixteen before it.
+__device__ __forceinline__ int first_bucket(const Hist& h, Place place, uint64_t goal)
+{
+    const int lane = threadIdx.x & 63;
+    auto reached = [&](int b) {
+        return place == kCount ? h.count[b] >= goal : place == kReach ? h.mass[b] >= goal : h.mass[b] > goal;
+    };
+    const uint64_t coarse = __ballot(reached(16 * lane + 15));
+    const int from = coarse ? 16 * (__ffsll((unsigned long long)coarse) - 1) : kBuckets - 16;
+    const uint64_t fine = __ballot(reached(from + (lane & 15)));
+    return fine ? from + __ffsll((unsigned long long)fine) - 1 : kLast;
+}
+
+// Each filter leaves a weight between two sums of buckets; so each goal, and the bucket of each place, lies between
+// two others.  By the first wavefront, into s.plan.
+__device__ __forceinline__ void make_plan(const Hist& h, const Scale& r, const Wish& w, Shared& s)
+{
+    if (threadIdx.x < 64) {
+        int from[4], to[4], n = 0;
+        Plan q;
+        uint64_t lo = h.mass[kLast], hi = lo;                // the weight that is left
+        q.k = w.k > 0 && (uint32_t)w.k < h.count[kLast];
+        q.p = w.p < 1.f;
+        q.m = -1;
+        q.m_order = kNowhere;
+        if (q.k) {
+            const int b = first_bucket(h, kCount, w.k);
+            lo = h.mass_before(b);
+            hi = h.mass[b];
+            from[0] = to[0] = b;
+            n = 1;
+        }
+        if (q.p) {
+            const uint64_t least = reach_goal(w.p, lo);
+            const int f = first_bucket(h, kReach, least), t = first_bucket(h, kReach, reach_goal(w.p, hi));
+            lo = least;
+            hi = h.mass[t] < hi ? h.mass[t] : hi;
+            from[n] = f;
+            to[n++] = t;
+        }
+        uint64_t order;
+        int bucket;
+        if (w.m > 0.f && least_place(r, w, order, bucket)) {
+            q.m = bucket;
+            q.m_order = order;
+            lo = h.mass_before(bucket) < lo ? h.mass_before(bucket) : lo;
+            hi = h.mass[bucket] < hi ? h.mass[bucket] : hi;
+            from[n] = to[n] = bucket;
+            ++n;
+        }
+        if (w.draw) {
+            from[n] = first_bucket(h, kPass, pass_goal(w.at, lo));
+            to[n] = first_bucket(h, kPass, pass_goal(w.at, hi));
+            ++n;
+        }
+        if (threadIdx.x == 0) {
+            // overlapping ranges become one: an entry is collected once
+            int m = 0;
+            for (int i = 0; i < n; ++i) {
+                int f = from[i], t = to[i];
+                for (int j = 0; j < m;)
+                    if (from[j] <= t && to[j] >= f) {
+                        f = from[j] < f ? from[j] : f;
+                        t = to[j] > t ? to[j] : t;
+                        --m;
+                        from[j] = from[m];
+                        to[j] = to[m];
+                        j = 0;
+                    } else {
+                        ++j;
+                    }
+                from[m] = f;
+                to[m++] = t;
+            }
+            q.ranges = m;
+            for (int i = 0; i < 4; ++i) {
+                q.from[i] = i < m ? (float)from[i] : infinity();
+                q.to[i] = i < m ? (float)(to[i] + 1) : -infinity();
+            }
+            s.plan = q;
         }
     }
     __syncthreads();
 }
 
-// The place's entry, in s.found_order, and the weight up to and with it, in s.found_mass.  For kUpTo:
-// the weight of the entries whose place is at most `goal`, which lies in bucket `given`.
-template <Place P, typename T>
-__device__ void find(const T* row, int vocab, bool infinite, const Row& r, Shared& s, uint64_t goal, int given)
+// The entries for which in(l, i) holds, into the list (in any order); s.number of them.
+template <typename Source, typename F> __device__ __forceinline__ void gather(const Source& row, Shared& s, F in)
 {
-    const int tid = threadIdx.x;
-    if (tid == 0)
+    if (threadIdx.x == 0)
         s.number = 0;
     __syncthreads();
-    find_bucket<P>(s.h, s, goal, given, 0, 0);
-    const int bucket = s.at;
-    uint64_t prefix = 0;
-    int shift = 32 + kIndexBits;
-    auto in = [&](float l, uint64_t order) { return bucket_of(r, l) == bucket && order >> shift == prefix; };
-    while (s.number > kList) {                               // shift is 0 at the latest when one entry is left
-        const int next = shift > kDigitBits ? shift - kDigitBits : 0;
-        const uint64_t mass0 = s.base_mass;
-        const uint32_t count0 = s.base_count;
-        clear(s.x.digits);
-        __syncthreads();
-        each(row, vocab, [&](float raw, int i) {
-            const float l = entry(raw, infinite);
-            if (l > -__builtin_inff()) {
-                const uint64_t order = order_of(l, i);
-                if (in(l, order)) {
-                    const int d = (int)(order >> next) & ((1 << (shift - next)) - 1);
-                    atomicAdd(&s.x.digits.count[d], 1u);
-                    atomicAdd((unsigned long long*)&s.x.digits.mass[d], (unsigned long long)steps_of(weight_of(r, s.table, l)));
+    row.each4([&](const float(&l)[4], int i) {
+        bool hit[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            hit[e] = in(l[e], i + e);
+        if (hit[0] | hit[1] | hit[2] | hit[3]) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (hit[e]) {
+                    const uint32_t at = atomicAdd(&s.number, 1u);
+                    if (at < kList)
+                        s.x.list.order[at] = order_of(l[e], i + e);
                 }
-            }
-        });
-        scan(s.x.digits, s);
-        find_bucket<P>(s.x.digits, s, goal, (int)(goal >> next) & ((1 << (shift - next)) - 1), mass0, count0);
-        prefix = prefix << (shift - next) | (uint32_t)s.at;
-        shift = next;
-    }
-    const uint64_t mass0 = s.base_mass;
-    const uint32_t count0 = s.base_count;
-    __syncthreads();
-    if (tid == 0) {
-        s.number = 0;
-        s.found_mass = mass0;
-    }
-    __syncthreads();
-    each(row, vocab, [&](float raw, int i) {
-        const float l = entry(raw, infinite);
-        if (l > -__builtin_inff()) {
-            const uint64_t order = order_of(l, i);
-            if (in(l, order)) {
-                const uint32_t at = atomicAdd(&s.number, 1u);
-                if (at < kList) {                            // always: the histogram counted them
-                    s.x.list.order[at] = order;
-                    s.x.list.weight[at] = steps_of(weight_of(r, s.table, l));
-                }
-            }
         }
     });
     __syncthreads();
-    const int n = min((int)s.number, kList);
-    if (tid < n) {
-        const uint64_t mine = s.x.list.order[tid], w = s.x.list.weight[tid];
-        if (P == kUpTo) {
+}
+
+// Those of the plan's ranges.
+template <typename Source> __device__ __forceinline__ void gather_plan(const Source& row, const Scale& r, Shared& s)
+{
+    const Plan q = s.plan;
+    gather(row, s, [&](float l, int) {
+        const float f = height_of(r, l);
+        bool hit = (f >= q.from[0] && f < q.to[0]) | (f >= q.from[1] && f < q.to[1]);
+        if (q.ranges > 2)
+            hit |= (f >= q.from[2] && f < q.to[2]) | (f >= q.from[3] && f < q.to[3]);
+        return hit && live_entry(l);
+    });
+}
+
+// The value of the lane `mask` away.
+__device__ __forceinline__ uint64_t other(uint64_t x, int mask)
+{
+    return (uint64_t)(uint32_t)__shfl_xor((int)(x >> 32), mask) << 32 | (uint32_t)__shfl_xor((int)x, mask);
+}
+
+// The places looked up one after the other among the s.number <= 64 entries of the list, each compared with all of its
+// bucket for what is before it.  By the first wavefront, into s.choice.
+__device__ __forceinline__ void choose_few(const Hist& h, const Scale& r, const Wish& w, Shared& s)
+{
+    if (threadIdx.x < 64) {
+        const int lane = threadIdx.x, n = (int)s.number;
+        const Plan q = s.plan;
+        const bool there = lane < n;
+        const uint64_t x = there ? s.x.list.order[lane] : kNowhere;
+        const int bucket = there ? bucket_of(r, logit_of(x)) : -1;
+        const uint64_t own = there ? steps_of(r, s.table, logit_of(x)) : 0;
+        uint64_t mass = there ? h.mass_before(bucket) : 0;
+        uint32_t count = there ? h.count_before(bucket) : 0;
+        for (int i = 0; i < n; ++i) {
+            const bool before = at_lane(x, i) < x && (int)at_lane((uint32_t)bucket, i) == bucket;
+            mass += before ? at_lane(own, i) : 0;
+            count += before;
+        }
+        Choice c = {kNowhere, h.mass[kLast], -1};
+        auto look = [&](Place place, uint64_t goal) {
+            const uint64_t hit = __ballot(there && takes(place, goal, mass, own, count, 1));
+            const int at = hit ? __ffsll((unsigned long long)hit) - 1 : 0;
+            c.cut = at_lane(x, at);
+            c.total = at_lane(mass + own, at);
+        };
+        if (q.k)
+            look(kCount, w.k);
+        if (q.p)
+            look(kReach, reach_goal(w.p, c.total));
+        if (q.m >= 0 && q.m_order < c.cut) {                 // with the entries of its bucket that are not behind it
+            c.total = h.mass_before(q.m) + at_lane(lane_scan(there && bucket == q.m && x <= q.m_order ? own : (uint64_t)0), 63);
+            c.cut = q.m_order;
+        }
+        if (w.draw) {
+            const uint64_t hit = __ballot(there && takes(kPass, pass_goal(w.at, c.total), mass, own, count, 1));
+            c.token = (int)(at_lane(x, hit ? __ffsll((unsigned long long)hit) - 1 : 0) & (kSampleMaxVocab - 1));
+        }
+        if (lane == 0)
+            s.choice = c;
+    }
+    __syncthreads();
+}
+
+// The same with the list sorted (bitonic: within wavefronts by exchanged registers).
+template <int THREADS>
+__device__ __forceinline__ void choose_sorted(const Hist& h, const Scale& r, const Wish& w, Shared& s)
+{
+    constexpr int PER = kList / THREADS;                     // entries j * THREADS + tid of a thread
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = (int)s.number;
+    const Plan q = s.plan;
+    int size = 64;
+    while (size < n)
+        size *= 2;
+    uint64_t x[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+        x[j] = j * THREADS + tid < n ? s.x.list.order[j * THREADS + tid] : kNowhere;
+    for (int run = 2; run <= size; run *= 2)
+        for (int far = run / 2; far > 0; far /= 2) {
+            if (far >= 64) {                                 // another wavefront's
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    s.x.list.order[j * THREADS + tid] = x[j];
+                __syncthreads();
+            }
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                const int i = j * THREADS + tid;
+                if (j * THREADS >= size)
+                    break;
+                const uint64_t y = far >= 64 ? s.x.list.order[i ^ far] : other(x[j], far);
+                const bool up = ((i & run) == 0) == ((i & far) == 0);        // the smaller one is kept here
+                x[j] = (x[j] < y) == up ? x[j] : y;
+            }
+        }
+    __syncthreads();
+    // weights, and their sums in the order of the list
+    uint64_t own[PER], sum[PER];
+    int bucket[PER];
+    uint64_t before = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int i = j * THREADS + tid;
+        const bool there = i < n;
+        const float l = there ? logit_of(x[j]) : r.max;
+        bucket[j] = there ? bucket_of(r, l) : kLast;
+        own[j] = there ? steps_of(r, s.table, l) : 0;
+        sum[j] = lane_scan(own[j]);
+        if (lane == 63)
+            s.wave_mass[wave] = sum[j];
+        if (there)
+            s.x.list.order[i] = x[j];
+        __syncthreads();
+        uint64_t all = 0;
+#pragma unroll
+        for (int v = 0; v < THREADS / 64; ++v) {
+            sum[j] += v < wave ? s.wave_mass[v] : 0;
+            all += s.wave_mass[v];
+        }
+        sum[j] += before;
+        before += all;
+        __syncthreads();
+    }
+    // a bucket's first entry leaves its place and the sum before it
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int i = j * THREADS + tid;
+        if (i < n && (i == 0 || bucket_of(r, logit_of(s.x.list.order[i - 1])) != bucket[j])) {
+            s.first[bucket[j]] = i;
+            s.x.list.mass[i] = sum[j] - own[j];
+        }
+    }
+    __syncthreads();
+    uint64_t mass[PER];
+    uint32_t count[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int i = j * THREADS + tid;
+        mass[j] = count[j] = 0;
+        if (i < n) {
+            const int f = s.first[bucket[j]];
+            mass[j] = h.mass_before(bucket[j]) + (sum[j] - own[j] - s.x.list.mass[f]);
+            count[j] = h.count_before(bucket[j]) + (uint32_t)(i - f);
+        }
+    }
+    Choice c = {kNowhere, h.mass[kLast], -1};
+    auto look = [&](Place place, uint64_t goal) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (j * THREADS + tid < n && takes(place, goal, mass[j], own[j], count[j], 1)) {
+                s.found_order = x[j];
+                s.found_mass = mass[j] + own[j];
+            }
+        __syncthreads();
+    };
+    if (q.k) {
+        look(kCount, w.k);
+        c.cut = s.found_order;
+        c.total = s.found_mass;
+    }
+    if (q.p) {
+        look(kReach, reach_goal(w.p, c.total));
+        c.cut = s.found_order;
+        c.total = s.found_mass;
+    }
+    if (q.m >= 0 && q.m_order < c.cut) {                     // up to the last entry of its bucket that is not behind it
+        __syncthreads();
+        if (tid == 0)
+            s.found_mass = h.mass_before(q.m);
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (j * THREADS + tid < n && bucket[j] == q.m && x[j] <= q.m_order)
+                atomicMax((unsigned long long*)&s.found_mass, (unsigned long long)(mass[j] + own[j]));
+        __syncthreads();
+        c.cut = q.m_order;
+        c.total = s.found_mass;
+    }
+    if (w.draw) {
+        look(kPass, pass_goal(w.at, c.total));
+        c.token = (int)(s.found_order & (kSampleMaxVocab - 1));
+    }
+    if (tid == 0)
+        s.choice = c;
+    __syncthreads();
+}
+
+// The bucket of a scanned histogram that takes in the place, and what is before it.  For kUpTo
+// it is the bucket `given`.
+template <int THREADS>
+__device__ __forceinline__ void find_bucket(const Hist& h, Shared& s, Place place, uint64_t goal, int given,
+                                            uint64_t mass0, uint32_t count0)
+{
+    for (int b = threadIdx.x; b < kBuckets; b += THREADS) {
+        const uint64_t m0 = h.mass_before(b);
+        const uint32_t c0 = h.count_before(b);
+        if (place == kUpTo ? b == given : takes(place, goal, mass0 + m0, h.mass[b] - m0, count0 + c0, h.count[b] - c0)) {
+            s.at = b;
+            s.base_mass = mass0 + m0;
+            s.base_count = count0 + c0;
+        }
+    }
+    __syncthreads();
+}
+
+// One place after the other, where the list cannot hold the entries of all: its bucket's entries are cut by digits of
+// the order until kList are left, and compared with each other.  s.found_order is the place's entry and
+// s.found_mass the weight up to and with it; for kUpTo the weight of the entries whose place is at most `goal`, which
+// lies in bucket `given`.
+template <typename Source>
+__device__ __forceinline__ void find(const Source& row, const Scale& r, Shared& s, Place place, uint64_t goal, int given)
+{
+    constexpr int THREADS = Source::THREADS;
+    const int tid = threadIdx.x;
+    find_bucket<THREADS>(s.h, s, place, goal, given, 0, 0);
+    const int bucket = s.at;
+    uint64_t prefix = 0;
+    int shift = 32 + kIndexBits;
+    auto in = [&](float l, int i) {
+        return live_entry(l) && bucket_of(r, l) == bucket && order_of(l, i) >> shift == prefix;
+    };
+    gather(row, s, in);
+#pragma unroll 1
+    while (s.number > kList) {                               // at shift 0 one entry is left
+        const int next = shift > kDigitBits ? shift - kDigitBits : 0, mask = (1 << (shift - next)) - 1;
+        const uint64_t mass0 = s.base_mass;
+        const uint32_t count0 = s.base_count;
+        clear<THREADS>(s.x.digits);
+        __syncthreads();
+        row.each([&](float l, int i) {
+            if (in(l, i)) {
+                const int d = (int)(order_of(l, i) >> next) & mask;
+                atomicAdd(&s.x.digits.count[d], 1u);
+                atomicAdd((unsigned long long*)&s.x.digits.mass[d], (unsigned long long)steps_of(r, s.table, l));
+            }
+        });
+        scan<THREADS>(s.x.digits, s);
+        find_bucket<THREADS>(s.x.digits, s, place, goal, (int)(goal >> next) & mask, mass0, count0);
+        prefix = prefix << (shift - next) | (uint32_t)s.at;
+        shift = next;
+        gather(row, s, in);
+    }
+    const uint64_t mass0 = s.base_mass;
+    const uint32_t count0 = s.base_count;
+    const int n = (int)s.number;
+    for (int j = tid; j < n; j += THREADS)
+        s.x.list.mass[j] = steps_of(r, s.table, logit_of(s.x.list.order[j]));
+    if (tid == 0)
+        s.found_mass = mass0;
+    __syncthreads();
+    for (int j = tid; j < n; j += THREADS) {
+        const uint64_t mine = s.x.list.order[j], w = s.x.list.mass[j];
+        if (place == kUpTo) {
             if (mine <= goal)
                 atomicAdd((unsigned long long*)&s.found_mass, (unsigned long long)w);
         } else {
@@ -274,10 +923,10 @@ __device__ void find(const T* row, int vocab, bool infinite, const Row& r, Share
             uint32_t count = count0;
             for (int i = 0; i < n; ++i) {
                 const bool before = s.x.list.order[i] < mine;
-                mass += before ? s.x.list.weight[i] : 0;
+                mass += before ? s.x.list.mass[i] : 0;
                 count += before;
             }
-            if (takes<P>(goal, mass, w, count, 1)) {
+            if (takes(place, goal, mass, w, count, 1)) {
                 s.found_order = mine;
                 s.found_mass = mass + w;
             }
@@ -286,151 +935,146 @@ __device__ void find(const T* row, int vocab, bool infinite, const Row& r, Share
     __syncthreads();
 }
 
+template <typename Source>
+__device__ __forceinline__ void choose_slowly(const Source& row, const Scale& r, const Wish& w, Shared& s)
+{
+    const Plan q = s.plan;
+    Choice c = {kNowhere, s.h.mass[kLast], -1};
+#pragma unroll 1
+    for (int step = 0; step < 4; ++step) {
+        Place place = kPass;
+        uint64_t goal = 0;
+        if (step == 0) {
+            if (!q.k)
+                continue;
+            place = kCount;
+            goal = w.k;
+        } else if (step == 1) {
+            if (!q.p)
+                continue;
+            place = kReach;
+            goal = reach_goal(w.p, c.total);
+        } else if (step == 2) {
+            if (q.m < 0 || q.m_order >= c.cut)
+                continue;
+            place = kUpTo;
+            goal = q.m_order;
+        } else {
+            if (!w.draw)
+                continue;
+            goal = pass_goal(w.at, c.total);
+        }
+        find(row, r, s, place, goal, q.m);
+        if (step < 3) {
+            c.cut = place == kUpTo ? goal : s.found_order;
+            c.total = s.found_mass;
+        } else {
+            c.token = (int)(s.found_order & (kSampleMaxVocab - 1));
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0)
+        s.choice = c;
+    __syncthreads();
+}
+
+// The choice from a scanned histogram, a plan and the list; rows that the list does not hold are read again.
+template <typename Source>
+__device__ __forceinline__ void choose(const Source& again, const Scale& r, const Wish& w, Shared& s)
+{
+    if (s.number <= 64)
+        choose_few(s.h, r, w, s);
+    else if (s.number <= kList)
+        choose_sorted<Source::THREADS>(s.h, r, w, s);
+    else
+        choose_slowly(again, r, w, s);
+}
+
+// The probability of an entry after the cut, in the share that the kept weight has of it.
+__device__ __forceinline__ float probability(const Scale& r, const double* table, const Choice& c, double share, float l, int i)
+{
+    return live_entry(l) && order_of(l, i) <= c.cut ? (float)(weight_of(r, table, l) * share) : 0.f;
+}
+
 }  // namespace
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void sample_kernel(const T* __restrict__ logits, int64_t stride, int vocab,
-                                                          const float* __restrict__ temperature,
-                                                          const int32_t* __restrict__ top_k,
-                                                          const float* __restrict__ top_p,
-                                                          const float* __restrict__ min_p, const float* __restrict__ u,
-                                                          int32_t* __restrict__ tokens, float* __restrict__ probs)
+// A row of logits by one workgroup.
+template <typename T, typename Source>
+__global__ __launch_bounds__(Source::THREADS) void sample_row_kernel(const T* __restrict__ logits, Settings a)
 {
+    constexpr int THREADS = Source::THREADS;
     __shared__ Shared s;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, vocab = a.vocab;
     const int64_t n = blockIdx.x;
-    const T* row = logits + n * stride;
-    float* out = probs ? probs + n * vocab : nullptr;
-    const float t = temperature ? temperature[n] : 1.f;
-    const float inf = __builtin_inff();
-
-    // the largest entry (the first of equal ones) and the smallest
-    float hi = -inf, lo = inf;
-    int arg = INT32_MAX;
-    each(row, vocab, [&](float raw, int i) {
-        const float l = entry(raw);
-        if (l > hi || (l == hi && i < arg)) {
-            hi = l;
-            arg = i;
-        }
-        if (l > -inf)
-            lo = fminf(lo, l);
-    });
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const float h2 = __shfl_xor(hi, m), l2 = __shfl_xor(lo, m);
-        const int a2 = __shfl_xor(arg, m);
-        if (h2 > hi || (h2 == hi && a2 < arg)) {
-            hi = h2;
-            arg = a2;
-        }
-        lo = fminf(lo, l2);
-    }
-    if (lane == 0) {
-        s.wave_max[wave] = hi;
-        s.wave_min[wave] = lo;
-        s.wave_arg[wave] = arg;
-    }
-    if (tid < 32)
-        s.table[tid] = exp2(tid / 32.);
-    clear(s.h);
-    __syncthreads();
-    for (int w = 0; w < kWaves; ++w) {
-        const float h2 = s.wave_max[w];
-        if (h2 > hi || (h2 == hi && s.wave_arg[w] < arg)) {
-            hi = h2;
-            arg = s.wave_arg[w];
-        }
-        lo = fminf(lo, s.wave_min[w]);
-    }
-    const bool none = hi == -inf;
-    if (none || !(t > 0.f)) {                                // nothing to draw from, or the largest is taken
-        if (tokens && tid == 0)
-            tokens[n] = none ? -1 : arg;
+    Source row;
+    row.row = logits + n * a.stride;
+    row.first = 0;
+    row.end = vocab;
+    const Wish w = wish_of(a, n);
+    row.load();
+    float* out = a.probs ? a.probs + n * vocab : nullptr;
+    float hi, lo;
+    uint32_t live;
+    extremes(row, hi, lo, live);
+    start_table(s);
+    clear<THREADS>(s.h);
+    reduce<THREADS>(hi, lo, live, s);
+    if (live == 0 || !(w.t > 0.f)) {                         // nothing to draw from, or the largest is taken
+        const int arg = live == 0 ? -1 : index_of(row, hi, s);
+        if (a.tokens && tid == 0)
+            a.tokens[n] = arg;
         if (out)
-            for (int i = tid; i < vocab; i += kThreads)
-                out[i] = !none && i == arg ? 1.f : 0.f;
+            for (int i = tid; i < vocab; i += THREADS)
+                out[i] = i == arg ? 1.f : 0.f;
         return;
     }
-    const bool infinite = hi == inf;
-    Row r;
-    r.max = infinite ? 0.f : hi;
-    const float span = fminf(infinite ? 0.f : hi - lo, 32.f * t);
-    r.step = span > 0.f ? fminf((kBuckets - 1) / span, 3e38f) : 0.f;
-    r.c = 46.166241308446828384 / (double)t;                 // 32 log2 e
-
-    each(row, vocab, [&](float raw, int i) {
-        const float l = entry(raw, infinite);
-        if (l > -inf) {
-            const int b = bucket_of(r, l);
-            atomicAdd(&s.h.count[b], 1u);
-            atomicAdd((unsigned long long*)&s.h.mass[b], (unsigned long long)steps_of(weight_of(r, s.table, l)));
-        }
-    });
-    scan(s.h, s);
-
-    uint64_t cut = ~0ull;                                    // the last place that is kept
-    uint64_t total = s.h.mass[kBuckets - 1];
-    const int k = top_k ? top_k[n] : 0;
-    if (k > 0 && (uint32_t)k < s.h.count[kBuckets - 1]) {
-        find<kCount>(row, vocab, infinite, r, s, (uint64_t)k, 0);
-        cut = s.found_order;
-        total = s.found_mass;
+    const Scale r = scale_of(hi, lo, w.t);
+    Streamed<T, THREADS> again = {row.row, 0, vocab, false};
+    if (hi == infinity()) {                                  // nothing else counts
+        row.only_infinite();
+        again.only_infinite();
+        float h2, l2;
+        extremes(row, h2, l2, live);
+        reduce<THREADS>(h2, l2, live, s);
     }
-    const float p = top_p ? top_p[n] : 1.f;
-    const uint64_t whole = total;
-    if (p < 1.f) {
-        const uint64_t goal = (uint64_t)fmax(ceil((double)p * (double)whole), 1.);
-        find<kReach>(row, vocab, infinite, r, s, goal, 0);
-        cut = s.found_order;
-        total = s.found_mass;
-    }
-    const float mp = min_p && min_p[n] > 0.f ? fminf(min_p[n], 1.f) : 0.f;       // NaN: off
-    if (mp > 0.f) {
-        // the smallest logit whose weight is at least mp
-        const double least = log((double)mp), back = 1. / (double)t;
-        float l = (float)((double)r.max + least * (double)t);
-        auto heavy = [&](float v) { return ((double)v - (double)r.max) * back >= least; };
-        for (int i = 0; i < 4 && !heavy(l); ++i)
-            l = of_key(key_of(l) + 1);
-        for (int i = 0; i < 4 && heavy(of_key(key_of(l) - 1)); ++i)
-            l = of_key(key_of(l) - 1);
-        if (l > (infinite ? 0.f : lo)) {
-            const uint64_t last = order_of(l, kSampleMaxVocab - 1);
-            if (last < cut) {
-                find<kUpTo>(row, vocab, infinite, r, s, last, bucket_of(r, l));
-                cut = last;
-                total = s.found_mass;
-            }
-        }
-    }
+    fill(row, r, w.k > 0, s);
+    scan<THREADS>(s.h, s);
+    make_plan(s.h, r, w, s);
+    gather_plan(row, r, s);
+    choose(again, r, w, s);
+    const Choice c = s.choice;
+    if (a.tokens && tid == 0)
+        a.tokens[n] = c.token;
     if (out) {
-        const double share = 1. / ((double)total / kOne);
-        each(row, vocab, [&](float raw, int i) {
-            const float l = entry(raw, infinite);
-            out[i] = l > -inf && order_of(l, i) <= cut ? (float)(weight_of(r, s.table, l) * share) : 0.f;
+        const double share = kOne / (double)c.total;
+        row.each([&](float l, int i) {
+            if (i < vocab)
+                out[i] = probability(r, s.table, c, share, l, i);
         });
-    }
-    if (tokens) {
-        const float x = u[n];
-        const double at = x >= 1.f ? 1. - 5.9604644775390625e-8 : x > 0.f ? (double)x : 0.;      // below 1 by an fp32 half step
-        find<kPass>(row, vocab, infinite, r, s, (uint64_t)(at * (double)total), 0);
-        if (tid == 0)
-            tokens[n] = (int32_t)(s.found_order & (kSampleMaxVocab - 1));
     }
 }
 
-bool sample_fits(int64_t rows, int) { return rows <= UINT32_MAX / kThreads; }
+bool sample_fits(int64_t rows, int) { return rows <= UINT32_MAX / 1024; }
 
 size_t sample_workspace_bytes(int64_t, int) { return 0; }
+
+template <typename T, typename Source> static hipError_t launch_rows(const SampleArgs& p, hipStream_t stream)
+{
+    const Settings a = {p.stride, p.vocab, 0, 0, p.temperature, p.top_k, p.top_p, p.min_p, p.u, p.tokens, p.probs};
+    hipLaunchKernelGGL((sample_row_kernel<T, Source>), dim3((unsigned)p.rows), dim3(Source::THREADS), 0, stream,
+                       (const T*)p.logits, a);
+    return hipGetLastError();
+}
 
 template <typename T> static hipError_t launch_T(const SampleArgs& p, hipStream_t stream)
 {
     if (p.rows == 0)
         return hipSuccess;
-    hipLaunchKernelGGL((sample_kernel<T>), dim3((unsigned)p.rows), dim3(kThreads), 0, stream, (const T*)p.logits,
-                       p.stride, p.vocab, p.temperature, p.top_k, p.top_p, p.min_p, p.u, p.tokens, p.probs);
-    return hipGetLastError();
+    if (p.vocab <= 256 * 8) return launch_rows<T, Held<T, 256, 8>>(p, stream);
+    if (p.vocab <= 256 * 32) return launch_rows<T, Held<T, 256, 32>>(p, stream);
+    if (p.vocab <= 1024 * 16) return launch_rows<T, Held<T, 1024, 16>>(p, stream);
+    if (p.vocab <= 1024 * 32) return launch_rows<T, Held<T, 1024, 32>>(p, stream);
+    return launch_rows<T, Streamed<T, 1024>>(p, stream);
 }
 
 hipError_t launch_sample(const SampleArgs& p, hipStream_t stream)
