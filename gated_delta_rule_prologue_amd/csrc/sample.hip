@@ -6,18 +6,28 @@
 // first k; those before which less than p of the weight (of the first k) has passed; those with
 // w >= min_p.  The token is the first at which the running weight exceeds u times the weight
 // that is kept, so the draw too is a place in that order.  No sort of the row is needed for it:
-// a histogram of the distance from the maximum (768 buckets over at most 16 nats, 256 over what is behind) bounds the weight before each place, and so the few buckets in which each can lie; only their entries
-// are collected and sorted, and the places are looked up one after the other.  More entries in those buckets than
-// kList (ties, places in the last bucket) are cut further by digits of (logit, index).
+// a histogram of the distance from the maximum (768 buckets over 16 nats, 256 over what is
+// behind, or 1024 over less) bounds the weight before each place, and so the few buckets in
+// which each can lie; only their entries are collected, and the places are looked up one after
+// the other: up to 64 entries by one wavefront that compares each with all, up to 1024 sorted.
+// More entries in those buckets (ties, places in the last bucket) are cut further by digits of
+// (logit, index).
 //
 // Weights are formed in 64 bits and added as whole numbers in steps of 2^-43 of the largest: sums
 // of 2^20 of them fit 63 bits, no order of additions changes them, and the choice agrees with
 // one made in 64-bit floating point but at a border nearer than some 10^-11.
 //
-// Bound by a chain of passes where there are few rows, by the arithmetic of the weights (some 25
-// instructions an entry) where there are many.  A row of up to 32,768 entries stays in the registers of one
-// workgroup for all passes.  Longer rows, and shorter ones where they are few, are cut into chunks, one workgroup
-// each, with a launch for the maximum, the histogram, the collection and the choice.
+// Bound by a chain of dependent passes where there are few rows (maximum, histogram, its sums,
+// collection, lookup: some 4 us each), by the arithmetic of the weights (some 35 instructions an
+// entry, half of them 64-bit) and the 64-bit LDS additions where there are many; reading the
+// logits is a tenth of it.  A row of up to 32,768 entries stays in the registers of one workgroup
+// for all passes, so they are one launch: 1 row of 32,000 20 us, 64 25 us, 256 in bf16 28 us.
+// Longer rows are read again by each pass, and while they are few they are cut into chunks, one
+// workgroup each, with a launch for the maximum, the histograms, the collection and the choice
+// (and one for the distribution): 64 rows of 128,000 50 us, of which 7, 12, 16 and 12 are the
+// launches; 256 rows, whole, 103 us.
+#include <type_traits>
+
 #include "common.h"
 #include "kernels.h"
 #include "norm_rows.h"
@@ -115,34 +125,52 @@ __device__ __forceinline__ float height_of(const Scale& r, float l)
 }
 __device__ __forceinline__ int bucket_of(const Scale& r, float l) { return (int)height_of(r, l); }
 
+// The constants of the weights' arithmetic, held in registers: as literals each would be moved into the accumulator
+// of its product first.
+struct Constants {
+    double whole, c4, c3, c2, c1, one, steps;
+    __device__ __forceinline__ Constants()
+        : whole(6755399441055744.),                          // 1.5 * 2^52: a sum's low word is its whole part
+          c4(9.17256270182464329e-9), c3(1.69385097243718201e-6), c2(2.34596198202246789e-4),
+          c1(2.16608493924982909e-2),                        // powers of ln 2 / 32 over 4!, 3!, 2!, 1!
+          one(1.), steps(4503599627370496.)                  // 2^52: the steps are the sum's mantissa
+    {
+        asm volatile("" : "+v"(whole), "+v"(c4), "+v"(c3), "+v"(c2), "+v"(c1), "+v"(one), "+v"(steps));
+    }
+};
+
 // exp((l - max) / temperature): 2^(n / 32) from the table, and the rest of the exponent, at most
-// ln 2 / 64, by its series to the fourth power (10^-12).  Adding 1.5 * 2^52 leaves n in the sum's low word.
-__device__ __forceinline__ double series_of(const Scale& r, float l, int& n)
+// ln 2 / 64, by its series to the fourth power (10^-12).
+__device__ __forceinline__ double series_of(const Constants& k, const Scale& r, float l, int& n)
 {
-    const double d = (double)l - r.top, m = __builtin_fma(d, r.c, 6755399441055744.);
-    const double t = __builtin_fma(d, r.c, -(m - 6755399441055744.));
-    double s = __builtin_fma(t, 9.17256270182464302e-09, 1.69385097243718210e-06);               // powers of ln 2 / 32 over 4!, 3!, 2!
-    s = __builtin_fma(s, t, 2.34596198202246799e-04);
-    s = __builtin_fma(s, t, 2.16608493924982902e-02);
+    const double d = (double)l - r.top, m = __builtin_fma(d, r.c, k.whole);
+    const double t = __builtin_fma(d, r.c, -(m - k.whole));
+    double s = __builtin_fma(t, k.c4, k.c3);
+    s = __builtin_fma(s, t, k.c2);
+    s = __builtin_fma(s, t, k.c1);
     n = (int)__double_as_longlong(m);
-    return __builtin_fma(s, t, 1.);
+    return __builtin_fma(s, t, k.one);
 }
 // In steps of 2^-43; entries below `floor` have less than half a step.
-__device__ __forceinline__ uint64_t steps_of(const Scale& r, const double* table, float l)
+__device__ __forceinline__ uint64_t steps_of(const Constants& k, const Scale& r, const double* table, float l)
 {
     int n;
-    const double s = series_of(r, fmaxf(l, r.floor), n), t = table[n & 31];
+    const double s = series_of(k, r, fmaxf(l, r.floor), n), t = table[n & 31];
     const double e = __hiloint2double(__double2hiint(t) + (((n >> 5) + 43) << 20), __double2loint(t));
-    const double w = __builtin_fma(e, s, 4503599627370496.); // + 2^52: the steps are the mantissa
+    const double w = __builtin_fma(e, s, k.steps);
     const bool some = l >= r.floor;
     return (uint64_t)(uint32_t)(some ? __double2hiint(w) & 0xfffff : 0) << 32 | (uint32_t)(some ? __double2loint(w) : 0);
+}
+__device__ __forceinline__ uint64_t steps_of(const Scale& r, const double* table, float l)
+{
+    return steps_of(Constants(), r, table, l);
 }
 __device__ __forceinline__ double weight_of(const Scale& r, const double* table, float l)
 {
     if (((double)l - r.top) * r.c < -32. * 1100.)
         return 0.;
     int n;
-    const double s = series_of(r, l, n);
+    const double s = series_of(Constants(), r, l, n);
     return ldexp(table[n & 31] * s, n >> 5);
 }
 
@@ -496,14 +524,24 @@ __device__ __forceinline__ Wish wish_of(const Settings& a, int64_t n)
 template <typename Source>
 __device__ __forceinline__ void fill(const Source& row, const Scale& r, bool counted, Shared& s)
 {
-    row.each([&](float l, int) {
-        const int b = bucket_of(r, l);
-        const uint64_t w = steps_of(r, s.table, l);
-        if (w || (counted && live_entry(l))) {
-            if (counted)
-                atomicAdd(&s.h.count[b], 1u);
-            atomicAdd((unsigned long long*)&s.h.mass[b], (unsigned long long)w);
+    const Constants k;
+    row.each4([&](const float(&l)[4], int) {
+        int b[4];
+        uint64_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            b[e] = bucket_of(r, l[e]);
+            w[e] = steps_of(k, r, s.table, l[e]);
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (w[e])
+                atomicAdd((unsigned long long*)&s.h.mass[b[e]], (unsigned long long)w[e]);
+        if (counted)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (live_entry(l[e]))
+                    atomicAdd(&s.h.count[b[e]], 1u);
     });
 }
 
@@ -1054,22 +1092,336 @@ __global__ __launch_bounds__(Source::THREADS) void sample_row_kernel(const T* __
     }
 }
 
+// ---- rows cut into chunks
+
+// What is left of a row between the launches.
+struct Parts {
+    float *hi, *lo;                                          // [rows][chunks]
+    uint32_t *live, *number;                                 // [rows][chunks]; number: entries in the chunk's list
+    uint64_t* mass;                                          // [rows][chunks][kBuckets], then of the row [rows][kBuckets]
+    uint32_t* count;
+    uint64_t* list;                                          // [rows][chunks][kList]
+    Plan* plan;                                              // [rows]
+    Choice* choice;
+};
+
+namespace {
+
+template <typename Source, typename T>
+__device__ __forceinline__ Source chunk_of(const T* logits, const Settings& a, int64_t n, int chunk)
+{
+    Source row;
+    row.row = logits + n * a.stride;
+    row.first = chunk * a.chunk;
+    row.end = a.vocab - row.first < a.chunk ? a.vocab : row.first + a.chunk;
+    row.load();
+    return row;
+}
+
+// The row's extremes from its chunks'; entries beside an infinite maximum are counted anew.
+__device__ __forceinline__ void row_extremes(const Parts& x, const Settings& a, int64_t n, float& hi, float& lo, uint32_t& live)
+{
+    hi = -infinity();
+    lo = infinity();
+    live = 0;
+    for (int c = 0; c < a.chunks; ++c) {
+        hi = fmaxf(hi, x.hi[n * a.chunks + c]);
+        lo = fminf(lo, x.lo[n * a.chunks + c]);
+        live += x.live[n * a.chunks + c];
+    }
+}
+
+// A row's scanned histogram from its chunks'.
+template <int THREADS>
+__device__ __forceinline__ void sum_chunks(const Parts& x, const Settings& a, int64_t n, bool counted, Shared& s)
+{
+    constexpr int PER = kBuckets / THREADS;
+    const int64_t from = n * a.chunks * kBuckets;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int b = i * THREADS + threadIdx.x;
+        uint64_t m = 0;
+        uint32_t c = 0;
+#pragma unroll 8
+        for (int j = 0; j < a.chunks; ++j) {
+            m += x.mass[from + (int64_t)j * kBuckets + b];
+            if (counted)
+                c += x.count[from + (int64_t)j * kBuckets + b];
+        }
+        s.h.mass[b] = m;
+        s.h.count[b] = c;
+    }
+    scan<THREADS>(s.h, s);
+}
+
+}  // namespace
+
+template <typename T, typename Source>
+__global__ __launch_bounds__(Source::THREADS) void sample_max_kernel(const T* __restrict__ logits, Settings a, Parts x)
+{
+    __shared__ Shared s;
+    const int64_t n = blockIdx.x / a.chunks;
+    const int chunk = blockIdx.x % a.chunks;
+    const Source row = chunk_of<Source>(logits, a, n, chunk);
+    float hi, lo;
+    uint32_t live;
+    extremes(row, hi, lo, live);
+    reduce<Source::THREADS>(hi, lo, live, s);
+    if (threadIdx.x == 0) {
+        x.hi[blockIdx.x] = hi;
+        x.lo[blockIdx.x] = lo;
+        x.live[blockIdx.x] = live;
+    }
+}
+
+template <typename T, typename Source>
+__global__ __launch_bounds__(Source::THREADS) void sample_hist_kernel(const T* __restrict__ logits, Settings a, Parts x)
+{
+    constexpr int THREADS = Source::THREADS;
+    __shared__ Shared s;
+    const int64_t n = blockIdx.x / a.chunks;
+    Source row = chunk_of<Source>(logits, a, n, blockIdx.x % a.chunks);
+    const Wish w = wish_of(a, n);
+    float hi, lo;
+    uint32_t live;
+    row_extremes(x, a, n, hi, lo, live);
+    if (live == 0 || !(w.t > 0.f))
+        return;
+    start_table(s);
+    clear<THREADS>(s.h);
+    __syncthreads();
+    const Scale r = scale_of(hi, lo, w.t);
+    if (hi == infinity())
+        row.only_infinite();
+    fill(row, r, w.k > 0, s);
+    __syncthreads();
+    const int64_t to = (int64_t)blockIdx.x * kBuckets;
+    for (int b = threadIdx.x; b < kBuckets; b += THREADS) {
+        x.mass[to + b] = s.h.mass[b];
+        if (w.k > 0)
+            x.count[to + b] = s.h.count[b];
+    }
+}
+
+template <typename T, typename Source>
+__global__ __launch_bounds__(Source::THREADS) void sample_gather_kernel(const T* __restrict__ logits, Settings a, Parts x)
+{
+    constexpr int THREADS = Source::THREADS;
+    __shared__ Shared s;
+    const int64_t n = blockIdx.x / a.chunks;
+    const int chunk = blockIdx.x % a.chunks, tid = threadIdx.x;
+    Source row = chunk_of<Source>(logits, a, n, chunk);
+    const Wish w = wish_of(a, n);
+    float hi, lo;
+    uint32_t live;
+    row_extremes(x, a, n, hi, lo, live);
+    if (live == 0 || !(w.t > 0.f)) {                         // in place of a list: where the maximum is first
+        const int arg = live == 0 ? INT32_MAX : index_of(row, hi, s);
+        if (tid == 0)
+            x.number[blockIdx.x] = (uint32_t)arg;
+        return;
+    }
+    const Scale r = scale_of(hi, lo, w.t);
+    if (hi == infinity())
+        row.only_infinite();
+    sum_chunks<THREADS>(x, a, n, w.k > 0, s);
+    make_plan(s.h, r, w, s);
+    if (chunk == 0) {
+        const int64_t to = ((int64_t)gridDim.x + n) * kBuckets;
+        for (int b = tid; b < kBuckets; b += THREADS) {
+            x.mass[to + b] = s.h.mass[b];
+            x.count[to + b] = s.h.count[b];
+        }
+        if (tid == 0)
+            x.plan[n] = s.plan;
+    }
+    gather_plan(row, r, s);
+    if (tid == 0)
+        x.number[blockIdx.x] = s.number;
+    const int here = s.number < kList ? (int)s.number : kList;
+    for (int j = tid; j < here; j += THREADS)
+        x.list[(int64_t)blockIdx.x * kList + j] = s.x.list.order[j];
+}
+
+template <typename T>
+__global__ __launch_bounds__(1024) void sample_choose_kernel(const T* __restrict__ logits, Settings a, Parts x)
+{
+    constexpr int THREADS = 1024;
+    __shared__ Shared s;
+    const int64_t n = blockIdx.x, rows = gridDim.x;
+    const int tid = threadIdx.x;
+    const Wish w = wish_of(a, n);
+    float hi, lo;
+    uint32_t live;
+    row_extremes(x, a, n, hi, lo, live);
+    if (live == 0 || !(w.t > 0.f)) {
+        int arg = INT32_MAX;
+        for (int c = 0; c < a.chunks; ++c) {
+            const int i = (int)x.number[n * a.chunks + c];
+            arg = i < arg ? i : arg;
+        }
+        if (tid == 0) {
+            if (a.tokens)
+                a.tokens[n] = live == 0 ? -1 : arg;
+            x.choice[n].token = live == 0 ? -1 : arg;
+        }
+        return;
+    }
+    const Scale r = scale_of(hi, lo, w.t);
+    start_table(s);
+    const int64_t from = (rows * a.chunks + n) * kBuckets;
+    for (int b = tid; b < kBuckets; b += THREADS) {
+        s.h.mass[b] = x.mass[from + b];
+        s.h.count[b] = x.count[from + b];
+    }
+    uint32_t all = 0;                                        // chunks * vocab at most
+    for (int c = 0; c < a.chunks; ++c) {
+        const uint32_t here = x.number[n * a.chunks + c];
+        if (here <= kList && all + here <= kList && (uint32_t)tid >= all && (uint32_t)tid < all + here)
+            s.x.list.order[tid] = x.list[(n * a.chunks + c) * kList + tid - all];
+        all += here;
+    }
+    if (tid == 0) {
+        s.plan = x.plan[n];
+        s.number = all;
+    }
+    __syncthreads();
+    Streamed<T, THREADS> again = {logits + n * a.stride, 0, a.vocab, hi == infinity()};
+    choose(again, r, w, s);
+    if (tid == 0) {
+        if (a.tokens)
+            a.tokens[n] = s.choice.token;
+        x.choice[n] = s.choice;
+    }
+}
+
+template <typename T, typename Source>
+__global__ __launch_bounds__(Source::THREADS) void sample_probs_kernel(const T* __restrict__ logits, Settings a, Parts x)
+{
+    __shared__ Shared s;
+    const int64_t n = blockIdx.x / a.chunks;
+    Source row = chunk_of<Source>(logits, a, n, blockIdx.x % a.chunks);
+    const Wish w = wish_of(a, n);
+    float hi, lo;
+    uint32_t live;
+    row_extremes(x, a, n, hi, lo, live);
+    const Choice c = x.choice[n];
+    float* out = a.probs + n * a.vocab;
+    if (live == 0 || !(w.t > 0.f)) {
+        row.each([&](float, int i) {
+            if (i < a.vocab)
+                out[i] = i == c.token ? 1.f : 0.f;
+        });
+        return;
+    }
+    start_table(s);
+    __syncthreads();
+    const Scale r = scale_of(hi, lo, w.t);
+    if (hi == infinity())
+        row.only_infinite();
+    const double share = kOne / (double)c.total;
+    row.each([&](float l, int i) {
+        if (i < row.end)
+            out[i] = probability(r, s.table, c, share, l, i);
+    });
+}
+
+namespace {
+
+struct Cut {
+    int chunk, chunks;                                       // chunks 0: whole rows
+};
+// Rows are cut where one workgroup would have to read them again and again, and few of them would leave most compute
+// units idle; into chunks of 16,384 where that takes no second round of workgroups.  us, fp32, whole rows, chunks of
+// 16,384, of 32,768: 1 of 128,000 57, 22, 27; 64 of 128,000 83, 62, 50; 64 of 40,000 31 and 30; 16 of 33,000 23 and 25;
+// 128 of 128,000 90 and 100; 8 of 32,000, which fit the registers, 23 and 32.
+Cut cut_of(int64_t rows, int vocab)
+{
+    if (rows > 96 || vocab <= 40 * 1024)
+        return {0, 0};
+    constexpr int small = 1024 * 16, large = 1024 * 32;
+    const int few = (vocab + small - 1) / small;
+    if (rows * few <= 256)
+        return {small, few};
+    return {large, (vocab + large - 1) / large};
+}
+
+// The parts laid out one after the other, 256 bytes apart at least; returns the bytes.
+size_t lay_out(int64_t rows, const Cut& c, char* at, Parts& x)
+{
+    size_t used = 0;
+    auto take = [&](auto*& p, size_t count) {
+        p = (typename std::remove_reference<decltype(p)>::type)(at + used);
+        used += (count * sizeof(*p) + 255) / 256 * 256;
+    };
+    const size_t all = (size_t)rows * c.chunks;
+    take(x.hi, all);
+    take(x.lo, all);
+    take(x.live, all);
+    take(x.number, all);
+    take(x.mass, (all + rows) * kBuckets);
+    take(x.count, (all + rows) * kBuckets);
+    take(x.list, all * kList);
+    take(x.plan, rows);
+    take(x.choice, rows);
+    return used;
+}
+
+}  // namespace
+
 bool sample_fits(int64_t rows, int) { return rows <= UINT32_MAX / 1024; }
 
-size_t sample_workspace_bytes(int64_t, int) { return 0; }
+size_t sample_workspace_bytes(int64_t rows, int vocab)
+{
+    const Cut c = cut_of(rows, vocab);
+    Parts x;
+    return c.chunks ? lay_out(rows, c, nullptr, x) : 0;
+}
+
+static Settings settings_of(const SampleArgs& p, const Cut& c)
+{
+    return {p.stride, p.vocab, c.chunk, c.chunks, p.temperature, p.top_k, p.top_p, p.min_p, p.u, p.tokens, p.probs};
+}
 
 template <typename T, typename Source> static hipError_t launch_rows(const SampleArgs& p, hipStream_t stream)
 {
-    const Settings a = {p.stride, p.vocab, 0, 0, p.temperature, p.top_k, p.top_p, p.min_p, p.u, p.tokens, p.probs};
     hipLaunchKernelGGL((sample_row_kernel<T, Source>), dim3((unsigned)p.rows), dim3(Source::THREADS), 0, stream,
-                       (const T*)p.logits, a);
+                       (const T*)p.logits, settings_of(p, {}));
     return hipGetLastError();
+}
+
+template <typename T, typename Source> static hipError_t launch_chunks(const SampleArgs& p, const Cut& c, hipStream_t stream)
+{
+    const Settings a = settings_of(p, c);
+    Parts x;
+    lay_out(p.rows, c, (char*)p.ws, x);
+    const dim3 grid((unsigned)(p.rows * c.chunks)), block(Source::THREADS);
+    const T* l = (const T*)p.logits;
+    hipError_t e = hipSuccess;
+    auto next = [&](auto kernel, dim3 g, dim3 b) {
+        if (e == hipSuccess) {
+            hipLaunchKernelGGL(kernel, g, b, 0, stream, l, a, x);
+            e = hipGetLastError();
+        }
+    };
+    next(sample_max_kernel<T, Source>, grid, block);
+    next(sample_hist_kernel<T, Source>, grid, block);
+    next(sample_gather_kernel<T, Source>, grid, block);
+    next(sample_choose_kernel<T>, dim3((unsigned)p.rows), dim3(1024));
+    if (p.probs)
+        next(sample_probs_kernel<T, Source>, grid, block);
+    return e;
 }
 
 template <typename T> static hipError_t launch_T(const SampleArgs& p, hipStream_t stream)
 {
     if (p.rows == 0)
         return hipSuccess;
+    const Cut c = cut_of(p.rows, p.vocab);
+    if (c.chunks > 0) {
+        if (c.chunk == 1024 * 16) return launch_chunks<T, Held<T, 1024, 16>>(p, c, stream);
+        return launch_chunks<T, Held<T, 1024, 32>>(p, c, stream);
+    }
     if (p.vocab <= 256 * 8) return launch_rows<T, Held<T, 256, 8>>(p, stream);
     if (p.vocab <= 256 * 32) return launch_rows<T, Held<T, 256, 32>>(p, stream);
     if (p.vocab <= 1024 * 16) return launch_rows<T, Held<T, 1024, 16>>(p, stream);

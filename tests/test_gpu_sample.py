@@ -243,3 +243,33 @@ def test_the_largest_vocabulary():
     u = np.array([0.3, 0.97], dtype=np.float32)
     for f in ({}, {"p": np.full(2, 0.95, np.float32)}, {"k": np.full(2, 500000, np.int32)}):
         check(logits, u, f)
+
+
+@pytest.mark.parametrize("V", [41000, 50001, 98304, 131073])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_that_are_cut_and_whole_ones(dtype, V):
+    """Batches that are worked on in chunks of either size, and as whole rows, choose alike to the bit, from a
+    workspace that holds anything; parts of rows are masked away."""
+    import torch
+    from gated_delta_rule_prologue_amd import binding as B
+    gen = torch.Generator().manual_seed(V)
+    N = 110
+    logits = (2 * torch.randn(N, V, generator=gen)).to({"bf16": torch.bfloat16, "f32": torch.float32}[dtype]).cuda()
+    logits[1, : V // 2] = float("-inf")
+    logits[2, V // 3:] = float("nan")
+    logits[3] = float("-inf")
+    logits[4, 1:] = float("-inf")
+    logits[5, [V // 2, V - 1]] = float("inf")
+    u = np.random.default_rng(V).random(N).astype(np.float32)
+    f = settings(N, V)
+    tokens, pr = check(logits, u, f, rows=range(0, N, 9))
+    for rows in (90, 12):
+        d = B.SampleDims(rows, V, B._dtype_code(logits), V)
+        ws = torch.full((B.sample_workspace_bytes(d),), 0xFF, dtype=torch.uint8, device="cuda")
+        assert ws.numel() > 0
+        for from_ in (0, N - rows):
+            at = slice(from_, from_ + rows)
+            some, some_pr = run(logits[at], u[at], want_probs=True, workspace=ws, **{n: v[at] for n, v in f.items()})
+            assert (some == tokens[at]).all() and (some_pr == pr[at]).all()
+            some, _ = run(logits[at], u[at], workspace=ws, **{n: v[at] for n, v in f.items()})
+            assert (some == tokens[at]).all()

@@ -198,6 +198,19 @@ def test_sample_refuses(B):
                 assert sam(B, **{out: at[other]}) == B.PRISM_EINVAL, (out, other)
 
 
+def test_sample_workspace(B):
+    need = lambda *a: B.sample_workspace_bytes(B.SampleDims(*a))
+    assert need(0, 200000, 0, 0) == 0 and need(1, 40960, 0, 0) == 0 and need(200, 200000, 0, 0) == 0
+    assert need(1, 131072, 0, 0) > 8 * 1024 * 20 and need(64, 131072, 0, 0) > 64 * 4 * 1024 * 20
+    d = B.SampleDims(4, 131072, 0, 131072)
+    at = dict(zip(SAM, far(9)))
+    n = need(4, 131072, 0, 131072)
+    assert sam(B, d, nb=n - 1) == sam(B, d, ws=None) == sam(B, d, ws=FAKE + 8) == B.PRISM_EINVAL
+    for other in SAM[:-1]:
+        assert sam(B, d, ws=at[other]) == B.PRISM_EINVAL, other
+    assert sam(B, d, ws=at["probs"] - n + 256) == B.PRISM_EINVAL
+
+
 def test_binding_refuses_before_calling(B):
     bf = torch.bfloat16
     x, w, cu = torch.zeros(8, 16, dtype=bf), torch.zeros(16, 4, dtype=bf), torch.tensor([0, 8], dtype=torch.int32)
