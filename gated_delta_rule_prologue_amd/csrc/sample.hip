@@ -235,9 +235,13 @@ template <typename T, int THREADS_> struct Streamed {
                 f(l, at + 4 * j);
             }
         }
-        if (whole + (int)threadIdx.x < end) {
-            const float l[4] = {entry(to_f32(row[whole + threadIdx.x]), infinite), -infinity(), -infinity(), -infinity()};
-            f(l, whole + threadIdx.x);
+        const int at = whole + 4 * (int)threadIdx.x;
+        if (at < end) {
+            float l[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                l[i] = at + i < end ? entry(to_f32(row[at + i]), infinite) : -infinity();
+            f(l, at);
         }
     }
 };
@@ -1034,6 +1038,27 @@ __device__ __forceinline__ float probability(const Scale& r, const double* table
     return live_entry(l) && order_of(l, i) <= c.cut ? (float)(weight_of(r, table, l) * share) : 0.f;
 }
 
+// The distribution that is left of the entries.
+template <typename Source>
+__device__ __forceinline__ void put_probs(const Source& row, const Scale& r, const Shared& s, const Choice& c, float* out)
+{
+    const double share = kOne / (double)c.total;
+    row.each4([&](const float(&l)[4], int i) {
+        rows::AtElement a;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            a[e] = __float_as_uint(probability(r, s.table, c, share, l[e], i + e));
+        if (i + 4 <= row.end) {
+            *reinterpret_cast<rows::AtElement*>(out + i) = a;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e < row.end)
+                    out[i + e] = __uint_as_float(a[e]);
+        }
+    });
+}
+
 }  // namespace
 
 // A row of logits by one workgroup.
@@ -1083,13 +1108,8 @@ __global__ __launch_bounds__(Source::THREADS) void sample_row_kernel(const T* __
     const Choice c = s.choice;
     if (a.tokens && tid == 0)
         a.tokens[n] = c.token;
-    if (out) {
-        const double share = kOne / (double)c.total;
-        row.each([&](float l, int i) {
-            if (i < vocab)
-                out[i] = probability(r, s.table, c, share, l, i);
-        });
-    }
+    if (out)                                                 // read again, so that no registers are held for it
+        put_probs(again, r, s, c, out);
 }
 
 // ---- rows cut into chunks
@@ -1319,11 +1339,7 @@ __global__ __launch_bounds__(Source::THREADS) void sample_probs_kernel(const T* 
     const Scale r = scale_of(hi, lo, w.t);
     if (hi == infinity())
         row.only_infinite();
-    const double share = kOne / (double)c.total;
-    row.each([&](float l, int i) {
-        if (i < row.end)
-            out[i] = probability(r, s.table, c, share, l, i);
-    });
+    put_probs(row, r, s, c, out);
 }
 
 namespace {
