@@ -428,8 +428,8 @@ __device__ __forceinline__ float lane_max(float x)
     return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), 63));
 }
 
-// The largest and smallest entry, and the number of them (the wavefront's comes in), over the workgroup.
-template <int THREADS> __device__ __forceinline__ void reduce(float& hi, float& lo, uint32_t& live, Shared& s)
+// The largest and smallest entry, over the workgroup.
+template <int THREADS> __device__ __forceinline__ void reduce(float& hi, float& lo, Shared& s)
 {
     constexpr int WAVES = THREADS / 64;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -438,29 +438,36 @@ template <int THREADS> __device__ __forceinline__ void reduce(float& hi, float& 
     if (lane == 0) {
         s.wave_max[wave] = hi;
         s.wave_min[wave] = lo;
-        s.wave_count[wave] = live;
     }
     __syncthreads();
-    live = 0;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) {
         hi = fmaxf(hi, s.wave_max[w]);
         lo = fminf(lo, s.wave_min[w]);
-        live += s.wave_count[w];
     }
     __syncthreads();
 }
 
-template <typename Source> __device__ __forceinline__ void extremes(const Source& row, float& hi, float& lo, uint32_t& live)
+// An instruction each: the compiler would first make quiet the NaN that entries are not.
+__device__ __forceinline__ float larger(float a, float b)
+{
+    asm("v_max_f32 %0, %1, %0" : "+v"(a) : "v"(b));
+    return a;
+}
+__device__ __forceinline__ float smaller(float a, float b)
+{
+    asm("v_min_f32 %0, %1, %0" : "+v"(a) : "v"(b));
+    return a;
+}
+
+// The largest entry (-infinity: there is none) and the smallest that counts.
+template <typename Source> __device__ __forceinline__ void extremes(const Source& row, float& hi, float& lo)
 {
     hi = -infinity();
     lo = infinity();
-    live = 0;
     row.each([&](float l, int) {
-        const bool there = live_entry(l);
-        hi = fmaxf(hi, l);
-        lo = fminf(lo, there ? l : infinity());
-        live += (uint32_t)__popcll(__ballot(there));         // of the wavefront
+        hi = larger(hi, l);
+        lo = smaller(lo, live_entry(l) ? l : infinity());
     });
 }
 
@@ -1077,13 +1084,12 @@ __global__ __launch_bounds__(Source::THREADS) void sample_row_kernel(const T* __
     row.load();
     float* out = a.probs ? a.probs + n * vocab : nullptr;
     float hi, lo;
-    uint32_t live;
-    extremes(row, hi, lo, live);
+    extremes(row, hi, lo);
     start_table(s);
     clear<THREADS>(s.h);
-    reduce<THREADS>(hi, lo, live, s);
-    if (live == 0 || !(w.t > 0.f)) {                         // nothing to draw from, or the largest is taken
-        const int arg = live == 0 ? -1 : index_of(row, hi, s);
+    reduce<THREADS>(hi, lo, s);
+    if (!live_entry(hi) || !(w.t > 0.f)) {                         // nothing to draw from, or the largest is taken
+        const int arg = !live_entry(hi) ? -1 : index_of(row, hi, s);
         if (a.tokens && tid == 0)
             a.tokens[n] = arg;
         if (out)
@@ -1096,9 +1102,6 @@ __global__ __launch_bounds__(Source::THREADS) void sample_row_kernel(const T* __
     if (hi == infinity()) {                                  // nothing else counts
         row.only_infinite();
         again.only_infinite();
-        float h2, l2;
-        extremes(row, h2, l2, live);
-        reduce<THREADS>(h2, l2, live, s);
     }
     fill(row, r, w.k > 0, s);
     scan<THREADS>(s.h, s);
@@ -1117,7 +1120,7 @@ __global__ __launch_bounds__(Source::THREADS) void sample_row_kernel(const T* __
 // What is left of a row between the launches.
 struct Parts {
     float *hi, *lo;                                          // [rows][chunks]
-    uint32_t *live, *number;                                 // [rows][chunks]; number: entries in the chunk's list
+    uint32_t* number;                                        // [rows][chunks]: entries in the chunk's list
     uint64_t* mass;                                          // [rows][chunks][kBuckets], then of the row [rows][kBuckets]
     uint32_t* count;
     uint64_t* list;                                          // [rows][chunks][kList]
@@ -1138,16 +1141,14 @@ __device__ __forceinline__ Source chunk_of(const T* logits, const Settings& a, i
     return row;
 }
 
-// The row's extremes from its chunks'; entries beside an infinite maximum are counted anew.
-__device__ __forceinline__ void row_extremes(const Parts& x, const Settings& a, int64_t n, float& hi, float& lo, uint32_t& live)
+// The row's extremes from its chunks'.
+__device__ __forceinline__ void row_extremes(const Parts& x, const Settings& a, int64_t n, float& hi, float& lo)
 {
     hi = -infinity();
     lo = infinity();
-    live = 0;
     for (int c = 0; c < a.chunks; ++c) {
         hi = fmaxf(hi, x.hi[n * a.chunks + c]);
         lo = fminf(lo, x.lo[n * a.chunks + c]);
-        live += x.live[n * a.chunks + c];
     }
 }
 
@@ -1184,13 +1185,11 @@ __global__ __launch_bounds__(Source::THREADS) void sample_max_kernel(const T* __
     const int chunk = blockIdx.x % a.chunks;
     const Source row = chunk_of<Source>(logits, a, n, chunk);
     float hi, lo;
-    uint32_t live;
-    extremes(row, hi, lo, live);
-    reduce<Source::THREADS>(hi, lo, live, s);
+    extremes(row, hi, lo);
+    reduce<Source::THREADS>(hi, lo, s);
     if (threadIdx.x == 0) {
         x.hi[blockIdx.x] = hi;
         x.lo[blockIdx.x] = lo;
-        x.live[blockIdx.x] = live;
     }
 }
 
@@ -1203,9 +1202,8 @@ __global__ __launch_bounds__(Source::THREADS) void sample_hist_kernel(const T* _
     Source row = chunk_of<Source>(logits, a, n, blockIdx.x % a.chunks);
     const Wish w = wish_of(a, n);
     float hi, lo;
-    uint32_t live;
-    row_extremes(x, a, n, hi, lo, live);
-    if (live == 0 || !(w.t > 0.f))
+    row_extremes(x, a, n, hi, lo);
+    if (!live_entry(hi) || !(w.t > 0.f))
         return;
     start_table(s);
     clear<THREADS>(s.h);
@@ -1233,10 +1231,9 @@ __global__ __launch_bounds__(Source::THREADS) void sample_gather_kernel(const T*
     Source row = chunk_of<Source>(logits, a, n, chunk);
     const Wish w = wish_of(a, n);
     float hi, lo;
-    uint32_t live;
-    row_extremes(x, a, n, hi, lo, live);
-    if (live == 0 || !(w.t > 0.f)) {                         // in place of a list: where the maximum is first
-        const int arg = live == 0 ? INT32_MAX : index_of(row, hi, s);
+    row_extremes(x, a, n, hi, lo);
+    if (!live_entry(hi) || !(w.t > 0.f)) {                         // in place of a list: where the maximum is first
+        const int arg = !live_entry(hi) ? INT32_MAX : index_of(row, hi, s);
         if (tid == 0)
             x.number[blockIdx.x] = (uint32_t)arg;
         return;
@@ -1272,9 +1269,8 @@ __global__ __launch_bounds__(1024) void sample_choose_kernel(const T* __restrict
     const int tid = threadIdx.x;
     const Wish w = wish_of(a, n);
     float hi, lo;
-    uint32_t live;
-    row_extremes(x, a, n, hi, lo, live);
-    if (live == 0 || !(w.t > 0.f)) {
+    row_extremes(x, a, n, hi, lo);
+    if (!live_entry(hi) || !(w.t > 0.f)) {
         int arg = INT32_MAX;
         for (int c = 0; c < a.chunks; ++c) {
             const int i = (int)x.number[n * a.chunks + c];
@@ -1282,8 +1278,8 @@ __global__ __launch_bounds__(1024) void sample_choose_kernel(const T* __restrict
         }
         if (tid == 0) {
             if (a.tokens)
-                a.tokens[n] = live == 0 ? -1 : arg;
-            x.choice[n].token = live == 0 ? -1 : arg;
+                a.tokens[n] = !live_entry(hi) ? -1 : arg;
+            x.choice[n].token = !live_entry(hi) ? -1 : arg;
         }
         return;
     }
@@ -1323,11 +1319,10 @@ __global__ __launch_bounds__(Source::THREADS) void sample_probs_kernel(const T* 
     Source row = chunk_of<Source>(logits, a, n, blockIdx.x % a.chunks);
     const Wish w = wish_of(a, n);
     float hi, lo;
-    uint32_t live;
-    row_extremes(x, a, n, hi, lo, live);
+    row_extremes(x, a, n, hi, lo);
     const Choice c = x.choice[n];
     float* out = a.probs + n * a.vocab;
-    if (live == 0 || !(w.t > 0.f)) {
+    if (!live_entry(hi) || !(w.t > 0.f)) {
         row.each([&](float, int i) {
             if (i < a.vocab)
                 out[i] = i == c.token ? 1.f : 0.f;
@@ -1373,7 +1368,6 @@ size_t lay_out(int64_t rows, const Cut& c, char* at, Parts& x)
     const size_t all = (size_t)rows * c.chunks;
     take(x.hi, all);
     take(x.lo, all);
-    take(x.live, all);
     take(x.number, all);
     take(x.mass, (all + rows) * kBuckets);
     take(x.count, (all + rows) * kBuckets);
