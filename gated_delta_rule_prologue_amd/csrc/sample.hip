@@ -21,11 +21,11 @@
 // collection, lookup: some 4 us each), by the arithmetic of the weights (some 35 instructions an
 // entry, half of them 64-bit) and the 64-bit LDS additions where there are many; reading the
 // logits is a tenth of it.  A row of up to 32,768 entries stays in the registers of one workgroup
-// for all passes, so they are one launch: 1 row of 32,000 20 us, 64 25 us, 256 in bf16 28 us.
+// for all passes, so they are one launch: 1 row of 32,000 19 us, 64 23 us, 256 in bf16 27 us.
 // Longer rows are read again by each pass, and while they are few they are cut into chunks, one
 // workgroup each, with a launch for the maximum, the histograms, the collection and the choice
-// (and one for the distribution): 64 rows of 128,000 50 us, of which 7, 12, 16 and 12 are the
-// launches; 256 rows, whole, 103 us.
+// (and one for the distribution): 64 rows of 128,000 50 us, of which 7, 13, 15 and 13 are
+// the launches; 256 rows, whole, 92 us.
 #include <type_traits>
 
 #include "common.h"
@@ -190,18 +190,42 @@ __device__ __forceinline__ float entry(float l, bool infinite)
 // any element's address.
 template <typename T, int THREADS_> struct Streamed {
     static constexpr int THREADS = THREADS_;
+    // vectors in flight (256 rows of 128,000 fp32: one 95 us, two 92, four 94; in bf16, of 65,536: one 47, four 49)
+    static constexpr int AHEAD = sizeof(T) == 2 ? 1 : 2;
     const T* row;
     int first, end;
     bool infinite;                                           // entries of +infinity are all that counts
     __device__ __forceinline__ void load() { infinite = false; }
     __device__ __forceinline__ void only_infinite() { infinite = true; }
+    // f(vector, index of its first element) for every whole vector, AHEAD of them on their way to a lane
+    template <typename F> __device__ __forceinline__ void vectors(int whole, F f) const
+    {
+        constexpr int VE = Vec16<T>::N, STEP = THREADS * VE;
+        auto load = [&](int at) {                            // behind the last one that again
+            return *reinterpret_cast<const rows::AtElement*>(row + (at < whole ? at : whole - VE));
+        };
+        int at = first + threadIdx.x * VE;
+        if (at >= whole)
+            return;
+        rows::AtElement a[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+            a[u] = load(at + u * STEP);
+        for (; at < whole; at += AHEAD * STEP)
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                const rows::AtElement x = a[u];
+                a[u] = load(at + (u + AHEAD) * STEP);
+                if (at + u * STEP < whole)
+                    f(x, at + u * STEP);
+            }
+    }
     // f(entry, index) for every element, spread over the workgroup
     template <typename F> __device__ __forceinline__ void each(F f) const
     {
         constexpr int VE = Vec16<T>::N;
         const int whole = first + (end - first) / VE * VE;
-        for (int at = first + threadIdx.x * VE; at < whole; at += THREADS * VE) {
-            const rows::AtElement a = *reinterpret_cast<const rows::AtElement*>(row + at);
+        vectors(whole, [&](const rows::AtElement& a, int at) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if constexpr (sizeof(T) == 2) {
@@ -211,7 +235,7 @@ template <typename T, int THREADS_> struct Streamed {
                     f(entry(__uint_as_float(a[i]), infinite), at + i);
                 }
             }
-        }
+        });
         if (whole + (int)threadIdx.x < end)
             f(entry(to_f32(row[whole + threadIdx.x]), infinite), whole + threadIdx.x);
     }
@@ -220,8 +244,7 @@ template <typename T, int THREADS_> struct Streamed {
     {
         constexpr int VE = Vec16<T>::N;
         const int whole = first + (end - first) / VE * VE;
-        for (int at = first + threadIdx.x * VE; at < whole; at += THREADS * VE) {
-            const rows::AtElement a = *reinterpret_cast<const rows::AtElement*>(row + at);
+        vectors(whole, [&](const rows::AtElement& a, int at) {
 #pragma unroll
             for (int j = 0; j < VE / 4; ++j) {
                 float l[4];
@@ -234,7 +257,7 @@ template <typename T, int THREADS_> struct Streamed {
                 }
                 f(l, at + 4 * j);
             }
-        }
+        });
         const int at = whole + 4 * (int)threadIdx.x;
         if (at < end) {
             float l[4];
@@ -1344,11 +1367,11 @@ struct Cut {
 };
 // Rows are cut where one workgroup would have to read them again and again, and few of them would leave most compute
 // units idle; into chunks of 16,384 where that takes no second round of workgroups.  us, fp32, whole rows, chunks of
-// 16,384, of 32,768: 1 of 128,000 57, 22, 27; 64 of 128,000 83, 62, 50; 64 of 40,000 31 and 30; 16 of 33,000 23 and 25;
-// 128 of 128,000 90 and 100; 8 of 32,000, which fit the registers, 23 and 32.
+// 16,384, of 32,768: 1 of 128,000 56, 22, 27; 64 of 128,000 76, 62, 49; 64 of 50,001 38 and 35, 96 of them 38 and 41;
+// 128 of 128,000 79 and 100; 16 of 33,000 22 and 25; 8 of 32,000, which fit the registers, 22 and 32.
 Cut cut_of(int64_t rows, int vocab)
 {
-    if (rows > 96 || vocab <= 40 * 1024)
+    if (rows > 80 || vocab <= 40 * 1024)
         return {0, 0};
     constexpr int small = 1024 * 16, large = 1024 * 32;
     const int few = (vocab + small - 1) / small;
