@@ -312,7 +312,7 @@ struct SampleArgs {
     void* ws;
 };
 
-bool sample_fits(int64_t rows, int vocab);
+bool sample_fits(int64_t rows);
 size_t sample_workspace_bytes(int64_t rows, int vocab);
 hipError_t launch_sample(const SampleArgs& p, hipStream_t stream);
 

@@ -578,7 +578,7 @@ template <typename T> hipError_t fwd(const QkNormArgs& p, hipStream_t stream)
         typedef typename decltype(tag)::type S;
         const Side<T> q = side_of<S>(p, 0, false), k = side_of<S>(p, 1, false);
         // few tokens: k's rows on other compute units rather than behind q's (LM layer 28.8 us with its angles formed twice)
-        const bool both = k.heads > 0 && p.tokens >= 2048;
+        const bool both = k.heads > 0 && p.tokens >= 2048 && (int64_t)q.tile * k.heads <= 1 << 17;         // place()
         const int tile = both || q.tile > k.tile ? q.tile : k.tile;
         hipLaunchKernelGGL((qk_norm_kernel<S>), dim3((unsigned)q.blocks + (both ? 0 : k.blocks)), dim3(kThreads),
                            (size_t)tile * (p.rot / 2) * sizeof(float2), stream, row_args(p), q, k, both);

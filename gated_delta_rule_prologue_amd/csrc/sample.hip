@@ -1402,7 +1402,7 @@ size_t lay_out(int64_t rows, const Cut& c, char* at, Parts& x)
 
 }  // namespace
 
-bool sample_fits(int64_t rows, int) { return rows <= UINT32_MAX / 1024; }
+bool sample_fits(int64_t rows) { return rows <= UINT32_MAX / 1024; }
 
 size_t sample_workspace_bytes(int64_t rows, int vocab)
 {

@@ -302,7 +302,7 @@ prism_status prism_sample(const prism_sample_dims* d, const void* logits, const 
         return PRISM_EINVAL;
     if (d->rows > 0 && (!elem_ok(logits, d->dtype) || (!tokens && !probs) || (tokens && !u)))
         return PRISM_EINVAL;
-    if (d->vocab > PRISM_MAX_SAMPLE_VOCAB || !prism::sample_fits(d->rows, d->vocab))
+    if (d->vocab > PRISM_MAX_SAMPLE_VOCAB || !prism::sample_fits(d->rows))
         return PRISM_EUNSUPPORTED;
     const size_t need = prism_sample_workspace_bytes(d);
     if (need > 0 ? !ptr_ok(workspace) || workspace_bytes < need : !opt_ok(workspace))

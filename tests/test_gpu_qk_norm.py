@@ -233,3 +233,32 @@ def test_no_tokens():
     assert q.shape == (0, 2, 64) and k.shape == (0, 1, 64)
     g = B.qk_norm_bwd(d["q"], d["dq"], d["k"], d["dk"], **how)
     assert (g["wq"] == 0).all() and (g["wk"] == 0).all()
+
+
+def test_one_query_head_beside_thousands_of_keys():
+    assert check_all(make(2050, 1, 4099, 8, 8, seed=13), "rms", "half") <= 1
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements of q, and rows that lie as far apart: the last tokens' values are those that they have
+    alone."""
+    import torch
+    from gated_delta_rule_prologue_amd import binding as B
+    T, H, d, last = 2_100_000, 8, 128, 37
+    assert T * H * d > 2 ** 31
+    gen = torch.Generator().manual_seed(14)
+    rows = torch.zeros(T, H + 1, d, dtype=torch.bfloat16, device="cuda")
+    rows[-last:] = torch.randn(last, H + 1, d, generator=gen).to(rows)
+    dq, dk = torch.zeros(T, H, d).to(rows), torch.zeros(T, 1, d).to(rows)
+    dq[-last:], dk[-last:] = torch.randn(last, H, d, generator=gen).to(rows), torch.randn(last, 1, d, generator=gen).to(rows)
+    how = dict(norm="rms", freqs=B.rotary_freqs(64))
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    tail = slice(T - last, T)
+    own = pos[tail].clone()                                  # int32 arrays begin at 16 bytes
+    q, k = B.qk_norm(rows[:, :H], rows[:, H:], positions=pos, **how)
+    q1, k1 = B.qk_norm(rows[tail, :H], rows[tail, H:], positions=own, **how)
+    assert torch.equal(q[tail], q1) and torch.equal(k[tail], k1)
+    del q, k
+    g = B.qk_norm_bwd(rows[:, :H], dq, rows[:, H:], dk, positions=pos, **how)
+    g1 = B.qk_norm_bwd(rows[tail, :H], dq[tail], rows[tail, H:], dk[tail], positions=own, **how)
+    assert torch.equal(g["q"][tail], g1["q"]) and torch.equal(g["k"][tail], g1["k"])

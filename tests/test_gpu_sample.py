@@ -273,3 +273,52 @@ def test_rows_that_are_cut_and_whole_ones(dtype, V):
             assert (some == tokens[at]).all() and (some_pr == pr[at]).all()
             some, _ = run(logits[at], u[at], workspace=ws, **{n: v[at] for n, v in f.items()})
             assert (some == tokens[at]).all()
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 logits: the last rows choose as they do alone."""
+    import torch
+    from gated_delta_rule_prologue_amd import binding as B
+    N, V = 22_000, 100_003
+    assert N * V > 2 ** 31
+    logits = torch.zeros(N, V, dtype=torch.bfloat16, device="cuda")
+    logits[-9:] = (3 * torch.randn(9, V, generator=torch.Generator().manual_seed(15))).to(logits)
+    u = torch.rand(N, generator=torch.Generator().manual_seed(16)).cuda()
+    p = torch.full((N,), 0.9, device="cuda")
+    tokens, _ = B.sample(logits, u, top_p=p)
+    alone, probs = B.sample(logits[-9:], u[-9:].clone(), top_p=p[-9:].clone(), want_probs=True)
+    assert torch.equal(tokens[-9:], alone)
+    assert (probs.gather(1, alone[:, None].long()) > 0).all()
+    # rows of equal logits: the kept ones are the first 0.9 V
+    assert (tokens[:-9] == (u[:-9].double() * np.ceil(np.float64(np.float32(0.9)) * V)).floor().int()).all()
+
+
+@pytest.mark.parametrize("N,V", [(3, 60_000), (70, 60_000), (100, 60_000), (3, 1000)])
+def test_captured_and_beside_each_other(N, V):
+    """Two graphs over the same inputs, replayed on two streams at once between eager calls on new inputs."""
+    import torch
+    from gated_delta_rule_prologue_amd import binding as B
+    gen = torch.Generator().manual_seed(N)
+    new = lambda: (2 * torch.randn(N, V, generator=gen)).cuda()
+    logits, u = new(), torch.rand(N, generator=gen).cuda()
+    k, p = torch.full((N,), 400, dtype=torch.int32).cuda(), torch.full((N,), 0.95).cuda()
+    B.sample(logits, u, None, k, p, want_probs=True)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    graphs = []
+    for s in streams:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            out = B.sample(logits, u, None, k, p, want_probs=True)
+        graphs.append((g, out))
+    for _ in range(4):
+        logits.copy_(new())
+        u.copy_(torch.rand(N, generator=gen))
+        want = B.sample(logits, u, None, k, p, want_probs=True)
+        torch.cuda.synchronize()
+        for s, (g, _) in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for _, out in graphs:
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])

@@ -104,7 +104,7 @@ def test_channels(dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_many_runs(dtype):
-    """More runs than the backward has groups: every lane takes several, and weight gradients of many
+    """Long runs in the backward, several rounds of workgroups in the forward, and weight gradients of many
     tokens.  The reference by shifted sums of one sequence."""
     import torch
     from gated_delta_rule_prologue_amd import binding as B
@@ -127,7 +127,7 @@ def test_many_runs(dtype):
     pad = lambda v: torch.cat([v, torch.zeros(K - 1, x.shape[1]).double()])
     check("dx", g["x"][:, cols], sum(w[:, m] * dsp[K - 1 - m:K - 1 - m + T] for m in range(K)),
           sum(w[:, m].abs() * pad(eds + (K + 1) * dsa)[K - 1 - m:K - 1 - m + T] for m in range(K)), 1)
-    # a lane adds its runs of 64 tokens: T / (workgroups along the tokens) / groups, at most 300 here
+    # a lane adds its run of tokens, then come the lanes of a workgroup and the workgroups: at most 300 here
     adds = 300 + 64
     dw = torch.stack([(ds * xp[m:m + T]).sum(0) for m in range(K)], 1)
     ew = torch.stack([((eds + adds * dsa) * xp[m:m + T].abs()).sum(0) for m in range(K)], 1)
@@ -298,3 +298,31 @@ def test_no_tokens():
     assert y.shape == (0, 16) and torch.equal(ho, d["hist"])
     g = B.short_conv_bwd(d["x"], d["w"], d["cu_t"], d["dy"], bias=d["bias"], hist=d["hist"])
     assert all((g[n] == 0).all() for n in ("w", "bias", "hist"))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last sequence's values are those that it has alone."""
+    import torch
+    from gated_delta_rule_prologue_amd import binding as B
+    C, T, last = 4096, 530_000, 301
+    assert C * T > 2 ** 31
+    gen = torch.Generator().manual_seed(12)
+    x = torch.zeros(T, C, dtype=torch.bfloat16, device="cuda")
+    dy = torch.zeros_like(x)
+    x[-last - 2:] = torch.randn(last + 2, C, generator=gen).to(x)
+    dy[-last:] = torch.randn(last, C, generator=gen).to(x)
+    w, bias = torch.randn(C, 4, generator=gen).to(x), torch.randn(C, generator=gen).to(x)
+    hist = torch.randn(2, 3, C, generator=gen).to(x)
+    cu = torch.tensor([0, T - last, T], dtype=torch.int32).cuda()
+    alone = torch.tensor([0, last], dtype=torch.int32).cuda()
+    ho, ho1 = torch.empty_like(hist), torch.empty_like(hist[1:])
+    y, _ = B.short_conv(x, w, cu, bias=bias, hist=hist, hist_out=ho)
+    y1, _ = B.short_conv(x[-last:], w, alone, bias=bias, hist=hist[1:], hist_out=ho1)
+    assert torch.equal(y[-last:], y1) and torch.equal(ho[1:], ho1) and torch.equal(ho[0, 1:], x[-last - 2:-last])
+    del y
+    g = B.short_conv_bwd(x, w, cu, dy, bias=bias, hist=hist)
+    g1 = B.short_conv_bwd(x[-last:], w, alone, dy[-last:], bias=bias, hist=hist[1:])
+    assert torch.equal(g["x"][-last:], g1["x"]) and torch.equal(g["hist"][1:], g1["hist"])
+    # sums of the same 301 terms beside zeros, in two orders: 301 roundings of their magnitudes each
+    size = (dy[-last:].float().abs() * 1.1).sum(0)
+    assert ((g["bias"] - g1["bias"]).abs() <= 2 * 301 * 2.0 ** -24 * size).all()
