@@ -56,9 +56,9 @@ struct Hist {
 
 // What a row is measured by.
 struct Scale {
-    float max, min, floor;                                   // floor: a weight of 2^-45
+    float max, min;
     float step, far_step, far_from;                          // buckets per unit of l, near and far, where they meet
-    double c, top;                                           // 32 log2 e / temperature; max
+    double c, top, least;                                    // 32 log2 e / temperature; max; l - max of a weight of 2^-45
 };
 
 // What is asked of a row.
@@ -70,12 +70,13 @@ struct Wish {
 };
 
 // What a row's histogram says of it: which filters cut it (min_p's place, or kNowhere), and the ranges of buckets in
-// which the places lie, as bounds on (max - l) * step.
+// which the places lie, as bounds on height_of.
 struct Plan {
     uint64_t m_order;
     int k, p, m;                                             // k, p: whether they are in force; m: its bucket, or -1
     int ranges;
     float from[4], to[4];
+    float high[4], low[4];                                   // logits between which all of a range lie, and little else
 };
 
 struct Choice {
@@ -139,11 +140,11 @@ struct Constants {
     }
 };
 
-// exp((l - max) / temperature): 2^(n / 32) from the table, and the rest of the exponent, at most
+// exp(d / temperature): 2^(n / 32) from the table, and the rest of the exponent, at most
 // ln 2 / 64, by its series to the fourth power (10^-12).
-__device__ __forceinline__ double series_of(const Constants& k, const Scale& r, float l, int& n)
+__device__ __forceinline__ double series_of(const Constants& k, const Scale& r, double d, int& n)
 {
-    const double d = (double)l - r.top, m = __builtin_fma(d, r.c, k.whole);
+    const double m = __builtin_fma(d, r.c, k.whole);
     const double t = __builtin_fma(d, r.c, -(m - k.whole));
     double s = __builtin_fma(t, k.c4, k.c3);
     s = __builtin_fma(s, t, k.c2);
@@ -151,27 +152,29 @@ __device__ __forceinline__ double series_of(const Constants& k, const Scale& r, 
     n = (int)__double_as_longlong(m);
     return __builtin_fma(s, t, k.one);
 }
-// In steps of 2^-43; entries below `floor` have less than half a step.
+__device__ __forceinline__ double power_of(const double* table, int n, int add)
+{
+    const double t = table[n & 31];
+    return __hiloint2double(__double2hiint(t) + (((n >> 5) + add) << 20), __double2loint(t));
+}
+// In steps of 2^-43: what is below the scale's least has a quarter of one.
 __device__ __forceinline__ uint64_t steps_of(const Constants& k, const Scale& r, const double* table, float l)
 {
     int n;
-    const double s = series_of(k, r, fmaxf(l, r.floor), n), t = table[n & 31];
-    const double e = __hiloint2double(__double2hiint(t) + (((n >> 5) + 43) << 20), __double2loint(t));
-    const double w = __builtin_fma(e, s, k.steps);
-    const bool some = l >= r.floor;
-    return (uint64_t)(uint32_t)(some ? __double2hiint(w) & 0xfffff : 0) << 32 | (uint32_t)(some ? __double2loint(w) : 0);
+    const double s = series_of(k, r, fmax((double)l - r.top, r.least), n);
+    const double w = __builtin_fma(power_of(table, n, 43), s, k.steps);
+    return (uint64_t)(uint32_t)(__double2hiint(w) & 0xfffff) << 32 | (uint32_t)__double2loint(w);
 }
 __device__ __forceinline__ uint64_t steps_of(const Scale& r, const double* table, float l)
 {
     return steps_of(Constants(), r, table, l);
 }
-__device__ __forceinline__ double weight_of(const Scale& r, const double* table, float l)
+// For fp32, whose least value is 2^-149: at least 2^-151.
+__device__ __forceinline__ double weight_of(const Constants& k, const Scale& r, const double* table, float l)
 {
-    if (((double)l - r.top) * r.c < -32. * 1100.)
-        return 0.;
     int n;
-    const double s = series_of(Constants(), r, l, n);
-    return ldexp(table[n & 31] * s, n >> 5);
+    const double s = series_of(k, r, fmax((double)l - r.top, r.least * (151. / 45.)), n);
+    return power_of(table, n, 0) * s;
 }
 
 // Whether an entry counts, by its bits: the compiler takes a float comparison of what entry() has selected back to the
@@ -196,6 +199,7 @@ template <typename T, int THREADS_> struct Streamed {
     int first, end;
     bool infinite;                                           // entries of +infinity are all that counts
     __device__ __forceinline__ void load() { infinite = false; }
+    __device__ __forceinline__ void settle() {}
     __device__ __forceinline__ void only_infinite() { infinite = true; }
     // f(vector, index of its first element) for every whole vector, AHEAD of them on their way to a lane
     template <typename F> __device__ __forceinline__ void vectors(int whole, F f) const
@@ -305,6 +309,9 @@ template <typename T, int THREADS_, int PER_> struct Held {
                         }
                 }
         }
+    }
+    __device__ __forceinline__ void settle()                 // once they are there
+    {
         change([](float l) { return entry(l); });
     }
     template <typename F> __device__ __forceinline__ void each(F f) const
@@ -383,12 +390,16 @@ template <int CTRL, int ROWS> __device__ __forceinline__ uint64_t moved(uint64_t
 {
     return (uint64_t)moved<CTRL, ROWS>((uint32_t)(x >> 32)) << 32 | moved<CTRL, ROWS>((uint32_t)x);
 }
-template <typename N> __device__ __forceinline__ N lane_scan(N x)
+template <typename N> __device__ __forceinline__ N row_scan(N x)         // of 16 lanes
 {
     x += moved<0x111, 0xF>(x);
     x += moved<0x112, 0xF>(x);
     x += moved<0x114, 0xF>(x);
-    x += moved<0x118, 0xF>(x);
+    return x + moved<0x118, 0xF>(x);
+}
+template <typename N> __device__ __forceinline__ N lane_scan(N x)
+{
+    x = row_scan(x);
     x += moved<0x142, 0xA>(x);
     return x + moved<0x143, 0xC>(x);
 }
@@ -420,13 +431,9 @@ template <int THREADS> __device__ __forceinline__ void scan(Hist& h, Shared& s)
         s.wave_count[wave] = ct;
     }
     __syncthreads();
-    mt -= m_own;
-    ct -= c_own;
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-        mt += w < wave ? s.wave_mass[w] : 0;
-        ct += w < wave ? s.wave_count[w] : 0;
-    }
+    static_assert(WAVES <= 16, "the wavefronts before this one in a row of lanes");
+    mt += at_lane(row_scan(lane < wave ? s.wave_mass[lane] : 0), 15) - m_own;
+    ct += at_lane(row_scan(lane < wave ? s.wave_count[lane] : 0), 15) - c_own;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         h.mass[PER * tid + i] = mt + m[i];
@@ -524,9 +531,10 @@ __device__ __forceinline__ Scale scale_of(float hi, float lo, float t)
         r.far_step = 0.f;
         r.far_from = (float)kLast;
     }
-    r.c = 46.166241308446828384 / (double)t;                 // 32 log2 e
+    const double t64 = fmin((double)t, 1e300);               // an infinite one leaves -infinity no weight either
+    r.c = 46.166241308446828384 / t64;                       // 32 log2 e
     r.top = r.max;
-    r.floor = fmaxf((float)(r.top - 31.191623125197541 * (double)t), -3.4028234663852886e38f);      // 45 ln 2
+    r.least = -31.191623125197541 * t64;                     // 45 ln 2
     return r;
 }
 
@@ -638,6 +646,16 @@ __device__ __forceinline__ int first_bucket(const Hist& h, Place place, uint64_t
     return fine ? from + __ffsll((unsigned long long)fine) - 1 : kLast;
 }
 
+// The logit at a height, off to the given side by its rounding; where all have one height that side's infinity.
+__device__ __forceinline__ float logit_at(const Scale& r, float height, float side)
+{
+    float d = height * __builtin_amdgcn_rcpf(r.step);
+    if (r.far_step > 0.f)
+        d = fmaxf(d, (height - r.far_from) * __builtin_amdgcn_rcpf(r.far_step));
+    const float l = r.max - d + side * 4.7683716e-7f * (fabsf(r.max) + fabsf(d));     // 2^-21
+    return r.step > 0.f && fabsf(l) < infinity() ? l : side * infinity();
+}
+
 // Each filter leaves a weight between two sums of buckets; so each goal, and the bucket of each place, lies between
 // two others.  By the first wavefront, into s.plan.
 __device__ __forceinline__ void make_plan(const Hist& h, const Scale& r, const Wish& w, Shared& s)
@@ -706,12 +724,23 @@ __device__ __forceinline__ void make_plan(const Hist& h, const Scale& r, const W
             }
             s.plan = q;
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (threadIdx.x < 4) {                               // a hundredth of a bucket wider than the range: heights
+            const int i = threadIdx.x;                       // up to 1024 and their inverses are off by 2^-11 at most
+            const float f = s.plan.from[i], t = s.plan.to[i];
+            s.plan.high[i] = f < t ? logit_at(r, f - 0.01f, 1.f) : -infinity();
+            s.plan.low[i] = fmaxf(t < (float)kBuckets ? logit_at(r, t + 0.01f, -1.f) : -infinity(),
+                                  -3.4028234663852886e38f);  // masked entries stay outside
+        }
     }
     __syncthreads();
 }
 
-// The entries for which in(l, i) holds, into the list (in any order); s.number of them.
-template <typename Source, typename F> __device__ __forceinline__ void gather(const Source& row, Shared& s, F in)
+// The entries for which in(l, i) holds, into the list (in any order); s.number of them.  near(l) holds for these and
+// few others.
+template <typename Source, typename G, typename F>
+__device__ __forceinline__ void gather(const Source& row, Shared& s, G near, F in)
 {
     if (threadIdx.x == 0)
         s.number = 0;
@@ -720,11 +749,11 @@ template <typename Source, typename F> __device__ __forceinline__ void gather(co
         bool hit[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            hit[e] = in(l[e], i + e);
+            hit[e] = near(l[e]);
         if (hit[0] | hit[1] | hit[2] | hit[3]) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (hit[e]) {
+                if (hit[e] && in(l[e], i + e)) {
                     const uint32_t at = atomicAdd(&s.number, 1u);
                     if (at < kList)
                         s.x.list.order[at] = order_of(l[e], i + e);
@@ -738,11 +767,19 @@ template <typename Source, typename F> __device__ __forceinline__ void gather(co
 template <typename Source> __device__ __forceinline__ void gather_plan(const Source& row, const Scale& r, Shared& s)
 {
     const Plan q = s.plan;
-    gather(row, s, [&](float l, int) {
+    const bool more = __builtin_amdgcn_readfirstlane(q.ranges) > 2;
+    auto near = [&](float l) {
+        bool hit = (l <= q.high[0] && l >= q.low[0]) | (l <= q.high[1] && l >= q.low[1]);
+        if (more)
+            hit |= (l <= q.high[2] && l >= q.low[2]) | (l <= q.high[3] && l >= q.low[3]);
+        return hit;
+    };
+    gather(row, s, near, [&](float l, int) {
         const float f = height_of(r, l);
-        bool hit = (f >= q.from[0] && f < q.to[0]) | (f >= q.from[1] && f < q.to[1]);
-        if (q.ranges > 2)
-            hit |= (f >= q.from[2] && f < q.to[2]) | (f >= q.from[3] && f < q.to[3]);
+        bool hit = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            hit |= f >= q.from[i] && f < q.to[i];
         return hit && live_entry(l);
     });
 }
@@ -766,11 +803,13 @@ __device__ __forceinline__ void choose_few(const Hist& h, const Scale& r, const 
         const uint64_t own = there ? steps_of(r, s.table, logit_of(x)) : 0;
         uint64_t mass = there ? h.mass_before(bucket) : 0;
         uint32_t count = there ? h.count_before(bucket) : 0;
-        for (int i = 0; i < n; ++i) {
-            const bool before = at_lane(x, i) < x && (int)at_lane((uint32_t)bucket, i) == bucket;
-            mass += before ? at_lane(own, i) : 0;
-            count += before;
-        }
+        for (int i0 = 0; i0 < n; i0 += 4)                    // those behind the last are behind all
+#pragma unroll
+            for (int i = i0; i < i0 + 4; ++i) {
+                const bool before = at_lane(x, i) < x && (int)at_lane((uint32_t)bucket, i) == bucket;
+                mass += before ? at_lane(own, i) : 0;
+                count += before;
+            }
         Choice c = {kNowhere, h.mass[kLast], -1};
         auto look = [&](Place place, uint64_t goal) {
             const uint64_t hit = __ballot(there && takes(place, goal, mass, own, count, 1));
@@ -956,7 +995,8 @@ __device__ __forceinline__ void find(const Source& row, const Scale& r, Shared& 
     auto in = [&](float l, int i) {
         return live_entry(l) && bucket_of(r, l) == bucket && order_of(l, i) >> shift == prefix;
     };
-    gather(row, s, in);
+    const auto any = [](float) { return true; };
+    gather(row, s, any, in);
 #pragma unroll 1
     while (s.number > kList) {                               // at shift 0 one entry is left
         const int next = shift > kDigitBits ? shift - kDigitBits : 0, mask = (1 << (shift - next)) - 1;
@@ -975,7 +1015,7 @@ __device__ __forceinline__ void find(const Source& row, const Scale& r, Shared& 
         find_bucket<THREADS>(s.x.digits, s, place, goal, (int)(goal >> next) & mask, mass0, count0);
         prefix = prefix << (shift - next) | (uint32_t)s.at;
         shift = next;
-        gather(row, s, in);
+        gather(row, s, any, in);
     }
     const uint64_t mass0 = s.base_mass;
     const uint32_t count0 = s.base_count;
@@ -1063,9 +1103,10 @@ __device__ __forceinline__ void choose(const Source& again, const Scale& r, cons
 }
 
 // The probability of an entry after the cut, in the share that the kept weight has of it.
-__device__ __forceinline__ float probability(const Scale& r, const double* table, const Choice& c, double share, float l, int i)
+__device__ __forceinline__ float probability(const Constants& k, const Scale& r, const double* table, const Choice& c,
+                                             double share, float l, int i)
 {
-    return live_entry(l) && order_of(l, i) <= c.cut ? (float)(weight_of(r, table, l) * share) : 0.f;
+    return live_entry(l) && order_of(l, i) <= c.cut ? (float)(weight_of(k, r, table, l) * share) : 0.f;
 }
 
 // The distribution that is left of the entries.
@@ -1073,11 +1114,12 @@ template <typename Source>
 __device__ __forceinline__ void put_probs(const Source& row, const Scale& r, const Shared& s, const Choice& c, float* out)
 {
     const double share = kOne / (double)c.total;
+    const Constants k;
     row.each4([&](const float(&l)[4], int i) {
         rows::AtElement a;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            a[e] = __float_as_uint(probability(r, s.table, c, share, l[e], i + e));
+            a[e] = __float_as_uint(probability(k, r, s.table, c, share, l[e], i + e));
         if (i + 4 <= row.end) {
             *reinterpret_cast<rows::AtElement*>(out + i) = a;
         } else {
@@ -1105,11 +1147,12 @@ __global__ __launch_bounds__(Source::THREADS) void sample_row_kernel(const T* __
     row.end = vocab;
     const Wish w = wish_of(a, n);
     row.load();
+    start_table(s);                                          // while they are on their way
+    clear<THREADS>(s.h);
+    row.settle();
     float* out = a.probs ? a.probs + n * vocab : nullptr;
     float hi, lo;
     extremes(row, hi, lo);
-    start_table(s);
-    clear<THREADS>(s.h);
     reduce<THREADS>(hi, lo, s);
     if (!live_entry(hi) || !(w.t > 0.f)) {                         // nothing to draw from, or the largest is taken
         const int arg = !live_entry(hi) ? -1 : index_of(row, hi, s);
@@ -1161,7 +1204,7 @@ __device__ __forceinline__ Source chunk_of(const T* logits, const Settings& a, i
     row.first = chunk * a.chunk;
     row.end = a.vocab - row.first < a.chunk ? a.vocab : row.first + a.chunk;
     row.load();
-    return row;
+    return row;                                              // to be settled
 }
 
 // The row's extremes from its chunks'.
@@ -1206,7 +1249,8 @@ __global__ __launch_bounds__(Source::THREADS) void sample_max_kernel(const T* __
     __shared__ Shared s;
     const int64_t n = blockIdx.x / a.chunks;
     const int chunk = blockIdx.x % a.chunks;
-    const Source row = chunk_of<Source>(logits, a, n, chunk);
+    Source row = chunk_of<Source>(logits, a, n, chunk);
+    row.settle();
     float hi, lo;
     extremes(row, hi, lo);
     reduce<Source::THREADS>(hi, lo, s);
@@ -1230,6 +1274,7 @@ __global__ __launch_bounds__(Source::THREADS) void sample_hist_kernel(const T* _
         return;
     start_table(s);
     clear<THREADS>(s.h);
+    row.settle();
     __syncthreads();
     const Scale r = scale_of(hi, lo, w.t);
     if (hi == infinity())
@@ -1255,17 +1300,19 @@ __global__ __launch_bounds__(Source::THREADS) void sample_gather_kernel(const T*
     const Wish w = wish_of(a, n);
     float hi, lo;
     row_extremes(x, a, n, hi, lo);
-    if (!live_entry(hi) || !(w.t > 0.f)) {                         // in place of a list: where the maximum is first
+    if (!live_entry(hi) || !(w.t > 0.f)) {                   // in place of a list: where the maximum is first
+        row.settle();
         const int arg = !live_entry(hi) ? INT32_MAX : index_of(row, hi, s);
         if (tid == 0)
             x.number[blockIdx.x] = (uint32_t)arg;
         return;
     }
     const Scale r = scale_of(hi, lo, w.t);
-    if (hi == infinity())
-        row.only_infinite();
     sum_chunks<THREADS>(x, a, n, w.k > 0, s);
     make_plan(s.h, r, w, s);
+    row.settle();
+    if (hi == infinity())
+        row.only_infinite();
     if (chunk == 0) {
         const int64_t to = ((int64_t)gridDim.x + n) * kBuckets;
         for (int b = tid; b < kBuckets; b += THREADS) {
@@ -1340,6 +1387,7 @@ __global__ __launch_bounds__(Source::THREADS) void sample_probs_kernel(const T* 
     __shared__ Shared s;
     const int64_t n = blockIdx.x / a.chunks;
     Source row = chunk_of<Source>(logits, a, n, blockIdx.x % a.chunks);
+    row.settle();
     const Wish w = wish_of(a, n);
     float hi, lo;
     row_extremes(x, a, n, hi, lo);
