@@ -18,14 +18,13 @@
 // one made in 64-bit floating point but at a border nearer than some 10^-11.
 //
 // Bound by a chain of dependent passes where there are few rows (maximum, histogram, its sums,
-// collection, lookup: some 4 us each), by the arithmetic of the weights (some 35 instructions an
-// entry, half of them 64-bit) and the 64-bit LDS additions where there are many; reading the
-// logits is a tenth of it.  A row of up to 32,768 entries stays in the registers of one workgroup
-// for all passes, so they are one launch: 1 row of 32,000 19 us, 64 23 us, 256 in bf16 27 us.
-// Longer rows are read again by each pass, and while they are few they are cut into chunks, one
-// workgroup each, with a launch for the maximum, the histograms, the collection and the choice
-// (and one for the distribution): 64 rows of 128,000 50 us, of which 7, 13, 15 and 13 are
-// the launches; 256 rows, whole, 92 us.
+// collection, lookup: 1 to 7 us each), by the instructions of the weights (some 30 an entry, a third of
+// them 64-bit) and one compute unit's reads of a row where there are many; reading the logits once
+// would take a tenth to a third of it.  A row of up to 32,768 entries stays in the registers of one
+// workgroup for all passes, so they are one launch: 1 row of 32,000 16 us, 64 21 us, 256 in bf16
+// 26 us.  Longer rows are read again by each pass, and while they are few they are cut into chunks,
+// one workgroup each, with a launch for the maximum, the histograms, the collection and the choice
+// (and one for the distribution): 64 rows of 128,000 46 us; 256 rows, whole, 84 us.
 #include <type_traits>
 
 #include "common.h"
@@ -76,7 +75,7 @@ struct Plan {
     int k, p, m;                                             // k, p: whether they are in force; m: its bucket, or -1
     int ranges;
     float from[4], to[4];
-    float high[4], low[4];                                   // logits between which all of a range lie, and little else
+    float middle[4], reach[4];                               // all of a range is this near to its middle, and little else
 };
 
 struct Choice {
@@ -193,7 +192,7 @@ __device__ __forceinline__ float entry(float l, bool infinite)
 // any element's address.
 template <typename T, int THREADS_> struct Streamed {
     static constexpr int THREADS = THREADS_;
-    // vectors in flight (256 rows of 128,000 fp32: one 95 us, two 92, four 94; in bf16, of 65,536: one 47, four 49)
+    // vectors in flight (256 rows of 128,000 fp32: one 86 us, two 84, four 84; 128 of 50,001 in bf16: 35.5, 36.6, 39)
     static constexpr int AHEAD = sizeof(T) == 2 ? 1 : 2;
     const T* row;
     int first, end;
@@ -729,31 +728,33 @@ __device__ __forceinline__ void make_plan(const Hist& h, const Scale& r, const W
         if (threadIdx.x < 4) {                               // a hundredth of a bucket wider than the range: heights
             const int i = threadIdx.x;                       // up to 1024 and their inverses are off by 2^-11 at most
             const float f = s.plan.from[i], t = s.plan.to[i];
-            s.plan.high[i] = f < t ? logit_at(r, f - 0.01f, 1.f) : -infinity();
-            s.plan.low[i] = fmaxf(t < (float)kBuckets ? logit_at(r, t + 0.01f, -1.f) : -infinity(),
-                                  -3.4028234663852886e38f);  // masked entries stay outside
+            const float high = fminf(logit_at(r, f - 0.01f, 1.f), r.max);
+            const float low = t < (float)kBuckets ? fmaxf(logit_at(r, t + 0.01f, -1.f), r.min) : r.min;
+            const float off = 2.3841858e-7f * (fabsf(high) + fabsf(low));          // 2^-22: their own roundings
+            s.plan.middle[i] = f < t ? 0.5f * high + 0.5f * low : 0.f;
+            s.plan.reach[i] = f < t ? 0.5f * high - 0.5f * low + off : -infinity();
         }
     }
     __syncthreads();
 }
 
-// The entries for which in(l, i) holds, into the list (in any order); s.number of them.  near(l) holds for these and
-// few others.
+// The entries for which in(l, i) holds, into the list (in any order); s.number of them.  beyond(l) is positive for none
+// of these, and for most others.
 template <typename Source, typename G, typename F>
-__device__ __forceinline__ void gather(const Source& row, Shared& s, G near, F in)
+__device__ __forceinline__ void gather(const Source& row, Shared& s, G beyond, F in)
 {
     if (threadIdx.x == 0)
         s.number = 0;
     __syncthreads();
     row.each4([&](const float(&l)[4], int i) {
-        bool hit[4];
+        float x[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            hit[e] = near(l[e]);
-        if (hit[0] | hit[1] | hit[2] | hit[3]) {
+            x[e] = beyond(l[e]);
+        if (fminf(fminf(x[0], x[1]), fminf(x[2], x[3])) <= 0.f) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (hit[e] && in(l[e], i + e)) {
+                if (x[e] <= 0.f && in(l[e], i + e)) {
                     const uint32_t at = atomicAdd(&s.number, 1u);
                     if (at < kList)
                         s.x.list.order[at] = order_of(l[e], i + e);
@@ -768,13 +769,14 @@ template <typename Source> __device__ __forceinline__ void gather_plan(const Sou
 {
     const Plan q = s.plan;
     const bool more = __builtin_amdgcn_readfirstlane(q.ranges) > 2;
-    auto near = [&](float l) {
-        bool hit = (l <= q.high[0] && l >= q.low[0]) | (l <= q.high[1] && l >= q.low[1]);
+    // no lane masks for each entry: the scalar unit's operations on them would be half of the work
+    auto beyond = [&](float l) {
+        float x = fminf(fabsf(l - q.middle[0]) - q.reach[0], fabsf(l - q.middle[1]) - q.reach[1]);
         if (more)
-            hit |= (l <= q.high[2] && l >= q.low[2]) | (l <= q.high[3] && l >= q.low[3]);
-        return hit;
+            x = fminf(fminf(x, fabsf(l - q.middle[2]) - q.reach[2]), fabsf(l - q.middle[3]) - q.reach[3]);
+        return x;
     };
-    gather(row, s, near, [&](float l, int) {
+    gather(row, s, beyond, [&](float l, int) {
         const float f = height_of(r, l);
         bool hit = false;
 #pragma unroll
@@ -995,7 +997,7 @@ __device__ __forceinline__ void find(const Source& row, const Scale& r, Shared& 
     auto in = [&](float l, int i) {
         return live_entry(l) && bucket_of(r, l) == bucket && order_of(l, i) >> shift == prefix;
     };
-    const auto any = [](float) { return true; };
+    const auto any = [](float) { return 0.f; };
     gather(row, s, any, in);
 #pragma unroll 1
     while (s.number > kList) {                               // at shift 0 one entry is left
@@ -1416,7 +1418,8 @@ struct Cut {
 // Rows are cut where one workgroup would have to read them again and again, and few of them would leave most compute
 // units idle; into chunks of 16,384 where that takes no second round of workgroups.  us, fp32, whole rows, chunks of
 // 16,384, of 32,768: 1 of 128,000 56, 22, 27; 64 of 128,000 76, 62, 49; 64 of 50,001 38 and 35, 96 of them 38 and 41;
-// 128 of 128,000 79 and 100; 16 of 33,000 22 and 25; 8 of 32,000, which fit the registers, 22 and 32.
+// 128 of 128,000 79 and 100; 16 of 33,000 22 and 25; 8 of 32,000, which fit the registers, 22 and 32 (later steps took
+// as much from both sides).
 Cut cut_of(int64_t rows, int vocab)
 {
     if (rows > 80 || vocab <= 40 * 1024)
