@@ -786,10 +786,25 @@ template <typename Source> __device__ __forceinline__ void gather_plan(const Sou
     });
 }
 
-// The value of the lane `mask` away.
-__device__ __forceinline__ uint64_t other(uint64_t x, int mask)
+// The value of the lane that differs in the bit FAR (1 to 32), in registers where there is an instruction for it.
+template <int FAR> __device__ __forceinline__ uint32_t other(uint32_t x)
 {
-    return (uint64_t)(uint32_t)__shfl_xor((int)(x >> 32), mask) << 32 | (uint32_t)__shfl_xor((int)x, mask);
+    if constexpr (FAR == 1)
+        return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0xB1, 0xF, 0xF, false);
+    else if constexpr (FAR == 2)
+        return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, false);
+    else if constexpr (FAR == 8)
+        return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x128, 0xF, 0xF, false);
+    else if constexpr (FAR == 4 || FAR == 16)
+        return (uint32_t)__builtin_amdgcn_ds_swizzle((int)x, FAR << 10 | 0x1F);
+    else {
+        const auto both = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+        return threadIdx.x & 32 ? both[0] : both[1];
+    }
+}
+template <int FAR> __device__ __forceinline__ uint64_t other(uint64_t x)
+{
+    return (uint64_t)other<FAR>((uint32_t)(x >> 32)) << 32 | other<FAR>((uint32_t)x);
 }
 
 // The places looked up one after the other among the s.number <= 64 entries of the list, each compared with all of its
@@ -851,25 +866,36 @@ __device__ __forceinline__ void choose_sorted(const Hist& h, const Scale& r, con
 #pragma unroll
     for (int j = 0; j < PER; ++j)
         x[j] = j * THREADS + tid < n ? s.x.list.order[j * THREADS + tid] : kNowhere;
-    for (int run = 2; run <= size; run *= 2)
-        for (int far = run / 2; far > 0; far /= 2) {
-            if (far >= 64) {                                 // another wavefront's
-                __syncthreads();
+    auto keep = [&](int j, uint64_t y, int run, int far) {
+        const int i = j * THREADS + tid;
+        const bool up = ((i & run) == 0) == ((i & far) == 0);                // the smaller one is kept here
+        x[j] = (x[j] < y) == up ? x[j] : y;
+    };
+    for (int run = 2; run <= size; run *= 2) {
+        for (int far = run / 2; far >= 64; far /= 2) {       // another wavefront's
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                s.x.list.order[j * THREADS + tid] = x[j];
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                keep(j, s.x.list.order[(j * THREADS + tid) ^ far], run, far);
+        }
+        auto near = [&](auto far) {
+            constexpr int FAR = decltype(far)::value;
+            if (run > FAR && wave * 64 < size)
 #pragma unroll
                 for (int j = 0; j < PER; ++j)
-                    s.x.list.order[j * THREADS + tid] = x[j];
-                __syncthreads();
-            }
-#pragma unroll
-            for (int j = 0; j < PER; ++j) {
-                const int i = j * THREADS + tid;
-                if (j * THREADS >= size)
-                    break;
-                const uint64_t y = far >= 64 ? s.x.list.order[i ^ far] : other(x[j], far);
-                const bool up = ((i & run) == 0) == ((i & far) == 0);        // the smaller one is kept here
-                x[j] = (x[j] < y) == up ? x[j] : y;
-            }
-        }
+                    keep(j, other<FAR>(x[j]), run, FAR);
+        };
+        near(std::integral_constant<int, 32>{});
+        near(std::integral_constant<int, 16>{});
+        near(std::integral_constant<int, 8>{});
+        near(std::integral_constant<int, 4>{});
+        near(std::integral_constant<int, 2>{});
+        near(std::integral_constant<int, 1>{});
+    }
     __syncthreads();
     // weights, and their sums in the order of the list
     uint64_t own[PER], sum[PER];
