@@ -9,7 +9,7 @@
 // a histogram of the distance from the maximum (768 buckets over 16 nats, 256 over what is
 // behind, or 1024 over less) bounds the weight before each place, and so the few buckets in
 // which each can lie; only their entries are collected, and the places are looked up one after
-// the other: up to 64 entries by one wavefront that compares each with all, up to 1024 sorted.
+// the other: up to 64 entries by one wavefront, up to 1024 by the workgroup.
 // More entries in those buckets (ties, places in the last bucket) are cut further by digits of
 // (logit, index).
 //
@@ -21,10 +21,10 @@
 // collection, lookup: 1 to 7 us each), by the instructions of the weights (some 30 an entry, a third of
 // them 64-bit) and one compute unit's reads of a row where there are many; reading the logits once
 // would take a tenth to a third of it.  A row of up to 32,768 entries stays in the registers of one
-// workgroup for all passes, so they are one launch: 1 row of 32,000 16 us, 64 21 us, 256 in bf16
-// 26 us.  Longer rows are read again by each pass, and while they are few they are cut into chunks,
+// workgroup for all passes, so they are one launch: 1 row of 32,000 16 us, 64 19 us, 256 in bf16
+// 23 us.  Longer rows are read again by each pass, and while they are few they are cut into chunks,
 // one workgroup each, with a launch for the maximum, the histograms, the collection and the choice
-// (and one for the distribution): 64 rows of 128,000 46 us; 256 rows, whole, 84 us.
+// (and one for the distribution): 64 rows of 128,000 43 us; 256 rows, whole, 80 us.
 #include <type_traits>
 
 #include "common.h"
@@ -807,26 +807,56 @@ template <int FAR> __device__ __forceinline__ uint64_t other(uint64_t x)
     return (uint64_t)other<FAR>((uint32_t)(x >> 32)) << 32 | other<FAR>((uint32_t)x);
 }
 
-// The places looked up one after the other among the s.number <= 64 entries of the list, each compared with all of its
-// bucket for what is before it.  By the first wavefront, into s.choice.
+// A step of a bitonic sort within wavefronts: entry i of runs of `run`.
+template <int FAR> __device__ __forceinline__ uint64_t exchanged(uint64_t x, int i, int run)
+{
+    const uint64_t y = other<FAR>(x);
+    const bool up = ((i & run) == 0) == ((i & FAR) == 0);    // the smaller one is kept here
+    return (x < y) == up ? x : y;
+}
+// All steps within a wavefront of the stage that makes runs of `run`.
+template <typename F> __device__ __forceinline__ void near_steps(int run, F step)
+{
+    if (run > 32) step(std::integral_constant<int, 32>{});
+    if (run > 16) step(std::integral_constant<int, 16>{});
+    if (run > 8) step(std::integral_constant<int, 8>{});
+    if (run > 4) step(std::integral_constant<int, 4>{});
+    if (run > 2) step(std::integral_constant<int, 2>{});
+    step(std::integral_constant<int, 1>{});
+}
+
+// The places looked up one after the other among the s.number <= 64 entries of the list.  What is before an entry is
+// found by comparing it with the others of its bucket or, from 9 entries on, by sorting them and adding up (40 entries:
+// 3800 cycles by sorting, 9600 by comparing; 10: 3800 and 4200; 3: 2700 by comparing).  By the first wavefront, into
+// s.choice.
 __device__ __forceinline__ void choose_few(const Hist& h, const Scale& r, const Wish& w, Shared& s)
 {
     if (threadIdx.x < 64) {
         const int lane = threadIdx.x, n = (int)s.number;
         const Plan q = s.plan;
         const bool there = lane < n;
-        const uint64_t x = there ? s.x.list.order[lane] : kNowhere;
+        uint64_t x = there ? s.x.list.order[lane] : kNowhere;
+        if (n > 8)
+            for (int run = 2; run <= 64; run *= 2)
+                near_steps(run, [&](auto far) { x = exchanged<decltype(far)::value>(x, lane, run); });
         const int bucket = there ? bucket_of(r, logit_of(x)) : -1;
         const uint64_t own = there ? steps_of(r, s.table, logit_of(x)) : 0;
         uint64_t mass = there ? h.mass_before(bucket) : 0;
         uint32_t count = there ? h.count_before(bucket) : 0;
-        for (int i0 = 0; i0 < n; i0 += 4)                    // those behind the last are behind all
-#pragma unroll
-            for (int i = i0; i < i0 + 4; ++i) {
+        if (n > 8) {
+            const uint64_t sum = lane_scan(own) - own;
+            const int previous = __shfl_up(bucket, 1);       // by all lanes
+            const uint64_t firsts = __ballot(lane == 0 || previous != bucket) & (~0ull >> (63 - lane));
+            const int at = 63 - __clzll((long long)firsts);  // the bucket's first lane
+            mass += sum - ((uint64_t)(uint32_t)__shfl((int)(sum >> 32), at) << 32 | (uint32_t)__shfl((int)sum, at));
+            count += lane - at;
+        } else {
+            for (int i = 0; i < n; ++i) {
                 const bool before = at_lane(x, i) < x && (int)at_lane((uint32_t)bucket, i) == bucket;
                 mass += before ? at_lane(own, i) : 0;
                 count += before;
             }
+        }
         Choice c = {kNowhere, h.mass[kLast], -1};
         auto look = [&](Place place, uint64_t goal) {
             const uint64_t hit = __ballot(there && takes(place, goal, mass, own, count, 1));
@@ -866,11 +896,6 @@ __device__ __forceinline__ void choose_sorted(const Hist& h, const Scale& r, con
 #pragma unroll
     for (int j = 0; j < PER; ++j)
         x[j] = j * THREADS + tid < n ? s.x.list.order[j * THREADS + tid] : kNowhere;
-    auto keep = [&](int j, uint64_t y, int run, int far) {
-        const int i = j * THREADS + tid;
-        const bool up = ((i & run) == 0) == ((i & far) == 0);                // the smaller one is kept here
-        x[j] = (x[j] < y) == up ? x[j] : y;
-    };
     for (int run = 2; run <= size; run *= 2) {
         for (int far = run / 2; far >= 64; far /= 2) {       // another wavefront's
             __syncthreads();
@@ -879,22 +904,19 @@ __device__ __forceinline__ void choose_sorted(const Hist& h, const Scale& r, con
                 s.x.list.order[j * THREADS + tid] = x[j];
             __syncthreads();
 #pragma unroll
-            for (int j = 0; j < PER; ++j)
-                keep(j, s.x.list.order[(j * THREADS + tid) ^ far], run, far);
+            for (int j = 0; j < PER; ++j) {
+                const int i = j * THREADS + tid;
+                const uint64_t y = s.x.list.order[i ^ far];
+                const bool up = ((i & run) == 0) == ((i & far) == 0);
+                x[j] = (x[j] < y) == up ? x[j] : y;
+            }
         }
-        auto near = [&](auto far) {
-            constexpr int FAR = decltype(far)::value;
-            if (run > FAR && wave * 64 < size)
+        if (wave * 64 < size)
+            near_steps(run, [&](auto far) {
 #pragma unroll
                 for (int j = 0; j < PER; ++j)
-                    keep(j, other<FAR>(x[j]), run, FAR);
-        };
-        near(std::integral_constant<int, 32>{});
-        near(std::integral_constant<int, 16>{});
-        near(std::integral_constant<int, 8>{});
-        near(std::integral_constant<int, 4>{});
-        near(std::integral_constant<int, 2>{});
-        near(std::integral_constant<int, 1>{});
+                    x[j] = exchanged<decltype(far)::value>(x[j], j * THREADS + tid, run);
+            });
     }
     __syncthreads();
     // weights, and their sums in the order of the list
