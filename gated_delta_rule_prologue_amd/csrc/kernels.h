@@ -269,7 +269,7 @@ hipError_t launch_short_conv_bwd(const ShortConvArgs& p, hipStream_t stream);
 
 // Queries and keys of every head normalised, weighted and rotated (qk_norm.hip).
 constexpr int kQkMaxWidth = 512;
-constexpr int kQkBwdBlocks = 512;                // workgroups of q, and of k, in a backward that sums weights' gradients
+constexpr int kQkBwdBlocks = 1024;               // workgroups of q, and of k, in a backward that sums weights' gradients
 
 struct QkNormArgs {
     bool bf16;

@@ -596,9 +596,12 @@ template <typename T> hipError_t bwd(const QkNormArgs& p, hipStream_t stream)
         typedef typename decltype(tag)::type S;
         Side<T> q = side_of<S>(p, 0, true), k = side_of<S>(p, 1, true);
         if (weights) {                                       // as many workgroups each: their partial sums lie side by side
-            // (LM layer: 256 of them 36.9, 512 39.1 us; with a wavefront a row 15.5 and 13.3 us)
+            // fewer where a wavefront holds several rows, more where its lanes hold but a pair each (LM layer: 256 of them
+            // 36.9, 512 39.1 us; 4096 tokens of 4 + 4 heads of 256 in fp32: 256 25.5, 512 28.2 us; 20,000 of 5 + 1 of 75:
+            // 512 57, 1024 39 us; 4096 of 6 + 6 of 130 in bf16: 512 24.3, 1024 26.3 us)
             const int most = q.blocks > k.blocks ? q.blocks : k.blocks, all = qk_norm_bwd_blocks(p.tokens);
-            const int cap = S::GROUPS >= 16 && all > kQkBwdBlocks / 2 ? kQkBwdBlocks / 2 : all;
+            const int limit = S::GROUPS >= 8 ? kQkBwdBlocks / 4 : S::E > 2 ? kQkBwdBlocks / 2 : kQkBwdBlocks;
+            const int cap = all < limit ? all : limit;
             q.blocks = most < cap ? most : cap;
             k.blocks = k.heads ? q.blocks : 0;
         }
