@@ -423,8 +423,8 @@ __global__ __launch_bounds__(kThreads) void short_conv_step_kernel(const T* __re
 template <typename T, int K, int VE, Mode MODE>
 __global__ __launch_bounds__(kThreads) void short_conv_bwd_kernel(
     const T* __restrict__ x, int64_t ldx, const T* __restrict__ w, const T* __restrict__ bias,
-    const T* __restrict__ hist, const int32_t* __restrict__ cu, const T* __restrict__ dy, bool act, int n_seqs,
-    int tokens, int C, int lv_bits, int chunks, int run, T* __restrict__ dx, float* __restrict__ part)
+    const T* __restrict__ hist, const int32_t* __restrict__ cu, const T* __restrict__ dy, bool act, bool bias_grad,
+    int n_seqs, int tokens, int C, int lv_bits, int chunks, int run, T* __restrict__ dx, float* __restrict__ part)
 {
     constexpr bool FEW = MODE == kFew;
     typedef Group<T, VE> G;
@@ -508,7 +508,7 @@ __global__ __launch_bounds__(kThreads) void short_conv_bwd_kernel(
 #pragma unroll
                         for (int i = 0; i < kBatch; ++i)
                             weigh(K - 1 + i);
-                        if (bias)
+                        if (bias_grad)
 #pragma unroll
                             for (int i = 0; i < kBatch; ++i)
 #pragma unroll
@@ -781,7 +781,7 @@ template <typename T> hipError_t bwd(const ShortConvArgs& p, hipStream_t stream)
             hipLaunchKernelGGL((short_conv_bwd_kernel<T, K, VE, decltype(mode)::mode>), dim3((unsigned)nb * plan.chunks),
                                dim3(kThreads), kThreads * VE * sizeof(float), stream, (const T*)p.x, p.x_stride,
                                (const T*)p.w, (const T*)p.bias, (const T*)p.hist, p.cu_seqlens, (const T*)p.dy, p.silu,
-                               p.n_seqs, p.total_tokens, p.channels, plan.lv_bits, plan.chunks,
+                               p.dbias != nullptr, p.n_seqs, p.total_tokens, p.channels, plan.lv_bits, plan.chunks,
                                bwd_run(p.total_tokens, plan), (T*)p.dx, p.ws);
             return hipGetLastError();
         });

@@ -645,7 +645,7 @@ size_t prism_conv_workspace_bytes(const prism_conv_dims* d);
  *   hist_out    out [n_seqs, K - 1, C] or NULL (not written): the history to carry on; may be
  *               the buffer of hist
  * hist and hist_out are not looked at when K == 1.  Rows behind the last sequence
- * (cu_seqlens[n_seqs] and on) are neither read nor written.
+ * (cu_seqlens[n_seqs] and on) have no effect and are not written.
  */
 prism_status prism_short_conv(const prism_conv_dims* d, const void* x, const void* w, const void* bias,
                               const void* hist, const int32_t* cu_seqlens, int activation,

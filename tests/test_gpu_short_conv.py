@@ -326,3 +326,23 @@ def test_offsets_past_32_bits():
     # sums of the same 301 terms beside zeros, in two orders: 301 roundings of their magnitudes each
     size = (dy[-last:].float().abs() * 1.1).sum(0)
     assert ((g["bias"] - g1["bias"]).abs() <= 2 * 301 * 2.0 ** -24 * size).all()
+
+
+def test_gradient_of_a_bias_that_is_zero():
+    """The C entry forms dbias without a bias too: that of a bias of zeros."""
+    import ctypes
+    import torch
+    from gated_delta_rule_prologue_amd import binding as B
+    d = make([37, 0, 260, 3], 48, 4, "f32", bias=False, hist=False, seed=21)
+    T, C = d["x"].shape
+    zero = torch.zeros(C, device="cuda")
+    want = B.short_conv_bwd(d["x"], d["w"], d["cu_t"], d["dy"], bias=zero)
+    dims = B.ConvDims(4, T, C, 4, 0, C)
+    dx, dw, db = torch.empty_like(d["x"]), torch.empty(C, 4, device="cuda"), torch.full((C,), 7.0, device="cuda")
+    ws = torch.empty(B.conv_workspace_bytes(dims), dtype=torch.uint8, device="cuda")
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    got = B.lib().prism_short_conv_bwd(ctypes.byref(dims), p(d["x"]), p(d["w"]), None, None, p(d["cu_t"]), 1, p(d["dy"]), p(dx),
+                                       p(dw), p(db), None, p(ws), ws.numel(),
+                                       ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert got == B.PRISM_OK
+    assert torch.equal(dx, want["x"]) and torch.equal(dw, want["w"]) and torch.equal(db, want["bias"])
