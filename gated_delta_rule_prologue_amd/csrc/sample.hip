@@ -24,7 +24,8 @@
 // workgroup for all passes, so they are one launch: 1 row of 32,000 16 us, 64 19 us, 256 in bf16
 // 23 us.  Longer rows are read again by each pass, and while they are few they are cut into chunks,
 // one workgroup each, with a launch for the maximum, the histograms, the collection and the choice
-// (and one for the distribution): 64 rows of 128,000 43 us; 256 rows, whole, 81 us.
+// (and one for the distribution): 64 rows of 128,000 43 us; 256 rows, whole, 81 us;
+// beyond 288 rows by half as many lanes a row: 320 distributions of 50,001 81 us.
 #include <type_traits>
 
 #include "common.h"
@@ -1556,6 +1557,11 @@ template <typename T> static hipError_t launch_T(const SampleArgs& p, hipStream_
     }
     if (p.vocab <= 256 * 8) return launch_rows<T, Held<T, 256, 8>>(p, stream);
     if (p.vocab <= 256 * 32) return launch_rows<T, Held<T, 256, 32>>(p, stream);
+    // More rows than one workgroup on each compute unit: two smaller ones there overlap each other's waits.  us, with 1024
+    // and with 512 lanes: 320 of 50,001 with distributions 89 and 81, 2000 of 128,000 in bf16 466 and 402, 1000 of 9000 48
+    // and 30, 4000 of 32,000 in bf16 271 and 222; 260 of 50,001 45 and 48, 512 of 32,000 42 and 43.
+    if (p.rows > (p.vocab > 1024 * 16 && p.vocab <= 1024 * 32 ? 512 : 288))
+        return launch_rows<T, Streamed<T, 512>>(p, stream);
     if (p.vocab <= 1024 * 16) return launch_rows<T, Held<T, 1024, 16>>(p, stream);
     if (p.vocab <= 1024 * 32) return launch_rows<T, Held<T, 1024, 32>>(p, stream);
     return launch_rows<T, Streamed<T, 1024>>(p, stream);

@@ -322,3 +322,21 @@ def test_captured_and_beside_each_other(N, V):
         torch.cuda.synchronize()
         for _, out in graphs:
             assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+@pytest.mark.parametrize("V", [8193, 16385, 32771])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_rows_and_few(dtype, V):
+    """Many rows, worked on by smaller workgroups, choose as they do in small batches, to the bit."""
+    import torch
+    gen = torch.Generator().manual_seed(V)
+    N = 520
+    logits = (2 * torch.randn(N, V, generator=gen)).to({"bf16": torch.bfloat16, "f32": torch.float32}[dtype]).cuda()
+    logits[7, V // 3:] = float("-inf")
+    logits[8] = float("nan")
+    u = np.random.default_rng(V).random(N).astype(np.float32)
+    f = settings(N, V)
+    tokens, pr = check(logits, u, f, rows=range(0, N, 37))
+    for at in (slice(0, 200), slice(200, 400), slice(400, N)):
+        some, some_pr = run(logits[at], u[at], want_probs=True, **{n: v[at] for n, v in f.items()})
+        assert (some == tokens[at]).all() and (some_pr == pr[at]).all()
