@@ -80,7 +80,7 @@ struct Plan {
 };
 
 struct Choice {
-    uint64_t cut, total;                                     // the last place that is kept, the weight up to it
+    uint64_t cut, total;                                     // the last place that is kept, the weight up to it; 0: none was found
     int token;
 };
 
@@ -94,6 +94,7 @@ struct Shared {
     } x;
     double table[32];                                        // 2^(i / 32)
     uint64_t wave_mass[16], found_order, found_mass, base_mass;
+    uint64_t place_order[3], place_mass[3];                  // top-k's, top-p's and the draw's in the sorted list
     Plan plan;
     Choice choice;
     uint32_t wave_count[16], base_count, number;
@@ -161,7 +162,10 @@ __device__ __forceinline__ double power_of(const double* table, int n, int add)
 __device__ __forceinline__ uint64_t steps_of(const Constants& k, const Scale& r, const double* table, float l)
 {
     int n;
-    const double s = series_of(k, r, fmax((double)l - r.top, r.least), n);
+    double d = (double)l - r.top;
+    // an instruction: the compiler would keep a second, quieted copy of the scale's least beside it
+    asm("v_max_f64 %0, %0, %1" : "+v"(d) : "v"(r.least));
+    const double s = series_of(k, r, d, n);
     const double w = __builtin_fma(power_of(table, n, 43), s, k.steps);
     return (uint64_t)(uint32_t)(__double2hiint(w) & 0xfffff) << 32 | (uint32_t)__double2loint(w);
 }
@@ -859,9 +863,11 @@ __device__ __forceinline__ void choose_few(const Hist& h, const Scale& r, const 
             }
         }
         Choice c = {kNowhere, h.mass[kLast], -1};
+        bool missed = false;
         auto look = [&](Place place, uint64_t goal) {
             const uint64_t hit = __ballot(there && takes(place, goal, mass, own, count, 1));
             const int at = hit ? __ffsll((unsigned long long)hit) - 1 : 0;
+            missed |= hit == 0;
             c.cut = at_lane(x, at);
             c.total = at_lane(mass + own, at);
         };
@@ -875,8 +881,11 @@ __device__ __forceinline__ void choose_few(const Hist& h, const Scale& r, const 
         }
         if (w.draw) {
             const uint64_t hit = __ballot(there && takes(kPass, pass_goal(w.at, c.total), mass, own, count, 1));
+            missed |= hit == 0;
             c.token = (int)(at_lane(x, hit ? __ffsll((unsigned long long)hit) - 1 : 0) & (kSampleMaxVocab - 1));
         }
+        if (missed)
+            c.total = 0;
         if (lane == 0)
             s.choice = c;
     }
@@ -897,6 +906,8 @@ __device__ __forceinline__ void choose_sorted(const Hist& h, const Scale& r, con
 #pragma unroll
     for (int j = 0; j < PER; ++j)
         x[j] = j * THREADS + tid < n ? s.x.list.order[j * THREADS + tid] : kNowhere;
+    if (tid < 3)
+        s.place_mass[tid] = 0;
     for (int run = 2; run <= size; run *= 2) {
         for (int far = run / 2; far >= 64; far /= 2) {       // another wavefront's
             __syncthreads();
@@ -970,25 +981,26 @@ __device__ __forceinline__ void choose_sorted(const Hist& h, const Scale& r, con
         }
     }
     Choice c = {kNowhere, h.mass[kLast], -1};
-    auto look = [&](Place place, uint64_t goal) {
-        __syncthreads();
+    bool missed = false;
+    auto look = [&](int which, Place place, uint64_t goal) {
 #pragma unroll
         for (int j = 0; j < PER; ++j)
             if (j * THREADS + tid < n && takes(place, goal, mass[j], own[j], count[j], 1)) {
-                s.found_order = x[j];
-                s.found_mass = mass[j] + own[j];
+                s.place_order[which] = x[j];
+                s.place_mass[which] = mass[j] + own[j];
             }
         __syncthreads();
+        missed |= s.place_mass[which] == 0;
     };
     if (q.k) {
-        look(kCount, w.k);
-        c.cut = s.found_order;
-        c.total = s.found_mass;
+        look(0, kCount, w.k);
+        c.cut = s.place_order[0];
+        c.total = s.place_mass[0];
     }
     if (q.p) {
-        look(kReach, reach_goal(w.p, c.total));
-        c.cut = s.found_order;
-        c.total = s.found_mass;
+        look(1, kReach, reach_goal(w.p, c.total));
+        c.cut = s.place_order[1];
+        c.total = s.place_mass[1];
     }
     if (q.m >= 0 && q.m_order < c.cut) {                     // up to the last entry of its bucket that is not behind it
         __syncthreads();
@@ -1004,9 +1016,11 @@ __device__ __forceinline__ void choose_sorted(const Hist& h, const Scale& r, con
         c.total = s.found_mass;
     }
     if (w.draw) {
-        look(kPass, pass_goal(w.at, c.total));
-        c.token = (int)(s.found_order & (kSampleMaxVocab - 1));
+        look(2, kPass, pass_goal(w.at, c.total));
+        c.token = (int)(s.place_order[2] & (kSampleMaxVocab - 1));
     }
+    if (missed)
+        c.total = 0;
     if (tid == 0)
         s.choice = c;
     __syncthreads();
@@ -1141,15 +1155,17 @@ __device__ __forceinline__ void choose_slowly(const Source& row, const Scale& r,
     __syncthreads();
 }
 
-// The choice from a scanned histogram, a plan and the list; rows that the list does not hold are read again.
+// The choice from a scanned histogram, a plan and the list.  Rows that the list does not hold are read again, and so are
+// those where a place is not found in it, which the histogram alone then finds: no token is made up.
 template <typename Source>
 __device__ __forceinline__ void choose(const Source& again, const Scale& r, const Wish& w, Shared& s)
 {
-    if (s.number <= 64)
+    const uint32_t number = s.number;
+    if (number <= 64)
         choose_few(s.h, r, w, s);
-    else if (s.number <= kList)
+    else if (number <= kList)
         choose_sorted<Source::THREADS>(s.h, r, w, s);
-    else
+    if (number > kList || s.choice.total == 0)
         choose_slowly(again, r, w, s);
 }
 
