@@ -525,14 +525,17 @@ __device__ __forceinline__ Scale scale_of(float hi, float lo, float t)
     const bool infinite = hi == infinity();
     r.max = infinite ? 0.f : hi;
     r.min = infinite ? 0.f : lo;
-    const float range = r.max - r.min, near = kNats * t;
+    // a difference beyond fp32 counts as its largest number (both lines keep a slope, entries that far down share the
+    // last bucket), and no slope exceeds 2^125, so that logit_at can invert both
+    const float range = fminf(r.max - r.min, 3.402823466e38f), near = kNats * t;
+    constexpr float steepest = 4.253529587e37f;
     if (range * ((float)kNear / kLast) > near) {             // the far buckets are the wider ones
-        r.step = fminf(kNear / near, 3e38f);
-        r.far_step = (kLast - kNear) / (range - near);
+        r.step = fminf(kNear / near, steepest);
+        r.far_step = fminf((kLast - kNear) / (range - near), steepest);
         r.far_from = kNear - near * r.far_step;
     } else {
-        r.step = range > 0.f ? fminf(kLast / range, 3e38f) : 0.f;
-        r.far_step = 0.f;
+        r.step = range > 0.f ? fminf(kLast / range, steepest) : 0.f;
+        r.far_step = r.step;
         r.far_from = (float)kLast;
     }
     const double t64 = fmin((double)t, 1e300);               // an infinite one leaves -infinity no weight either
@@ -735,7 +738,7 @@ __device__ __forceinline__ void make_plan(const Hist& h, const Scale& r, const W
             const float f = s.plan.from[i], t = s.plan.to[i];
             const float high = fminf(logit_at(r, f - 0.01f, 1.f), r.max);
             const float low = t < (float)kBuckets ? fmaxf(logit_at(r, t + 0.01f, -1.f), r.min) : r.min;
-            const float off = 2.3841858e-7f * (fabsf(high) + fabsf(low));          // 2^-22: their own roundings
+            const float off = 2.3841858e-7f * (fabsf(high) + fabsf(low)) + 1.175494351e-38f;     // 2^-22: their own roundings
             s.plan.middle[i] = f < t ? 0.5f * high + 0.5f * low : 0.f;
             s.plan.reach[i] = f < t ? 0.5f * high - 0.5f * low + off : -infinity();
         }
