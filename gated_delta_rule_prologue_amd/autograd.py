@@ -175,7 +175,7 @@ class ShortConvFunction(torch.autograd.Function):
 
 
 def short_conv(x, w, cu_seqlens, bias=None, activation="silu", hist=None):
-    """Differentiable binding.short_conv: returns y.  No gradient reaches ``hist`` from a history
+    """Differentiable binding.short_conv: returns y, zero behind the last sequence.  No gradient reaches ``hist`` from a history
     carried out: sequences cut into pieces are trained piece by piece."""
     return ShortConvFunction.apply(x, w, bias, hist, cu_seqlens, activation)
 

@@ -16,7 +16,7 @@ The layer around the operator: ``norm_residual`` / ``norm_residual_bwd`` ->
 prism_norm_residual(_bwd), ``norm_gate`` / ``norm_gate_bwd`` -> prism_norm_gate(_bwd),
 ``decode_draft`` -> prism_decode_draft, ``decode_commit`` -> prism_decode_commit,
 ``verify_draft`` -> prism_verify_draft.  In front of it and behind the model's last product:
-``short_conv`` / ``short_conv_step`` / ``short_conv_bwd`` -> prism_short_conv(_step, _bwd), ``qk_norm`` /
+``short_conv`` / ``short_conv_step`` / ``short_conv_bwd`` -> prism_short_conv(_ex, _step, _bwd), ``qk_norm`` /
 ``qk_norm_bwd`` -> prism_qk_norm(_bwd), ``sample`` -> prism_sample.  These calls are checked and marshalled in C++
 (csrc/torch_calls.cpp) and run on the device of their tensors whichever is
 current, on ``stream`` or that device's current stream; what they allocate
@@ -158,6 +158,8 @@ def lib():
         L.prism_conv_workspace_bytes.restype = S
         L.prism_short_conv.argtypes = [C, P, P, P, P, P, I, P, P, P]
         L.prism_short_conv.restype = I
+        L.prism_short_conv_ex.argtypes = [C, P, P, P, P, P, I, I, P, P, P]
+        L.prism_short_conv_ex.restype = I
         L.prism_short_conv_step.argtypes = [C, P, P, P, P, I, P, P, P]
         L.prism_short_conv_step.restype = I
         L.prism_short_conv_bwd.argtypes = [C, P, P, P, P, P, I] + [P] * 6 + [S, P]
@@ -683,10 +685,11 @@ def sample_workspace_bytes(dims: SampleDims) -> int:
 def short_conv(x, w, cu_seqlens, bias=None, activation: Optional[str] = "silu", hist=None, hist_out=None, y=None,
                stream=None):
     """Causal depthwise convolution of packed sequences, act(bias + sum_m w[c, m] x[t - K + 1 + m])
-    (prism_short_conv): ``x`` [T, C] (any row stride: the columns of a wider tensor), ``w`` [C, K], K <= 8, tap
+    (prism_short_conv_ex): ``x`` [T, C] (any row stride: the columns of a wider tensor), ``w`` [C, K], K <= 8, tap
     K - 1 on the token itself, ``bias`` [C], ``activation`` "silu" or None, ``hist`` [N, K - 1, C] the rows in
     front of every sequence (None: zero).  ``hist_out`` (may be ``hist``) receives the history to
-    carry on.  Rows of ``y`` behind the last sequence are not written.  Returns (y, hist_out)."""
+    carry on.  Rows of y behind the last sequence are zero; a ``y`` that is given keeps its own.
+    Returns (y, hist_out)."""
     if stream is not None:
         with _on(x, stream):
             return short_conv(x, w, cu_seqlens, bias, activation, hist, hist_out, y)

@@ -254,6 +254,7 @@ struct ShortConvArgs {
     const void* hist;               // [n_seqs, taps - 1, channels] or null (zero)
     const int32_t* cu_seqlens;
     void *y, *hist_out;             // forward, step
+    bool clear_behind;              // forward: rows of y behind the last sequence become zero
     const void* dy;                 // backward
     void *dx, *dhist;
     float *dw, *dbias;

@@ -282,7 +282,7 @@ template <typename T, int K, int VE, Mode MODE>
 __global__ __launch_bounds__(kThreads) void short_conv_kernel(
     const T* __restrict__ x, int64_t ldx, const T* __restrict__ w, const T* __restrict__ bias,
     const T* __restrict__ hist, const int32_t* __restrict__ cu, bool act, int n_seqs, int tokens, int C, int lv_bits,
-    int chunks, int run, int walks, T* __restrict__ y, T* __restrict__ hist_out)
+    int chunks, int run, int walks, bool clear, T* __restrict__ y, T* __restrict__ hist_out)
 {
     constexpr bool FEW = MODE == kFew;
     typedef Group<T, VE> G;
@@ -324,8 +324,13 @@ __global__ __launch_bounds__(kThreads) void short_conv_kernel(
     load_taps<T, K, VE>(w, bias, me.c0, me.n, wv, bv);
     Cursor at;
     at.find(cu, n_seqs, t0, 0);
+    if (clear) {                                             // rows behind the last sequence, which the walk leaves alone
+#pragma unroll 1
+        for (int t = t0 > cu[n_seqs] ? t0 : cu[n_seqs]; t < t1; ++t)
+            G::template store_if<FEW>(out + (int64_t)t * C, me.n, typename G::Raw{});
+    }
     if (at.n >= n_seqs)
-        return;                                              // rows behind the last sequence are left alone
+        return;
     if (t0 - (K - 1) >= at.start) {
 #pragma unroll
         for (int m = 0; m < K - 1; ++m)
@@ -745,7 +750,7 @@ template <typename T> hipError_t fwd(const ShortConvArgs& p, hipStream_t stream)
                 hipLaunchKernelGGL((short_conv_kernel<T, K, VE, decltype(mode)::mode>), dim3(blocks), dim3(kThreads), 0,
                                    stream, (const T*)p.x, p.x_stride, (const T*)p.w, (const T*)p.bias,
                                    (const T*)p.hist, p.cu_seqlens, p.silu, p.n_seqs, p.total_tokens, p.channels,
-                                   plan.lv_bits, plan.chunks, run, (int)walks, (T*)p.y, (T*)p.hist_out);
+                                   plan.lv_bits, plan.chunks, run, (int)walks, p.clear_behind, (T*)p.y, (T*)p.hist_out);
                 return hipGetLastError();
             });
         if constexpr (K > 1)

@@ -151,11 +151,11 @@ size_t prism_conv_workspace_bytes(const prism_conv_dims* d)
     return round256((size_t)nb * d->channels * (d->taps + 1) * sizeof(float));
 }
 
-prism_status prism_short_conv(const prism_conv_dims* d, const void* x, const void* w, const void* bias,
-                              const void* hist, const int32_t* cu_seqlens, int activation, void* y, void* hist_out,
-                              void* stream)
+prism_status prism_short_conv_ex(const prism_conv_dims* d, const void* x, const void* w, const void* bias,
+                                 const void* hist, const int32_t* cu_seqlens, int activation, int clear_behind, void* y,
+                                 void* hist_out, void* stream)
 {
-    if (!conv_dims_ok(d) || !act_ok(activation))
+    if (!conv_dims_ok(d) || !act_ok(activation) || clear_behind < 0 || clear_behind > 1)
         return PRISM_EINVAL;
     if (!ptr_ok(w) || !opt_ok(bias) || !opt_ok(hist) || !ptr_ok(cu_seqlens) || !opt_ok(y) || !opt_ok(hist_out))
         return PRISM_EINVAL;
@@ -170,7 +170,15 @@ prism_status prism_short_conv(const prism_conv_dims* d, const void* x, const voi
     prism::ShortConvArgs p = conv_args(d, x, w, bias, hist, cu_seqlens, activation);
     p.y = y;
     p.hist_out = hist_out;
+    p.clear_behind = clear_behind;
     return from_hip(prism::launch_short_conv(p, (hipStream_t)stream));
+}
+
+prism_status prism_short_conv(const prism_conv_dims* d, const void* x, const void* w, const void* bias,
+                              const void* hist, const int32_t* cu_seqlens, int activation, void* y, void* hist_out,
+                              void* stream)
+{
+    return prism_short_conv_ex(d, x, w, bias, hist, cu_seqlens, activation, 0, y, hist_out, stream);
 }
 
 prism_status prism_short_conv_step(const prism_conv_dims* d, const void* x, const void* w, const void* bias,

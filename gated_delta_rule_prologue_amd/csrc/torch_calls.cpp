@@ -486,8 +486,9 @@ PyObject* short_conv(PyObject* const* a)
     void *bp = opt("bias", a[3], vec, dt, x), *hp = opt("hist", a[5], hist, dt, x);
     void* ho = opt("hist_out", a[6], hist, dt, x);
     Out y("y", a[7], x.sizes(), dt, x);
-    done("prism_short_conv",
-         prism_short_conv(&d, xp, wp, bp, hp, (const int32_t*)cup, (int)whole(a[4]), y.p, ho, stream_of(x)));
+    done("prism_short_conv_ex",                      // a new y holds anything: its rows behind the last sequence too are written
+         prism_short_conv_ex(&d, xp, wp, bp, hp, (const int32_t*)cup, (int)whole(a[4]), a[7] == Py_None, y.p, ho,
+                             stream_of(x)));
     return wrap(y.t);
 }
 

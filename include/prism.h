@@ -651,6 +651,13 @@ prism_status prism_short_conv(const prism_conv_dims* d, const void* x, const voi
                               const void* hist, const int32_t* cu_seqlens, int activation,
                               void* y, void* hist_out, void* stream);
 
+/* prism_short_conv with a choice for the rows of y behind the last sequence: left as they are
+ * (clear_behind 0), or zero (1), for a y whose memory holds anything and whose every row goes on
+ * to the next layer. */
+prism_status prism_short_conv_ex(const prism_conv_dims* d, const void* x, const void* w, const void* bias,
+                                 const void* hist, const int32_t* cu_seqlens, int activation, int clear_behind,
+                                 void* y, void* hist_out, void* stream);
+
 /* One new token a sequence (total_tokens must equal n_seqs; no cu_seqlens): y [n_seqs, C] from
  * x [n_seqs, C] and the history, and the history moved on by it.  hist is required when K > 1;
  * hist_out may be its buffer.  Other arguments as in prism_short_conv. */
