@@ -159,7 +159,8 @@ class ShortConvFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, bias, hist, cu_seqlens, activation):
         y, _ = binding.short_conv(x, w, cu_seqlens, bias=bias, activation=activation, hist=hist)
-        ctx.save_for_backward(x, w, bias, hist, cu_seqlens)
+        # a copy: histories are moved on in place, as a rule before the backward
+        ctx.save_for_backward(x, w, bias, None if hist is None else hist.clone(), cu_seqlens)
         ctx.activation = activation
         return y
 
@@ -176,7 +177,8 @@ class ShortConvFunction(torch.autograd.Function):
 
 def short_conv(x, w, cu_seqlens, bias=None, activation="silu", hist=None):
     """Differentiable binding.short_conv: returns y, zero behind the last sequence.  No gradient reaches ``hist`` from a history
-    carried out: sequences cut into pieces are trained piece by piece."""
+    carried out: sequences cut into pieces are trained piece by piece, and ``hist`` may be moved on to the
+    next piece (binding.short_conv with hist_out=hist) before this one's backward."""
     return ShortConvFunction.apply(x, w, bias, hist, cu_seqlens, activation)
 
 
