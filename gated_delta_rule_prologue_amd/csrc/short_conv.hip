@@ -424,6 +424,10 @@ __global__ __launch_bounds__(kThreads) void short_conv_step_kernel(const T* __re
         G::store(hist_out + (n * (K - 1) + m) * C + c0, cn, raw[m + 1]);
 }
 
+// Rows whose terms of dw and dbias a lane adds up in turn, before they join its sums of the stretches before: so the
+// rounding errors grow with 256 and a run's 256ths, not with a run.
+constexpr int kStretch = 256;
+
 // dx, and the workgroup's part of dw and dbias: part [block][C * K | C].
 template <typename T, int K, int VE, Mode MODE>
 __global__ __launch_bounds__(kThreads) void short_conv_bwd_kernel(
@@ -433,7 +437,8 @@ __global__ __launch_bounds__(kThreads) void short_conv_bwd_kernel(
 {
     constexpr bool FEW = MODE == kFew;
     typedef Group<T, VE> G;
-    extern __shared__ float buf[];                           // [groups][lv][VE]
+    extern __shared__ float buf[];                           // [groups][lv][VE]; before that, in runs beyond a stretch,
+                                                             // the lanes' sums [K + 1][VE][kThreads]
     const Where me(C, VE, lv_bits, chunks);
     const int total = cu[n_seqs] < tokens ? cu[n_seqs] : tokens;
     float acc[K + 1][VE], wv[K][VE], bv[VE];
@@ -481,6 +486,15 @@ __global__ __launch_bounds__(kThreads) void short_conv_bwd_kernel(
         const int whole = at.n < n_seqs ? (at.end < total ? at.end : total) : 0;
         int until = whole - t0, from = 0;                // in rows of the run
         for (int done = 0; done <= run - 1 + (K - 1);) {
+            if (done > 0 && done % kStretch == 0)
+#pragma unroll
+                for (int m = 0; m <= K; ++m)
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) {
+                        float* sum = buf + (m * VE + e) * kThreads + threadIdx.x;
+                        *sum = done == kStretch ? acc[m][e] : *sum + acc[m][e];
+                        acc[m][e] = 0.f;
+                    }
             auto plain = [&](int d) { return __all(d + kBatch <= until && (d == 0 || d - (K - 1) >= from)); };
             if (plain(done)) {
                 typename G::Raw xr[kBatch], dr[kBatch];
@@ -503,7 +517,7 @@ __global__ __launch_bounds__(kThreads) void short_conv_bwd_kernel(
                         G::unpack(xr[i], win[K - 1 + i]);
                         G::unpack(dr[i], dsw[K - 1 + i]);
                     }
-                    more = done + kBatch <= run - 1 + (K - 1) && plain(done + kBatch);
+                    more = done + kBatch <= run - 1 + (K - 1) && (done + kBatch) % kStretch != 0 && plain(done + kBatch);
                     if (more)
                         fetch();
 #pragma unroll
@@ -587,6 +601,12 @@ __global__ __launch_bounds__(kThreads) void short_conv_bwd_kernel(
                 advance<K, VE>(dsw, 1);
             }
         }
+        if (run - 1 + (K - 1) >= kStretch)
+#pragma unroll
+            for (int m = 0; m <= K; ++m)
+#pragma unroll
+                for (int e = 0; e < VE; ++e)
+                    acc[m][e] += buf[(m * VE + e) * kThreads + threadIdx.x];
     }
     // the groups' sums, added in their order; a row of the partials is [C][K], then [C]
     const int lv = 1 << lv_bits, cols = lv * VE, base = me.chunk * cols;
@@ -782,12 +802,14 @@ template <typename T> hipError_t bwd(const ShortConvArgs& p, hipStream_t stream)
         constexpr int K = decltype(taps)::value, VE = lane_channels_bwd(sizeof(T), K), VH = lane_channels(sizeof(T), K);
         const Plan plan(p.channels, VE);
         const int nb = short_conv_bwd_blocks(p.total_tokens, p.channels, p.bf16, K);
+        const int run = bwd_run(p.total_tokens, plan);
+        const size_t sums = run - 1 + (K - 1) >= kStretch ? K + 1 : 1;
         hipError_t e = with_mode(p.channels < VE, p.silu, [&](auto mode) -> hipError_t {
             hipLaunchKernelGGL((short_conv_bwd_kernel<T, K, VE, decltype(mode)::mode>), dim3((unsigned)nb * plan.chunks),
-                               dim3(kThreads), kThreads * VE * sizeof(float), stream, (const T*)p.x, p.x_stride,
+                               dim3(kThreads), sums * kThreads * VE * sizeof(float), stream, (const T*)p.x, p.x_stride,
                                (const T*)p.w, (const T*)p.bias, (const T*)p.hist, p.cu_seqlens, (const T*)p.dy, p.silu,
                                p.dbias != nullptr, p.n_seqs, p.total_tokens, p.channels, plan.lv_bits, plan.chunks,
-                               bwd_run(p.total_tokens, plan), (T*)p.dx, p.ws);
+                               run, (T*)p.dx, p.ws);
             return hipGetLastError();
         });
         if (e != hipSuccess)
