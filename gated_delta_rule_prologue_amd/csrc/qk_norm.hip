@@ -29,6 +29,9 @@ namespace prism {
 namespace {
 
 constexpr int kThreads = 256;
+// Rows whose terms of a weight's gradient a lane adds up in turn, at most, before they join its sum of the stretches
+// before in LDS: so the rounding errors grow with 256 and a lane's 256ths of the rows, not with its rows.
+constexpr int kStretch = 256;
 // The elements of a row that a lane holds: NP pairs of vectors of VE elements.
 template <typename T, bool INTERLEAVED_, int VE_, int LANES_, int NP_> struct Shape {
     typedef T elem;
@@ -420,6 +423,23 @@ __global__ __launch_bounds__(kThreads) void qk_norm_bwd_kernel(RowArgs p, Side<t
     Angles<S> angles;
     if (p.rot)
         angles.load(p.freqs, at);
+    // the lane's own places in LDS: the sums of its stretches
+    auto join = [&](bool first) {
+#pragma unroll
+        for (int i = 0; i < S::NP; ++i)
+#pragma unroll
+            for (int e = 0; e < S::VE; ++e) {
+                float* to = buf + opaque(group * p.width) + e;       // no registers for its addresses
+                const int a = i * 2 * S::VE + e, b = a + S::VE;
+                if (at[i].a >= 0)
+                    to[at[i].a] = first ? acc[a] : to[at[i].a] + acc[a];
+                if (at[i].b >= 0)
+                    to[at[i].b] = first ? acc[b] : to[at[i].b] + acc[b];
+                acc[a] = acc[b] = 0.f;
+            }
+    };
+    const int every = kStretch / me.part;                    // tokens of a stretch, or parts of them
+    int done = 0;
     const int64_t units = p.tokens * me.parts;
     RawRow<S> raw, raw_d;
     raw.clear();
@@ -472,19 +492,13 @@ __global__ __launch_bounds__(kThreads) void qk_norm_bwd_kernel(RowArgs p, Side<t
             }
             store_row<S>(dx, at, v);
         }
+        if (part && ++done % every == 0)
+            join(done == every);
     }
     if (!part)
         return;
-    // the groups' sums, added in their order
-#pragma unroll
-    for (int i = 0; i < S::NP; ++i)
-#pragma unroll
-        for (int e = 0; e < S::VE; ++e) {
-            if (at[i].a >= 0)
-                buf[group * p.width + at[i].a + e] = acc[i * 2 * S::VE + e];
-            if (at[i].b >= 0)
-                buf[group * p.width + at[i].b + e] = acc[i * 2 * S::VE + S::VE + e];
-        }
+    // the groups' sums, added in their order; the lane has had a stretch if it has had its every-th unit
+    join((int64_t)(every - 1) * me.blocks * S::GROUPS + (int64_t)block * S::GROUPS + group >= units);
     __syncthreads();
     for (int c = threadIdx.x; c < p.width; c += kThreads) {
         float t = 0.f;
@@ -559,8 +573,8 @@ template <typename S> Side<typename S::elem> side_of(const QkNormArgs& p, int i,
         s.tile /= 2;
     if (s.tile < 1)
         s.tile = 1;
-    // backward: all heads of a token on the same angles, or fewer where that leaves SIMDs without a wavefront
-    for (s.part = s.heads;; s.part = (s.part + 1) / 2) {
+    // backward: all heads of a token on the same angles (those of a stretch), or fewer where that leaves SIMDs without a wavefront
+    for (s.part = s.heads < kStretch ? s.heads : kStretch;; s.part = (s.part + 1) / 2) {
         s.parts = (s.heads + s.part - 1) / s.part;
         if (s.part == 1 || p.tokens * s.parts * S::LANES >= 1024 * 64)
             break;
