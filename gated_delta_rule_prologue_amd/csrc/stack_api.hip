@@ -139,13 +139,18 @@ bool sample_dims_ok(const prism_sample_dims* d)
            stride_ok(d->rows, d->stride);
 }
 
+bool sample_fits(const prism_sample_dims* d)
+{
+    return d->vocab <= PRISM_MAX_SAMPLE_VOCAB && prism::sample_fits(d->rows);
+}
+
 }  // namespace
 
 extern "C" {
 
 size_t prism_conv_workspace_bytes(const prism_conv_dims* d)
 {
-    if (!conv_dims_ok(d))
+    if (!conv_dims_ok(d) || !conv_fits(d))
         return 0;
     const int nb = prism::short_conv_bwd_blocks(d->total_tokens, d->channels, d->dtype == PRISM_BF16, d->taps);
     return round256((size_t)nb * d->channels * (d->taps + 1) * sizeof(float));
@@ -209,14 +214,14 @@ prism_status prism_short_conv_bwd(const prism_conv_dims* d, const void* x, const
     if (!conv_dims_ok(d) || !act_ok(activation))
         return PRISM_EINVAL;
     if (!ptr_ok(w) || !opt_ok(bias) || !opt_ok(hist) || !ptr_ok(cu_seqlens) || !opt_ok(dy) || !opt_ok(dx) ||
-        !ptr_ok(dw) || !opt_ok(dbias) || !opt_ok(dhist) || !ptr_ok(workspace))
+        !ptr_ok(dw) || !opt_ok(dbias) || !opt_ok(dhist))
         return PRISM_EINVAL;
     if (d->total_tokens > 0 && (!elem_ok(x, d->dtype) || !dy || !dx))
         return PRISM_EINVAL;
     if (!conv_fits(d))
         return PRISM_EUNSUPPORTED;
     const size_t need = prism_conv_workspace_bytes(d);
-    if (workspace_bytes < need)
+    if (!ptr_ok(workspace) || workspace_bytes < need)
         return PRISM_EINVAL;
     const ConvSizes z(d);
     const int64_t C = d->channels;
@@ -235,7 +240,7 @@ prism_status prism_short_conv_bwd(const prism_conv_dims* d, const void* x, const
 
 size_t prism_qk_workspace_bytes(const prism_qk_dims* d)
 {
-    if (!qk_dims_ok(d))
+    if (!qk_dims_ok(d) || !qk_fits(d))
         return 0;
     return round256((size_t)prism::qk_norm_bwd_blocks(d->tokens) * (d->heads_k > 0 ? 2 : 1) * d->width * sizeof(float));
 }
@@ -296,7 +301,7 @@ prism_status prism_qk_norm_bwd(const prism_qk_dims* d, const void* q, const void
 
 size_t prism_sample_workspace_bytes(const prism_sample_dims* d)
 {
-    return sample_dims_ok(d) ? round256(prism::sample_workspace_bytes(d->rows, d->vocab)) : 0;
+    return sample_dims_ok(d) && sample_fits(d) ? round256(prism::sample_workspace_bytes(d->rows, d->vocab)) : 0;
 }
 
 prism_status prism_sample(const prism_sample_dims* d, const void* logits, const float* temperature,
@@ -310,7 +315,7 @@ prism_status prism_sample(const prism_sample_dims* d, const void* logits, const 
         return PRISM_EINVAL;
     if (d->rows > 0 && (!elem_ok(logits, d->dtype) || (!tokens && !probs) || (tokens && !u)))
         return PRISM_EINVAL;
-    if (d->vocab > PRISM_MAX_SAMPLE_VOCAB || !prism::sample_fits(d->rows))
+    if (!sample_fits(d))
         return PRISM_EUNSUPPORTED;
     const size_t need = prism_sample_workspace_bytes(d);
     if (need > 0 ? !ptr_ok(workspace) || workspace_bytes < need : !opt_ok(workspace))

@@ -627,7 +627,7 @@ typedef struct {
 } prism_conv_dims;
 
 /* Bytes of device workspace prism_short_conv_bwd needs (fp32 partial sums of the weights'
- * gradients, one set per workgroup).  0 for invalid dims. */
+ * gradients, one set per workgroup).  0 for dims that it refuses. */
 size_t prism_conv_workspace_bytes(const prism_conv_dims* d);
 
 /*
@@ -693,7 +693,7 @@ typedef struct {
     int64_t k_stride, k_head_stride;
 } prism_qk_dims;
 
-/* Bytes of device workspace prism_qk_norm_bwd needs.  0 for invalid dims. */
+/* Bytes of device workspace prism_qk_norm_bwd needs.  0 for dims that it refuses. */
 size_t prism_qk_workspace_bytes(const prism_qk_dims* d);
 
 /*
@@ -735,7 +735,7 @@ typedef struct {
     int64_t stride;        /* elements from a row of logits to the next, >= 0 */
 } prism_sample_dims;
 
-/* Bytes of device workspace prism_sample needs (0: the workspace may be NULL); 0 for invalid dims. */
+/* Bytes of device workspace prism_sample needs (0: the workspace may be NULL); 0 for dims that it refuses. */
 size_t prism_sample_workspace_bytes(const prism_sample_dims* d);
 
 /*
