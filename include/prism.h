@@ -763,7 +763,8 @@ size_t prism_sample_workspace_bytes(const prism_sample_dims* d);
  * Entries of -infinity and NaN are never kept; a row without any other gives the token -1 and
  * probabilities of zero.  Beside entries of +infinity no others are kept.  Weights are formed
  * in 64 bits and added exactly in steps of 2^-43 of the largest: the same call gives the same
- * token, whatever else runs.
+ * token, whatever else runs.  Each is off by half a step at most, so a choice is that of exact sums
+ * but where it is nearer to another than vocab * 2^-43 of the largest weight.
  */
 prism_status prism_sample(const prism_sample_dims* d, const void* logits, const float* temperature,
                           const int32_t* top_k, const float* top_p, const float* min_p, const float* u,
