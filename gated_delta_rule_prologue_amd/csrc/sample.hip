@@ -1489,7 +1489,7 @@ struct Cut {
 // units idle; into chunks of 16,384 where that takes no second round of workgroups.  us, fp32, whole rows, chunks of
 // 16,384, of 32,768: 1 of 128,000 56, 22, 27; 64 of 128,000 76, 62, 49; 64 of 50,001 38 and 35, 96 of them 38 and 41;
 // 128 of 128,000 79 and 100; 16 of 33,000 22 and 25; 8 of 32,000, which fit the registers, 22 and 32 (later steps took
-// as much from both sides).
+// as much from both sides).  Rows longer than 128,000 go by the same limit, unmeasured against whole rows.
 Cut cut_of(int64_t rows, int vocab)
 {
     if (rows > 80 || vocab <= 40 * 1024)

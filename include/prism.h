@@ -684,8 +684,8 @@ typedef enum { PRISM_QK_NONE = 0, PRISM_QK_RMS = 1, PRISM_QK_L2 = 2 } prism_qk_k
 typedef enum { PRISM_ROT_HALF = 0, PRISM_ROT_INTERLEAVED = 1 } prism_rot_layout;
 
 typedef struct {
-    int64_t tokens;                        /* T >= 0 */
-    int32_t heads_q, heads_k;              /* >= 1; heads_k 0: no k */
+    int64_t tokens;                        /* T >= 0, less than 2^23 */
+    int32_t heads_q, heads_k;              /* 1..65535; heads_k 0: no k */
     int32_t width;                         /* elements per head, 1..512 */
     int32_t rot;                           /* elements that turn, even, 0..width */
     int32_t dtype;                         /* prism_dtype of every float tensor but freqs and the fp32 gradients */
@@ -729,7 +729,7 @@ prism_status prism_qk_norm_bwd(const prism_qk_dims* d, const void* q, const void
 #define PRISM_MAX_SAMPLE_VOCAB (1 << 20)
 
 typedef struct {
-    int64_t rows;          /* >= 0 */
+    int64_t rows;          /* >= 0, less than 2^22 */
     int32_t vocab;         /* 1..PRISM_MAX_SAMPLE_VOCAB */
     int32_t dtype;         /* prism_dtype of the logits */
     int64_t stride;        /* elements from a row of logits to the next, >= 0 */
